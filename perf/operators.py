@@ -147,6 +147,10 @@ def prepare(case, seed):
         T, E, k = case["T"], case["E"], case["k"]
         # the selection that the forward handed on: the k largest logits of each token
         st["idx"] = torch.sort(st["logits"], dim=1, descending=True, stable=True).indices[:, :k].to(torch.int32).contiguous()
+        s = torch.sigmoid(st["logits"].double()) if case["score"] == "sigmoid" else torch.softmax(st["logits"].double(), 1)
+        w = s.gather(1, st["idx"].long())
+        w = w / w.sum(dim=1, keepdim=True) if case["renorm"] else w
+        st["w"] = (w * case["scale"]).float()
         st["dw"] = torch.randn((T, k), generator=gen, device="cuda") * 0.01
         st["dlosses"] = torch.tensor([0.01, 0.001], device="cuda")
         st["seq"] = torch.from_numpy(_seq_offsets(T, case["seqs"], seed)).to("cuda")
@@ -318,7 +322,7 @@ def run(st):
             return moe.route_select(dims, st["opts"], st["logits"], balance_bias=st["bias"])
         if op == "select_grad":
             losses, load = moe.balance_loss(dims, st["opts"], st["logits"], st["idx"], seq_offsets=st["seq"])
-            dl = moe.route_select_backward(dims, st["opts"], st["logits"], st["idx"], st["dw"],
+            dl = moe.route_select_backward(dims, st["opts"], st["logits"], st["idx"], st["w"], st["dw"],
                                            dlosses=st["dlosses"], load=load, seq_offsets=st["seq"])
             return losses, load, dl
         if op == "gate_grad":
@@ -343,9 +347,8 @@ def work(case):
         E, k = case["E"], case["k"]
         return {"bytes": 4 * T * E + 8 * T * k + (4 * E if case["bias"] else 0), "flops": 6 * T * E + 2 * T * E * k}
     if op == "select_grad":
-        # the gradient needs the whole batch's loads, so the logits are read for the losses and again for it
         E, k = case["E"], case["k"]
-        return {"bytes": 8 * T * E + 8 * T * k + 4 * case["seqs"] * E, "flops": 24 * T * E}
+        return {"bytes": 8 * T * E + 12 * T * k + 4 * case["seqs"] * E, "flops": 24 * T * E}
     if op == "gate_grad":
         d, E = case["d"], case["E"]
         return {"bytes": 4 * T * E + 6 * T * d + 2 * E * d + 4 * E * d + 4 * E, "flops": 4 * T * E * d}
