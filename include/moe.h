@@ -407,6 +407,138 @@ int moe_layer_backward_ex(const moe_dims_t* dims, const void* x, const void* wg,
                           void* dw3, void* dw2, float* dlogits, float* dtopk_w, void* ws, size_t ws_bytes,
                           void* stream);
 
+/* ---- scored router: selection from scores, its losses and gradients ----
+ * The router of layers whose experts are chosen by softmax or sigmoid scores
+ * with a balance bias, optionally inside groups of experts. For the logits l
+ * of one token (fp32, as moe_route computes them):
+ *   s_e = sigmoid(l_e), or exp(l_e) / sum_i exp(l_i) over all E experts;
+ *   c_e = s_e + balance_bias[e]     the key: chooses, does not weigh;
+ *   an expert is out of the token's choice when its logit or its bias is -inf
+ *   or NaN (+inf counts as the largest finite logit); NaN in such places
+ *   reaches no output;
+ *   with groups > 1, the E / groups consecutive experts of a group have the
+ *   group key max c, or the sum of their two largest c (the one, if only one
+ *   is in the choice); the topk_groups groups with the largest keys are kept
+ *   (ties: lower group; a group with no expert in the choice comes last), and
+ *   the other groups' experts are out of the choice;
+ *   the k experts with the largest c are chosen, slot by slot (ties: larger
+ *   logit, then lower expert). Keys are compared as doubles;
+ *   topk_w[j] = scale * s_j, with renormalise divided by the sum of the chosen s.
+ * Where fewer than k experts are in the choice, the slots left take the
+ * experts out of it in ascending order with weight 0 (so every index is valid
+ * for moe_permute); a row with none gets experts 0 .. k-1 and weights 0.
+ * Limits: as moe_dims_t (only T, E and k are used), groups <= 64 dividing E,
+ * topk_groups * E / groups >= k, scale finite, else MOE_ERR_INVALID. */
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0,
+  MOE_SCORE_SIGMOID = 1
+} moe_score_t;
+typedef enum {
+  MOE_GROUP_MAX = 0,  /* group key: its largest key */
+  MOE_GROUP_TOP2 = 1  /* group key: the sum of its two largest keys */
+} moe_group_rule_t;
+typedef struct {
+  int32_t score;       /* moe_score_t */
+  int32_t groups;      /* groups of consecutive experts; 1 = no groups */
+  int32_t topk_groups; /* groups kept per token */
+  int32_t group_rule;  /* moe_group_rule_t */
+  int32_t renormalise; /* 1: weights divided by their sum */
+  float scale;         /* factor of the weights */
+} moe_route_opts_t;
+
+/* Selection from logits. logits [T][E] fp32; balance_bias [E] fp32 or NULL;
+ * outputs topk_idx [T][k] int32, topk_w [T][k] fp32. `opts` is a HOST pointer. */
+int moe_route_select(const moe_dims_t* dims, const moe_route_opts_t* opts, const float* logits,
+                     const float* balance_bias, int32_t* topk_idx, float* topk_w, void* stream);
+
+/* Gate GEMM + bias (moe_route's logits, bit for bit), then the selection.
+ * x [T][d], wg [E][d], bias [E] fp32 or NULL (added to the logits), logits
+ * [T][E] fp32 output (required: the backward reads it). d % 8 == 0. */
+int moe_route_scored(const moe_dims_t* dims, const moe_route_opts_t* opts, const void* x, const void* wg,
+                     const float* bias, const float* balance_bias, float* logits, int32_t* topk_idx, float* topk_w,
+                     void* stream);
+
+/* Balance losses over n_seq packed sequences: rows seq_offsets[s] ..
+ * seq_offsets[s+1]-1 (device int32 [n_seq+1], not decreasing, clamped to
+ * [0, T]; NULL with n_seq = 1: all T rows). Rows outside every sequence count
+ * in neither loss. With n_s rows, f[s][e] = how often sequence s chose expert
+ * e, shares q = s_e / sum_i s_i of each row and the sequences that have rows:
+ *   losses[0] = mean over them of E / (k n_s^2) sum_e f[s][e] sum_t q[t][e]
+ *   losses[1] = mean over their rows of (log sum_e exp l[t][e])^2
+ * (a row with every logit -inf adds nothing; no rows: both 0). Only
+ * opts->score is used. topk_idx [T][k] (entries outside [0, E) are not
+ * counted). Outputs losses [2] fp32, load [n_seq][E] int32 = f (the loads a
+ * caller adjusts balance_bias by). Fixed summation order. ws: at least
+ * moe_balance_workspace_bytes (0 for invalid arguments), 256-byte aligned.
+ * n_seq <= 65535 (MOE_ERR_UNSUPPORTED beyond). */
+size_t moe_balance_workspace_bytes(const moe_dims_t* dims, int32_t n_seq);
+int moe_balance_loss(const moe_dims_t* dims, const moe_route_opts_t* opts, const float* logits,
+                     const int32_t* topk_idx, const int32_t* seq_offsets, int32_t n_seq, float* losses, int32_t* load,
+                     void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of selection and losses with respect to the logits; the choice
+ * itself is piecewise constant. dlogits [T][E] fp32 = the gradient of
+ *   sum_t sum_j dtopk_w[t][j] topk_w[t][j] + dlosses[0] losses[0] + dlosses[1] losses[1]
+ * (the loads f are constants), every element written. dtopk_w [T][k] NULL: without the first term (topk_idx and
+ * topk_w may then be NULL too); dlosses (device fp32 [2]) NULL: without the
+ * others (load, seq_offsets and n_seq are then not looked at), else load
+ * [n_seq][E] as moe_balance_loss returned it for the same seq_offsets.
+ * topk_idx and topk_w as moe_route_select returned them for these logits and
+ * options: a slot of weight 0 passes no gradient, an entry outside [0, E) is
+ * skipped, repeated entries add up. Experts whose logit is -inf or NaN get 0. */
+int moe_route_select_backward(const moe_dims_t* dims, const moe_route_opts_t* opts, const float* logits,
+                              const int32_t* topk_idx, const float* topk_w, const float* dtopk_w,
+                              const float* dlosses, const int32_t* load, const int32_t* seq_offsets, int32_t n_seq,
+                              float* dlogits, void* stream);
+
+/* Gradients of the gate GEMM for a dense logit gradient:
+ *   dx = dx_in + dlogits Wg (bf16, one rounding), dwg = dlogits^T x, dbias = column sums (fp32)
+ * x [T][d], wg [E][d], dx_in [T][d] or NULL, dx [T][d] bf16 (may be dx_in);
+ * dlogits [T][E], dwg [E][d], dbias [E] fp32. bf16 only, d % 8 == 0, T <=
+ * 8388480, d <= 2^24 (MOE_ERR_UNSUPPORTED otherwise). T = 0 writes zero dwg and
+ * dbias. dwg's products are exact and its sums fp32; fixed summation order.
+ * ws: at least moe_gate_backward_workspace_bytes(dims), 256-byte aligned. */
+size_t moe_gate_backward_workspace_bytes(const moe_dims_t* dims);
+int moe_gate_backward(const moe_dims_t* dims, const void* x, const void* wg, const float* dlogits, const void* dx_in,
+                      void* dx, float* dwg, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* The experts' part of moe_layer_backward_ex, for routers whose gradient is
+ * taken elsewhere (moe_route_select_backward, moe_gate_backward): the same
+ * arguments without the gate's; dx [T][d] bf16 is the experts' part alone and
+ * dtopk_w [T][k] fp32 (required) the gradient of the weights. Expert weight
+ * gradients and dtopk_w are bitwise moe_layer_backward_ex's. Workspace, limits
+ * and errors as there. */
+int moe_experts_backward(const moe_dims_t* dims, const void* x, const void* w1, const void* w3, const void* w2,
+                         const int32_t* topk_idx, const float* topk_w, const int32_t* counts, const int32_t* offsets,
+                         const int32_t* perm, const int32_t* inv_perm, const void* dout, const void* gu,
+                         int wgrad_dtype, void* dx, void* dw1, void* dw3, void* dw2, float* dtopk_w, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* ---- dropout beside the combine ----
+ * The combine with dropout on the layer's output, added to a residual:
+ *   out[t][c] = residual[t][c] + keep(t, c) S sum_j topk_w[t][j] y_sorted[inv_perm[t*k+j]][c]
+ * keep is drawn from a counter-based generator and never stored: element
+ * i = t*d + c takes 16-bit number i % 8 (low half of word 0, its high half, low
+ * half of word 1, ..) of Philox4x32 with ten rounds, key = seed (low word
+ * first), counter = {i / 8 (64 bits), offset (64 bits)}, and is kept when it is
+ * at least thr = round(65536 p), ties to even; S = 65536 / (65536 - thr). p = 0
+ * keeps all, p = 1 drops all (out = residual). p outside [0, 1] or NaN:
+ * MOE_ERR_INVALID. rng: DEVICE pointer to {seed, offset}, 8-byte aligned, read
+ * when the kernel runs: a captured graph draws anew when its owner updates it
+ * between replays. Two calls with the same seed and offset draw the same.
+ * A dropped element is the residual alone, whatever its value.
+ *   moe_combine_dropout: arguments as moe_combine, and residual [T][d] (the
+ *     dtype; NULL = 0; out may be residual). Sum, scaling and residual in fp32,
+ *     one rounding.
+ *   moe_dropout_backward: dy = keep S dout [T][d], the gradient of the combined
+ *     sum, which moe_experts_backward or moe_layer_backward takes as its dout
+ *     (residual's gradient is dout itself); dy may be dout.
+ * d % 8 == 0 (MOE_ERR_UNSUPPORTED otherwise); bf16 and fp32. */
+int moe_combine_dropout(const moe_dims_t* dims, double p, const uint64_t* rng, const void* y_sorted,
+                        const int32_t* inv_perm, const float* topk_w, const void* residual, void* out, void* stream);
+int moe_dropout_backward(const moe_dims_t* dims, double p, const uint64_t* rng, const void* dout, void* dy,
+                         void* stream);
+
 /* ---- stage timing (instrumentation; process-wide, not thread-safe) ----
  * While enabled, every kernel the library launches is bracketed by HIP events
  * recorded on the stream it is launched on. Stages: */
@@ -433,7 +565,13 @@ enum {
   MOE_STAGE_BWD_WG13 = 19,    /* backward: WGrad of W1 and W3 */
   MOE_STAGE_BWD_GATE = 20,    /* backward: gate weight and bias gradients */
   MOE_STAGE_FFN_FUSED = 21,   /* FC1 + FC2 + combine in one launch (moe_layer_forward_fused) */
-  MOE_NUM_STAGES = 22
+  MOE_STAGE_SELECT = 22,       /* scored selection */
+  MOE_STAGE_BALANCE = 23,      /* balance losses */
+  MOE_STAGE_SELECT_BWD = 24,   /* scored selection's and losses' backward */
+  MOE_STAGE_GATE_BWD = 25,     /* dense gate gradients */
+  MOE_STAGE_COMBINE_DROP = 26, /* combine with dropout */
+  MOE_STAGE_DROP_BWD = 27,     /* dropout backward */
+  MOE_NUM_STAGES = 28
 };
 /* Start recording; `capacity` = launches per stage to keep (host memory only);
  * `stage_mask` = bit s set records stage s (0 = every stage). Discards

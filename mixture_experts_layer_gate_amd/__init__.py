@@ -13,4 +13,6 @@ from .api import (  # noqa: F401
     probe_hbm_read_gbps, probe_mfma_tflops, workspace_bytes_shared, layer_forward_shared,
     backward_workspace_bytes, layer_backward, layer_forward_train, ffn_block_rows, gate_on_matrix_cores, pack_weights, pack_weights_transposed,
     fused_status, plan_layout, read_plan, read_plan_multi_block, layer_forward_noalloc, NOALLOC_SCRATCH_BYTES,
+    RouteOptions, route_select, route_scored, balance_loss, balance_workspace_bytes, route_select_backward,
+    gate_backward, gate_backward_workspace_bytes, experts_backward, combine_dropout, dropout_backward,
 )

@@ -19,7 +19,8 @@ _LIB_NAME = "libmoe_amd.so"
 
 STAGES = ["gate", "topk", "hist", "scan", "scatter", "plan", "fc1", "fc2", "combine", "dispatch",
           "bwd_wt", "bwd_fc1", "bwd_dh", "bwd_swiglu", "bwd_route", "bwd_dx", "bwd_dxsum", "bwd_act_t",
-          "bwd_wg2", "bwd_wg13", "bwd_gate", "ffn_fused"]
+          "bwd_wg2", "bwd_wg13", "bwd_gate", "ffn_fused", "select", "balance", "select_grad", "gate_grad",
+          "combine_drop", "drop_grad"]
 MOE_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 # Every symbol include/moe.h declares.
@@ -30,7 +31,10 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_workspace_bytes", "moe_route
            "moe_layer_backward", "moe_layer_forward_fused", "moe_ffn_block_rows", "moe_gate_on_matrix_cores", "moe_pack_weights",
            "moe_layer_forward_packed", "moe_fused_status", "moe_layer_plan_layout", "moe_pack_weights_transposed",
            "moe_layer_forward_noalloc", "moe_layer_forward_fused_packed", "moe_layer_forward_train",
-           "moe_layer_backward_saved", "moe_layer_backward_ex"]
+           "moe_layer_backward_saved", "moe_layer_backward_ex", "moe_route_select", "moe_route_scored",
+           "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_select_backward",
+           "moe_gate_backward_workspace_bytes", "moe_gate_backward", "moe_experts_backward", "moe_combine_dropout",
+           "moe_dropout_backward"]
 
 # Bytes of the static scratch moe_layer_forward_noalloc uses (MOE_NOALLOC_SCRATCH_BYTES in include/moe.h).
 NOALLOC_SCRATCH_BYTES = 128 << 20
@@ -60,6 +64,36 @@ class Dims:
         return _Dims(self.T, self.d, self.f, self.E, self.k, MOE_DTYPE.get(self.dtype, -1))
 
 
+class _RouteOpts(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_rule", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+@dataclass(frozen=True)
+class RouteOptions:
+    """How route_select chooses experts from gate logits: scores by "softmax" (over
+    all experts) or "sigmoid"; with groups > 1, only the topk_groups groups of
+    consecutive experts with the largest group key are chosen from, the key being
+    the group's largest score plus balance bias ("max") or the sum of its two
+    largest ("top2"); weights divided by their sum when renormalise, times scale."""
+    score: str = "softmax"
+    groups: int = 1
+    topk_groups: int = 1
+    group_rule: str = "max"
+    renormalise: bool = True
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.score not in ("softmax", "sigmoid"):
+            raise ValueError(f"score must be 'softmax' or 'sigmoid', not {self.score!r}")
+        if self.group_rule not in ("max", "top2"):
+            raise ValueError(f"group_rule must be 'max' or 'top2', not {self.group_rule!r}")
+
+    def c(self) -> _RouteOpts:
+        return _RouteOpts(int(self.score == "sigmoid"), self.groups, self.topk_groups, int(self.group_rule == "top2"),
+                          int(bool(self.renormalise)), self.scale)
+
+
 def library_path() -> str:
     return os.environ.get("MOE_AMD_LIB", os.path.join(_PKG, _LIB_NAME))
 
@@ -68,6 +102,7 @@ _lib = None
 _P = ctypes.c_void_p
 _S = ctypes.c_size_t
 _DP = ctypes.POINTER(_Dims)
+_OP = ctypes.POINTER(_RouteOpts)
 
 
 def load_library():
@@ -111,6 +146,18 @@ def load_library():
     lib.moe_layer_forward_train.argtypes = [_DP] + [_P] * 16 + [_S, _P]
     lib.moe_layer_backward_saved.argtypes = [_DP] + [_P] * 22 + [_S, _P]
     lib.moe_layer_backward_ex.argtypes = [_DP] + [_P] * 13 + [ctypes.c_int] + [_P] * 9 + [_S, _P]
+    lib.moe_route_select.argtypes = [_DP, _OP, _P, _P, _P, _P, _P]
+    lib.moe_route_scored.argtypes = [_DP, _OP] + [_P] * 8
+    lib.moe_balance_workspace_bytes.restype = _S
+    lib.moe_balance_workspace_bytes.argtypes = [_DP, ctypes.c_int32]
+    lib.moe_balance_loss.argtypes = [_DP, _OP, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _S, _P]
+    lib.moe_route_select_backward.argtypes = [_DP, _OP] + [_P] * 7 + [ctypes.c_int32, _P, _P]
+    lib.moe_gate_backward_workspace_bytes.restype = _S
+    lib.moe_gate_backward_workspace_bytes.argtypes = [_DP]
+    lib.moe_gate_backward.argtypes = [_DP] + [_P] * 8 + [_S, _P]
+    lib.moe_experts_backward.argtypes = [_DP] + [_P] * 12 + [ctypes.c_int] + [_P] * 6 + [_S, _P]
+    lib.moe_combine_dropout.argtypes = [_DP, ctypes.c_double] + [_P] * 7
+    lib.moe_dropout_backward.argtypes = [_DP, ctypes.c_double] + [_P] * 4
     lib.moe_timing_enable.argtypes = [ctypes.c_int, ctypes.c_uint]
     lib.moe_timing_read.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int)]
     lib.moe_probe_cus.restype = ctypes.c_int
@@ -120,7 +167,9 @@ def load_library():
                "moe_layer_forward_shared", "moe_layer_backward", "moe_layer_forward_fused", "moe_fused_status",
                "moe_layer_plan_layout", "moe_pack_weights", "moe_pack_weights_transposed",
                "moe_layer_forward_packed", "moe_layer_forward_noalloc", "moe_layer_forward_fused_packed",
-               "moe_timing_enable", "moe_timing_disable", "moe_timing_read", "moe_probe_hbm_read", "moe_probe_mfma"):
+               "moe_timing_enable", "moe_timing_disable", "moe_timing_read", "moe_probe_hbm_read", "moe_probe_mfma",
+               "moe_route_select", "moe_route_scored", "moe_balance_loss", "moe_route_select_backward",
+               "moe_gate_backward", "moe_experts_backward", "moe_combine_dropout", "moe_dropout_backward"):
         getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -510,6 +559,259 @@ def layer_backward(dims: Dims, x, wg, w1, w3, w2, routing: dict, dout, ws=None, 
     else:
         _check("moe_layer_backward_saved", lib.moe_layer_backward_saved(*head, _ptr(gu), *tail))
     return g
+
+
+# ---- scored router, its losses and gradients, dropout beside the combine ----
+class _on:
+    """Scope of a call on its tensors' device: that device is made current, and with a
+    stream of the caller's that stream too, so that outputs and workspaces made here
+    belong to the stream the call runs on."""
+
+    def __init__(self, name: str, dev: torch.device, stream, *others):
+        if dev.type != "cuda":
+            raise ValueError(f"{name} must be a GPU tensor")
+        for n, t in others:
+            if t is not None and t.device != dev:
+                raise ValueError(f"{n} is on {t.device}, {name} on {dev}")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, {name} on {dev}")
+        self.scope = None
+        if stream is not None:
+            self.scope = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != dev.index:
+            self.scope = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.scope is not None:
+            self.scope.__enter__()
+
+    def __exit__(self, *exc):
+        if self.scope is not None:
+            self.scope.__exit__(*exc)
+
+
+def _out(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, dev):
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, dtype, shape)
+    return t
+
+
+def _scratch(ws: Optional[torch.Tensor], nbytes: int, dev):
+    """The caller's workspace, or a new one of nbytes. A tensor made here may be freed
+    when the call returns: torch's allocator hands it out again in stream order."""
+    if ws is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the inputs' device")
+    return ws
+
+
+def route_select(dims: Dims, opts: RouteOptions, logits, balance_bias=None, topk_idx=None, topk_w=None, stream=None):
+    """Experts chosen from gate logits [T][E] (fp32) by their scores. balance_bias [E]
+    (fp32) is added to the scores for the choice only; an expert whose logit or bias is
+    -inf (or NaN) is out of the choice. Returns (topk_idx [T][k] int32, topk_w [T][k]
+    fp32); slots left over when fewer than k experts are in the choice hold the other
+    experts in ascending order with weight 0."""
+    lib = load_library()
+    dev = logits.device
+    with _on("logits", dev, stream, ("balance_bias", balance_bias), ("topk_idx", topk_idx), ("topk_w", topk_w)):
+        _need(logits, "logits", torch.float32, (dims.T, dims.E))
+        if balance_bias is not None:
+            _need(balance_bias, "balance_bias", torch.float32, (dims.E,))
+        idx = _out(topk_idx, "topk_idx", torch.int32, (dims.T, dims.k), dev)
+        w = _out(topk_w, "topk_w", torch.float32, (dims.T, dims.k), dev)
+        _check("moe_route_select", lib.moe_route_select(
+            ctypes.byref(dims.c()), ctypes.byref(opts.c()), _ptr(logits), _ptr(balance_bias), _ptr(idx), _ptr(w),
+            _stream(None)))
+    return idx, w
+
+
+def route_scored(dims: Dims, opts: RouteOptions, x, wg, bias=None, balance_bias=None, logits=None, topk_idx=None,
+                 topk_w=None, stream=None):
+    """Gate logits (those of route, bit for bit) and the selection of route_select.
+    Returns (logits, topk_idx, topk_w)."""
+    lib = load_library()
+    dev = x.device
+    with _on("x", dev, stream, ("wg", wg), ("bias", bias), ("balance_bias", balance_bias), ("logits", logits),
+             ("topk_idx", topk_idx), ("topk_w", topk_w)):
+        _need(x, "x", dims.dtype, (dims.T, dims.d))
+        _need(wg, "wg", dims.dtype, (dims.E, dims.d))
+        for name, b in (("bias", bias), ("balance_bias", balance_bias)):
+            if b is not None:
+                _need(b, name, torch.float32, (dims.E,))
+        lg = _out(logits, "logits", torch.float32, (dims.T, dims.E), dev)
+        idx = _out(topk_idx, "topk_idx", torch.int32, (dims.T, dims.k), dev)
+        w = _out(topk_w, "topk_w", torch.float32, (dims.T, dims.k), dev)
+        _check("moe_route_scored", lib.moe_route_scored(
+            ctypes.byref(dims.c()), ctypes.byref(opts.c()), _ptr(x), _ptr(wg), _ptr(bias), _ptr(balance_bias),
+            _ptr(lg), _ptr(idx), _ptr(w), _stream(None)))
+    return lg, idx, w
+
+
+def _seqs(seq_offsets):
+    if seq_offsets is None:
+        return 1
+    if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
+        raise ValueError("seq_offsets must be a vector of at least two offsets")
+    _need(seq_offsets, "seq_offsets", torch.int32, tuple(seq_offsets.shape))
+    return seq_offsets.numel() - 1
+
+
+def balance_workspace_bytes(dims: Dims, n_seq: int = 1) -> int:
+    return int(load_library().moe_balance_workspace_bytes(ctypes.byref(dims.c()), n_seq))
+
+
+def balance_loss(dims: Dims, opts: RouteOptions, logits, topk_idx, seq_offsets=None, losses=None, load=None, ws=None,
+                 stream=None):
+    """Balance losses of a selection over packed sequences (seq_offsets [S+1] int32, None
+    for one sequence of all rows). Returns (losses [2] fp32: the balance loss and the mean
+    squared log-sum-exp of the logits; load [S][E] int32: how often each sequence chose
+    each expert)."""
+    lib = load_library()
+    dev = logits.device
+    with _on("logits", dev, stream, ("topk_idx", topk_idx), ("seq_offsets", seq_offsets), ("losses", losses), ("load", load)):
+        _need(logits, "logits", torch.float32, (dims.T, dims.E))
+        _need(topk_idx, "topk_idx", torch.int32, (dims.T, dims.k))
+        n_seq = _seqs(seq_offsets)
+        lo = _out(losses, "losses", torch.float32, (2,), dev)
+        ld = _out(load, "load", torch.int32, (n_seq, dims.E), dev)
+        w = _scratch(ws, balance_workspace_bytes(dims, n_seq), dev)
+        _check("moe_balance_loss", lib.moe_balance_loss(
+            ctypes.byref(dims.c()), ctypes.byref(opts.c()), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), n_seq,
+            _ptr(lo), _ptr(ld), _ptr(w), w.numel() * w.element_size(), _stream(None)))
+    return lo, ld
+
+
+def route_select_backward(dims: Dims, opts: RouteOptions, logits, topk_idx, topk_w, dtopk_w, dlosses=None, load=None,
+                          seq_offsets=None, dlogits=None, stream=None):
+    """Gradient with respect to the logits of route_select's weights (upstream gradient
+    dtopk_w [T][k], None for none) and of balance_loss (upstream gradients dlosses [2],
+    None for none; load and seq_offsets as balance_loss had them). Returns dlogits [T][E]."""
+    lib = load_library()
+    dev = logits.device
+    with _on("logits", dev, stream, ("topk_idx", topk_idx), ("topk_w", topk_w), ("dtopk_w", dtopk_w), ("dlosses", dlosses),
+             ("load", load), ("seq_offsets", seq_offsets), ("dlogits", dlogits)):
+        _need(logits, "logits", torch.float32, (dims.T, dims.E))
+        for name, t, dt in (("topk_idx", topk_idx, torch.int32), ("topk_w", topk_w, torch.float32),
+                            ("dtopk_w", dtopk_w, torch.float32)):
+            if t is not None:
+                _need(t, name, dt, (dims.T, dims.k))
+        n_seq = 1
+        if dlosses is not None:
+            n_seq = _seqs(seq_offsets)
+            _need(dlosses, "dlosses", torch.float32, (2,))
+            if load is None:
+                raise ValueError("dlosses needs load, as balance_loss returned it")
+            _need(load, "load", torch.int32, (n_seq, dims.E))
+        dl = _out(dlogits, "dlogits", torch.float32, (dims.T, dims.E), dev)
+        _check("moe_route_select_backward", lib.moe_route_select_backward(
+            ctypes.byref(dims.c()), ctypes.byref(opts.c()), _ptr(logits), _ptr(topk_idx), _ptr(topk_w),
+            _ptr(dtopk_w), _ptr(dlosses), _ptr(load), _ptr(seq_offsets), n_seq, _ptr(dl), _stream(None)))
+    return dl
+
+
+def gate_backward_workspace_bytes(dims: Dims) -> int:
+    return int(load_library().moe_gate_backward_workspace_bytes(ctypes.byref(dims.c())))
+
+
+def gate_backward(dims: Dims, x, wg, dlogits, dx_in=None, dx=None, dwg=None, dbias=None, ws=None, stream=None):
+    """Gradients of the gate GEMM for a dense dlogits [T][E] (fp32): dx [T][d] = dx_in +
+    dlogits wg (bf16; dx may be dx_in), dwg [E][d] and dbias [E] (fp32). bf16 layers.
+    Returns (dx, dwg, dbias)."""
+    lib = load_library()
+    dev = x.device
+    with _on("x", dev, stream, ("wg", wg), ("dlogits", dlogits), ("dx_in", dx_in), ("dx", dx), ("dwg", dwg),
+             ("dbias", dbias)):
+        _need(x, "x", dims.dtype, (dims.T, dims.d))
+        _need(wg, "wg", dims.dtype, (dims.E, dims.d))
+        _need(dlogits, "dlogits", torch.float32, (dims.T, dims.E))
+        if dx_in is not None:
+            _need(dx_in, "dx_in", dims.dtype, (dims.T, dims.d))
+        ox = _out(dx, "dx", dims.dtype, (dims.T, dims.d), dev)
+        ow = _out(dwg, "dwg", torch.float32, (dims.E, dims.d), dev)
+        ob = _out(dbias, "dbias", torch.float32, (dims.E,), dev)
+        w = _scratch(ws, gate_backward_workspace_bytes(dims), dev)
+        _check("moe_gate_backward", lib.moe_gate_backward(
+            ctypes.byref(dims.c()), _ptr(x), _ptr(wg), _ptr(dlogits), _ptr(dx_in), _ptr(ox), _ptr(ow), _ptr(ob),
+            _ptr(w), w.numel() * w.element_size(), _stream(None)))
+    return ox, ow, ob
+
+
+def experts_backward(dims: Dims, x, w1, w3, w2, routing: dict, dout, ws=None, stream=None, grads=None, gu=None,
+                     wgrad_dtype=torch.float32):
+    """The experts' part of layer_backward, for a router whose gradient is taken by
+    route_select_backward and gate_backward: routing and options as there. Returns a dict
+    with dx (the experts' part), dw1, dw3, dw2 and dtopk_w [T][k]."""
+    lib = load_library()
+    dev = x.device
+    g = dict(grads or {})
+    with _on("x", dev, stream, ("w1", w1), ("w3", w3), ("w2", w2), ("dout", dout), ("gu", gu), *routing.items(), *g.items()):
+        _need(x, "x", dims.dtype, (dims.T, dims.d))
+        _need(dout, "dout", dims.dtype, (dims.T, dims.d))
+        for name, w, shp in (("w1", w1, (dims.E, dims.f, dims.d)), ("w3", w3, (dims.E, dims.f, dims.d)),
+                             ("w2", w2, (dims.E, dims.d, dims.f))):
+            _need(w, name, dims.dtype, shp)
+        n = dims.T * dims.k
+        for name, dt, shp in (("topk_idx", torch.int32, (dims.T, dims.k)),
+                              ("topk_w", torch.float32, (dims.T, dims.k)), ("counts", torch.int32, (dims.E,)),
+                              ("offsets", torch.int32, (dims.E + 1,)), ("perm", torch.int32, (n,)),
+                              ("inv_perm", torch.int32, (n,))):
+            _need(routing[name], name, dt, shp)
+        if wgrad_dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("wgrad_dtype must be torch.float32 or torch.bfloat16")
+        if gu is not None:
+            _need(gu, "gu", dims.dtype, (n, 2 * dims.f))
+        for name, shp, dt in (("dx", (dims.T, dims.d), dims.dtype), ("dw1", (dims.E, dims.f, dims.d), wgrad_dtype),
+                              ("dw3", (dims.E, dims.f, dims.d), wgrad_dtype),
+                              ("dw2", (dims.E, dims.d, dims.f), wgrad_dtype),
+                              ("dtopk_w", (dims.T, dims.k), torch.float32)):
+            g[name] = _out(g.get(name), name, dt, shp, dev)
+        w = _scratch(ws, backward_workspace_bytes(dims), dev)
+        r = routing
+        _check("moe_experts_backward", lib.moe_experts_backward(
+            ctypes.byref(dims.c()), _ptr(x), _ptr(w1), _ptr(w3), _ptr(w2), _ptr(r["topk_idx"]), _ptr(r["topk_w"]),
+            _ptr(r["counts"]), _ptr(r["offsets"]), _ptr(r["perm"]), _ptr(r["inv_perm"]), _ptr(dout), _ptr(gu),
+            MOE_DTYPE[wgrad_dtype], _ptr(g["dx"]), _ptr(g["dw1"]), _ptr(g["dw3"]), _ptr(g["dw2"]),
+            _ptr(g["dtopk_w"]), _ptr(w), w.numel() * w.element_size(), _stream(None)))
+    return g
+
+
+def combine_dropout(dims: Dims, p: float, rng, y_sorted, inv_perm, topk_w, residual=None, out=None, stream=None):
+    """combine with dropout of probability p on the combined rows and an optional residual
+    [T][d] added: residual + keep / (1 - p) * sum. rng: int64 tensor [2] on the GPU, seed
+    and offset; the same pair draws the same decisions (dropout_backward takes it again).
+    out may be residual. Returns out [T][d]."""
+    lib = load_library()
+    dev = y_sorted.device
+    with _on("y_sorted", dev, stream, ("rng", rng), ("inv_perm", inv_perm), ("topk_w", topk_w), ("residual", residual),
+             ("out", out)):
+        _need(rng, "rng", torch.int64, (2,))
+        _need(y_sorted, "y_sorted", dims.dtype, (dims.T * dims.k, dims.d))
+        _need(inv_perm, "inv_perm", torch.int32, (dims.T * dims.k,))
+        _need(topk_w, "topk_w", torch.float32, (dims.T, dims.k))
+        if residual is not None:
+            _need(residual, "residual", dims.dtype, (dims.T, dims.d))
+        o = _out(out, "out", dims.dtype, (dims.T, dims.d), dev)
+        _check("moe_combine_dropout", lib.moe_combine_dropout(
+            ctypes.byref(dims.c()), p, _ptr(rng), _ptr(y_sorted), _ptr(inv_perm), _ptr(topk_w), _ptr(residual),
+            _ptr(o), _stream(None)))
+    return o
+
+
+def dropout_backward(dims: Dims, p: float, rng, dout, dy=None, stream=None):
+    """Gradient of combine_dropout's combined rows: keep / (1 - p) * dout with the decisions
+    of the same p and rng. dy may be dout. Returns dy [T][d]."""
+    lib = load_library()
+    dev = dout.device
+    with _on("dout", dev, stream, ("rng", rng), ("dy", dy)):
+        _need(rng, "rng", torch.int64, (2,))
+        _need(dout, "dout", dims.dtype, (dims.T, dims.d))
+        o = _out(dy, "dy", dims.dtype, (dims.T, dims.d), dev)
+        _check("moe_dropout_backward", lib.moe_dropout_backward(
+            ctypes.byref(dims.c()), p, _ptr(rng), _ptr(dout), _ptr(o), _stream(None)))
+    return o
 
 
 def timing_enable(capacity: int, stages=None):

@@ -246,7 +246,8 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const int32_t* __restric
 }
 
 // One workgroup per token, 8 columns per thread: dx_t = sum_j (dxs[p_j] + dl_j Wg[e_j]),
-// j ascending, fp32, rounded once to bf16.
+// j ascending, fp32, rounded once to bf16. Without kGate the experts' rows alone.
+template <bool kGate>
 __global__ __launch_bounds__(256) void dx_combine_kernel(const float* __restrict__ dxs,
                                                          const int32_t* __restrict__ inv_perm,
                                                          const int32_t* __restrict__ idx,
@@ -263,13 +264,15 @@ __global__ __launch_bounds__(256) void dx_combine_kernel(const float* __restrict
       const float* r = dxs + static_cast<int64_t>(clamp_assign(inv_perm[a], n_assign)) * d + c;
       const f32x4_t r0 = *reinterpret_cast<const f32x4_t*>(r);
       const f32x4_t r1 = *reinterpret_cast<const f32x4_t*>(r + 4);
-      float gw[8];
-      unpack8(*reinterpret_cast<const u32x4_t*>(wg + static_cast<int64_t>(clamp_assign(idx[a], E)) * d + c), gw);
-      const float l = dl[a];
+      float gw[8], l = 0.0f;
+      if constexpr (kGate) {
+        unpack8(*reinterpret_cast<const u32x4_t*>(wg + static_cast<int64_t>(clamp_assign(idx[a], E)) * d + c), gw);
+        l = dl[a];
+      }
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
         acc[m] += m < 4 ? r0[m] : r1[m - 4];
-        acc[m] += l * gw[m];
+        if constexpr (kGate) acc[m] += l * gw[m];
       }
     }
     *reinterpret_cast<u32x4_t*>(dx + t * d + c) = pack8(acc);
@@ -406,8 +409,12 @@ hipError_t launch_route_bwd(const int32_t* idx, const float* topk_w, const int32
 hipError_t launch_dx_combine(const float* dxs, const int32_t* inv_perm, const int32_t* idx, const float* dl,
                              const void* wg, int64_t T, int k, int E, int64_t d, void* dx, hipStream_t s) {
   if (T <= 0) return hipSuccess;
-  hipLaunchKernelGGL(dx_combine_kernel, dim3(static_cast<unsigned>(T)), dim3(256), 0, s, dxs, inv_perm, idx, dl,
-                     static_cast<const bf16_t*>(wg), k, E, d, static_cast<bf16_t*>(dx));
+  if (wg)
+    hipLaunchKernelGGL(dx_combine_kernel<true>, dim3(static_cast<unsigned>(T)), dim3(256), 0, s, dxs, inv_perm, idx, dl,
+                       static_cast<const bf16_t*>(wg), k, E, d, static_cast<bf16_t*>(dx));
+  else
+    hipLaunchKernelGGL(dx_combine_kernel<false>, dim3(static_cast<unsigned>(T)), dim3(256), 0, s, dxs, inv_perm, idx,
+                       dl, nullptr, k, E, d, static_cast<bf16_t*>(dx));
   return hipGetLastError();
 }
 

@@ -2,17 +2,18 @@
 // fused FFN kernel so that both produce the same bits:
 // out[t][c..c+7] = sum_{j ascending} w[t][j] * y[inv_perm[t*k + j]][c..c+7]
 // (fp32 fused multiply-add), plus y[n_assign + s*T + t] for shared experts s
-// ascending, rounded once to the output type.
+// ascending, rounded once to the output type. The sum itself (combine_sum) is
+// also what the combine with dropout starts from.
 #pragma once
 #include "common.h"
 
 namespace moe {
 
+// the routed slots' sum, in slot order
 template <int kDtype>
-__device__ __forceinline__ void combine_vec(const void* __restrict__ y, const int32_t* __restrict__ inv_perm,
-                                            const float* __restrict__ w, void* __restrict__ out, int64_t d, int k,
-                                            int64_t n_assign, int n_shared, int64_t T, int64_t t, int64_t c) {
-  float acc[8];
+__device__ __forceinline__ void combine_sum(const void* __restrict__ y, const int32_t* __restrict__ inv_perm,
+                                            const float* __restrict__ w, int64_t d, int k, int64_t n_assign, int64_t t,
+                                            int64_t c, float (&acc)[8]) {
 #pragma unroll
   for (int r = 0; r < 8; ++r) acc[r] = 0.0f;
   // slots in groups of up to 4: the group's row loads are all issued before
@@ -44,6 +45,14 @@ __device__ __forceinline__ void combine_vec(const void* __restrict__ y, const in
         for (int r = 0; r < 8; ++r) acc[r] = __builtin_fmaf(wj[q], v[q][r], acc[r]);
       }
   }
+}
+
+template <int kDtype>
+__device__ __forceinline__ void combine_vec(const void* __restrict__ y, const int32_t* __restrict__ inv_perm,
+                                            const float* __restrict__ w, void* __restrict__ out, int64_t d, int k,
+                                            int64_t n_assign, int n_shared, int64_t T, int64_t t, int64_t c) {
+  float acc[8];
+  combine_sum<kDtype>(y, inv_perm, w, d, k, n_assign, t, c, acc);
   // shared experts: rows n_assign + s*T + t, weight 1, after the routed slots
   for (int sh = 0; sh < n_shared; ++sh) {
     const int64_t p = n_assign + static_cast<int64_t>(sh) * T + t;

@@ -174,6 +174,7 @@ hipError_t launch_swiglu_bwd(const float* q, const void* gu, const int32_t* perm
                              int64_t f, void* dgu, float* dwp, hipStream_t s);
 hipError_t launch_route_bwd(const int32_t* idx, const float* topk_w, const int32_t* inv_perm, const float* dwp,
                             int64_t T, int k, int E, float* dl, float* dtopk_w, float* dlogits, hipStream_t s);
+// wg null: without the gate's part
 hipError_t launch_dx_combine(const float* dxs, const int32_t* inv_perm, const int32_t* idx, const float* dl,
                              const void* wg, int64_t T, int k, int E, int64_t d, void* dx, hipStream_t s);
 int gate_parts();

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "moe.h"
+#include "abi_host.h"
 #include "kernels.h"
 
 namespace moe {
@@ -27,58 +28,11 @@ int device_cu_count() {
   return cache[dev];
 }
 
+Timing g_timing;
+
 namespace {
 
-constexpr size_t kAlign = 256;
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-// ---------------- stage timing ----------------
-struct Timing {
-  std::mutex mu;
-  bool on = false;
-  int cap = 0;
-  unsigned mask = 0xffffffffu;
-  std::vector<hipEvent_t> ev[MOE_NUM_STAGES][2];
-  int n[MOE_NUM_STAGES] = {0};
-} g_timing;
-
-struct StageScope {
-  int stage;
-  hipStream_t s;
-  int slot = -1;
-  StageScope(int st, hipStream_t stream) : stage(st), s(stream) {
-    if (!g_timing.on || !((g_timing.mask >> stage) & 1u)) return;
-    if (g_timing.n[stage] < g_timing.cap) {
-      slot = g_timing.n[stage]++;
-      (void)hipEventRecord(g_timing.ev[stage][0][slot], s);
-    }
-  }
-  ~StageScope() {
-    if (slot >= 0) (void)hipEventRecord(g_timing.ev[stage][1][slot], s);
-  }
-};
-
 // ---------------- validation ----------------
-// a * b * c < lim, computed without overflow (a, b, c >= 0)
-bool product_below(int64_t a, int64_t b, int64_t c, int64_t lim) {
-  return static_cast<__int128>(a) * b * c < static_cast<__int128>(lim);
-}
-
-int check_dims(const moe_dims_t* dm) {
-  if (!dm) return MOE_ERR_INVALID;
-  if (dm->T < 0 || dm->d < 1 || dm->f < 1) return MOE_ERR_INVALID;
-  if (dm->d >= (int64_t(1) << 31) || dm->f >= (int64_t(1) << 31)) return MOE_ERR_INVALID;
-  if (dm->k < 1 || dm->E < dm->k || dm->E > 1024) return MOE_ERR_INVALID;
-  if (dm->dtype != MOE_DTYPE_F32 && dm->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID;
-  // T*k and T*E below 2^31 (k, E >= 1, so T first: the products then fit in 64 bits)
-  if (dm->T >= (int64_t(1) << 31)) return MOE_ERR_INVALID;
-  if (dm->T * dm->k >= (int64_t(1) << 31) || dm->T * dm->E >= (int64_t(1) << 31)) return MOE_ERR_INVALID;
-  // every workspace piece ([T*k][max(d, f)] fp32 at most, and the backward's
-  // transposed activations) stays far inside size_t
-  const int64_t wide = dm->d > dm->f ? dm->d : dm->f;
-  if (!product_below(dm->T * dm->k + 64 * int64_t(dm->E) + 64, 2 * wide, 8, int64_t(1) << 60)) return MOE_ERR_INVALID;
-  return MOE_OK;
-}
 // shared experts: 1 <= n_shared, E + n_shared <= 1024, T * (k + n_shared) < 2^31 and
 // the workspace pieces of those rows inside size_t (dims already checked)
 int check_shared(const moe_dims_t* dm, int n_shared) {
@@ -91,23 +45,8 @@ int check_shared(const moe_dims_t* dm, int n_shared) {
 }
 
 int elt_bytes(const moe_dims_t* dm) { return dm->dtype == MOE_DTYPE_BF16 ? 2 : 4; }
-bool ok16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-bool ok4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
-bool ok4_or_null(const void* p) { return !p || (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 // ---------------- workspace layouts ----------------
-struct Carver {
-  char* base;
-  size_t off = 0;
-  explicit Carver(void* b) : base(static_cast<char*>(b)) {}
-  template <typename P>
-  P* take(size_t bytes) {
-    P* p = base ? reinterpret_cast<P*>(base + off) : nullptr;
-    off = align_up(off + bytes);
-    return p;
-  }
-};
-
 struct RouteWs { float* logits; };
 size_t route_ws(const moe_dims_t* dm, void* ws, bool need_logits, RouteWs* out) {
   Carver c(ws);
@@ -177,8 +116,6 @@ size_t layer_ws(const moe_dims_t* dm, void* ws, LayerWs* out, int n_shared = 0) 
   if (out) *out = r;
   return c.off;
 }
-
-int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 // ---------------- static scratch of the allocation-free entry point ----------------
 // One copy of this array per GPU the library runs on, held until the process
@@ -504,7 +441,7 @@ const char* moe_status_string(int status) {
   switch (status) {
     case MOE_OK: return "ok";
     case MOE_ERR_INVALID: return "invalid argument (null or misaligned pointer, or shape outside the limits)";
-    case MOE_ERR_UNSUPPORTED: return "shape not supported by the GPU path (needs d % 64 == 0, f % 64 == 0, and x, h and one expert matrix under 4 GiB)";
+    case MOE_ERR_UNSUPPORTED: return "shape not supported by the GPU path (the layer needs d % 64 == 0, f % 64 == 0, and x, h and one expert matrix under 4 GiB; moe.h gives each entry point's limits)";
     case MOE_ERR_WORKSPACE: return "workspace too small (see moe_workspace_bytes)";
     case MOE_ERR_HIP: return "HIP launch or runtime error";
     case MOE_ERR_SCRATCH: return "the call needs more scratch than moe_layer_forward_noalloc's static buffer holds (MOE_NOALLOC_SCRATCH_BYTES)";
@@ -787,15 +724,17 @@ size_t moe_backward_workspace_bytes(const moe_dims_t* dm) {
 
 // gu_saved: g | u rows kept by moe_layer_forward_train (read instead of the
 // FC1 recompute), or null. wgrad_bf16: dw1, dw3, dw2 are bf16 (else fp32).
+// gate: with the gate's own part (wg read, dwg and dbias written, dx with the
+// logits' gradient); without it those pointers are not looked at.
 static int run_backward(const moe_dims_t* dm, const void* x, const void* wg, const void* w1, const void* w3,
                         const void* w2, const int32_t* topk_idx, const float* topk_w, const int32_t* counts,
                         const int32_t* offsets, const int32_t* perm, const int32_t* inv_perm, const void* dout,
                         void* dx, float* dwg, float* dbias, void* dw1, void* dw3, void* dw2, float* dlogits,
                         float* dtopk_w, const void* gu_saved, bool wgrad_bf16, void* ws, size_t ws_bytes,
-                        void* stream) {
+                        void* stream, bool gate = true) {
   if (int st = check_dims(dm)) return st;
-  if (!ok16(wg) || !ok16(w1) || !ok16(w3) || !ok16(w2) || !ok16(dwg) || !ok4(dbias) || !ok16(dw1) || !ok16(dw3) ||
-      !ok16(dw2) || !ok4(counts) || !ok4(offsets) || !ok4_or_null(dlogits) || !ok4_or_null(dtopk_w))
+  if (gate && (!ok16(wg) || !ok16(dwg) || !ok4(dbias))) return MOE_ERR_INVALID;
+  if (!ok16(w1) || !ok16(w3) || !ok16(w2) || !ok16(dw1) || !ok16(dw3) || !ok16(dw2) || !ok4(counts) || !ok4(offsets) || !ok4_or_null(dlogits) || !ok4_or_null(dtopk_w))
     return MOE_ERR_INVALID;
   if (dm->T > 0 && (!ok16(x) || !ok4(topk_idx) || !ok4(topk_w) || !ok4(perm) || !ok4(inv_perm) || !ok16(dout) ||
                     !ok16(dx)))
@@ -813,8 +752,8 @@ static int run_backward(const moe_dims_t* dm, const void* x, const void* wg, con
     // (a bf16 gradient of n elements is n / 2 zero floats; E f d is even)
     const int64_t nw = wgrad_bf16 ? E * f * d / 2 : E * f * d;
     for (auto pr : {std::make_pair(static_cast<float*>(dw1), nw), std::make_pair(static_cast<float*>(dw3), nw),
-                    std::make_pair(static_cast<float*>(dw2), nw), std::make_pair(dwg, E * d),
-                    std::make_pair(dbias, int64_t(E))})
+                    std::make_pair(static_cast<float*>(dw2), nw), std::make_pair(dwg, gate ? E * d : 0),
+                    std::make_pair(dbias, gate ? int64_t(E) : 0)})
       if (int st = hip_status(launch_fill_zero(pr.first, pr.second, s))) return st;
     return MOE_OK;
   }
@@ -850,7 +789,8 @@ static int run_backward(const moe_dims_t* dm, const void* x, const void* wg, con
   }
   {
     StageScope sc(MOE_STAGE_BWD_DXSUM, s);
-    if (int st = hip_status(launch_dx_combine(b.dxs, inv_perm, topk_idx, b.dl, wg, T, k, E, d, dx, s))) return st;
+    if (int st = hip_status(launch_dx_combine(b.dxs, inv_perm, topk_idx, b.dl, gate ? wg : nullptr, T, k, E, d, dx, s)))
+      return st;
   }
   {
     StageScope sc(MOE_STAGE_BWD_ACT_T, s);
@@ -877,6 +817,7 @@ static int run_backward(const moe_dims_t* dm, const void* x, const void* wg, con
     if (int st = hip_status(launch_wgrad(b.dgut, b.xgt, dw1, dw3, b.kofs, b.pp, E, 2 * f, d, f, s, wgrad_bf16)))
       return st;
   }
+  if (!gate) return MOE_OK;
   StageScope sc(MOE_STAGE_BWD_GATE, s);
   return hip_status(launch_gate_grad(x, perm, offsets, b.dl, T, k, d, E, b.gpart, b.bpart, dwg, dbias, s));
 }
@@ -910,6 +851,19 @@ int moe_layer_backward_ex(const moe_dims_t* dm, const void* x, const void* wg, c
   if (gu && (reinterpret_cast<uintptr_t>(gu) & 15)) return MOE_ERR_INVALID;
   return run_backward(dm, x, wg, w1, w3, w2, topk_idx, topk_w, counts, offsets, perm, inv_perm, dout, dx, dwg, dbias,
                       dw1, dw3, dw2, dlogits, dtopk_w, gu, wgrad_dtype == MOE_DTYPE_BF16, ws, ws_bytes, stream);
+}
+
+int moe_experts_backward(const moe_dims_t* dm, const void* x, const void* w1, const void* w3, const void* w2,
+                         const int32_t* topk_idx, const float* topk_w, const int32_t* counts, const int32_t* offsets,
+                         const int32_t* perm, const int32_t* inv_perm, const void* dout, const void* gu,
+                         int wgrad_dtype, void* dx, void* dw1, void* dw3, void* dw2, float* dtopk_w, void* ws,
+                         size_t ws_bytes, void* stream) {
+  if (wgrad_dtype != MOE_DTYPE_F32 && wgrad_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID;
+  if (gu && (reinterpret_cast<uintptr_t>(gu) & 15)) return MOE_ERR_INVALID;
+  if (dm && dm->T > 0 && !dtopk_w) return MOE_ERR_INVALID;
+  return run_backward(dm, x, nullptr, w1, w3, w2, topk_idx, topk_w, counts, offsets, perm, inv_perm, dout, dx, nullptr,
+                      nullptr, dw1, dw3, dw2, nullptr, dtopk_w, gu, wgrad_dtype == MOE_DTYPE_BF16, ws, ws_bytes,
+                      stream, false);
 }
 
 int moe_timing_enable(int capacity, unsigned stage_mask) {
