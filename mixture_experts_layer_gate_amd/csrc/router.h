@@ -31,7 +31,7 @@ int balance_parts(int64_t T, int n_seq);
 int balance_blocks(int E);  // expert blocks of the part reduction
 hipError_t launch_balance(const SelectOpts& o, const float* logits, const int32_t* idx, const int32_t* seq_offsets,
                           int n_seq, int64_t T, int E, int k, int parts, float* part_p, int32_t* part_f,
-                          double* part_z, double* term, float* losses, int32_t* load, hipStream_t s);
+                          double* part_z, double* term, uint32_t* done, float* losses, int32_t* load, hipStream_t s);
 
 // Dropout: an element is kept when its 16-bit number is at least thr, and then
 // scaled (scale 0 with thr 65536: everything is dropped). rng: {seed, offset},

@@ -49,6 +49,7 @@ struct BalanceWs {
   int32_t* f;
   double* z;
   double* term;
+  uint32_t* done;
 };
 size_t balance_ws(const moe_dims_t* dm, int n_seq, void* ws, BalanceWs* out) {
   Carver c(ws);
@@ -59,6 +60,7 @@ size_t balance_ws(const moe_dims_t* dm, int n_seq, void* ws, BalanceWs* out) {
   r.f = c.take<int32_t>(sizeof(int32_t) * np * dm->E);
   r.z = c.take<double>(sizeof(double) * np);
   r.term = c.take<double>(sizeof(double) * n_seq * (balance_blocks(dm->E) + 1));
+  r.done = c.take<uint32_t>(sizeof(uint32_t));
   if (out) *out = r;
   return c.off;
 }
@@ -131,7 +133,7 @@ int moe_balance_loss(const moe_dims_t* dm, const moe_route_opts_t* opts, const f
   hipStream_t s = static_cast<hipStream_t>(stream);
   StageScope sc(MOE_STAGE_BALANCE, s);
   return hip_status(launch_balance(o, logits, topk_idx, seq_offsets, n_seq, dm->T, dm->E, dm->k, b.parts, b.p, b.f, b.z,
-                                   b.term, losses, load, s));
+                                   b.term, b.done, losses, load, s));
 }
 
 int moe_route_select_backward(const moe_dims_t* dm, const moe_route_opts_t* opts, const float* logits,

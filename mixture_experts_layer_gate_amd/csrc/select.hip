@@ -29,16 +29,89 @@ __device__ __forceinline__ uint64_t order_bits(double c) {
 constexpr uint64_t kKeyTaken = 0;  // below every key: chosen already, or no expert
 constexpr uint64_t kKeyDead = 1;   // out of the choice: chosen last, in ascending order
 
+// Butterflies over the wave without LDS: lane distances 1, 2 (quad permutes), 4
+// (half-row mirror: the quads are uniform by then), 8 (row rotation), 16 and 32
+// (row swaps). After each step the lanes it joined hold the same value.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return __builtin_amdgcn_update_dpp(v, v, kCtrl, 0xf, 0xf, false);
+}
+template <int kDist>
+__device__ __forceinline__ void partner(uint32_t v, uint32_t& a, uint32_t& b) {
+  if constexpr (kDist == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    a = r[0]; b = r[1];
+  } else if constexpr (kDist == 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    a = r[0]; b = r[1];
+  } else {
+    a = v;
+    b = dpp<kDist == 1 ? 0xB1 : kDist == 2 ? 0x4E : kDist == 4 ? 0x141 : 0x128>(v);
+  }
+}
+template <int kDist>
+__device__ __forceinline__ void partner_of(float v, float& a, float& b) {
+  uint32_t x, y;
+  partner<kDist>(__float_as_uint(v), x, y);
+  a = __uint_as_float(x);
+  b = __uint_as_float(y);
+}
+template <int kDist>
+__device__ __forceinline__ void partner_of(double v, double& a, double& b) {
+  uint32_t lx, ly, hx, hy;
+  partner<kDist>(static_cast<uint32_t>(__double2loint(v)), lx, ly);
+  partner<kDist>(static_cast<uint32_t>(__double2hiint(v)), hx, hy);
+  a = __hiloint2double(static_cast<int>(hx), static_cast<int>(lx));
+  b = __hiloint2double(static_cast<int>(hy), static_cast<int>(ly));
+}
+template <int kDist, typename Op>
+__device__ __forceinline__ float step_f(float v, Op op) {
+  uint32_t a, b;
+  partner<kDist>(__float_as_uint(v), a, b);
+  return op(__uint_as_float(a), __uint_as_float(b));
+}
+template <typename Op>
+__device__ __forceinline__ float wave_all(float v, Op op) {
+  v = step_f<1>(v, op);
+  v = step_f<2>(v, op);
+  v = step_f<4>(v, op);
+  v = step_f<8>(v, op);
+  v = step_f<16>(v, op);
+  return step_f<32>(v, op);
+}
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-  return v;
+  return wave_all(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  return wave_all(v, [](float a, float b) { return a + b; });
 }
 template <typename F>
-__device__ __forceinline__ F wave_sum(F v) {
+__device__ __forceinline__ F wave_sum_any(F v) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
   return v;
+}
+template <int kDist>
+__device__ __forceinline__ uint32_t max_step(uint32_t v) {
+  uint32_t a, b;
+  partner<kDist>(v, a, b);
+  return a > b ? a : b;
+}
+template <int kDist>
+__device__ __forceinline__ uint32_t min_step(uint32_t v) {
+  uint32_t a, b;
+  partner<kDist>(v, a, b);
+  return a < b ? a : b;
+}
+// LDS written by this wave is readable by its other lanes.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
 }
 __device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int off) {
   const uint32_t lo = __shfl_xor(static_cast<uint32_t>(v), off), hi = __shfl_xor(static_cast<uint32_t>(v >> 32), off);
@@ -54,31 +127,62 @@ __device__ __forceinline__ float sigmoid_scaled(float l, float m) {
 
 // lane's experts: lane * VPL + i, i < VPL (so lower lanes hold lower experts)
 template <int VPL>
-__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, float (&l)[VPL]) {
+__device__ __forceinline__ void load_raw(const float* __restrict__ row, int E, float pad, float (&v)[VPL]) {
   const int e0 = (threadIdx.x & 63) * VPL;
+  if constexpr (VPL >= 4) {
+    // whole 16-byte loads where every row starts on such a boundary
+    if (E % 4 == 0 && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const float v = e0 + i < E ? row[e0 + i] : -INFINITY;
-    l[i] = live_value(v) ? fminf(v, kF32Max) : -INFINITY;
+      for (int i = 0; i < VPL; i += 4) {
+        const f32x4_t u = e0 + i < E ? *reinterpret_cast<const f32x4_t*>(row + e0 + i) : f32x4_t{pad, pad, pad, pad};
+        v[i] = u[0]; v[i + 1] = u[1]; v[i + 2] = u[2]; v[i + 3] = u[3];
+      }
+      return;
+    }
   }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) v[i] = e0 + i < E ? row[e0 + i] : pad;
+}
+template <int VPL>
+__device__ __forceinline__ void clean_row(float (&l)[VPL]) {
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) l[i] = live_value(l[i]) ? fminf(l[i], kF32Max) : -INFINITY;
+}
+template <int VPL>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, float (&l)[VPL]) {
+  load_raw<VPL>(row, E, -INFINITY, l);
+  clean_row<VPL>(l);
 }
 
-// One wave per token: scores and keys in registers, groups ranked from LDS,
-// then k rounds of a wave arg-max over (key, logit, lower expert).
+// LDS of one wave.
 template <int VPL>
-__global__ __launch_bounds__(64) void select_kernel(SelectOpts o, const float* __restrict__ logits,
-                                                    const float* __restrict__ bias, int T, int E, int k,
-                                                    int32_t* __restrict__ idx, float* __restrict__ w) {
-  __shared__ uint64_t skey[64 * VPL];
-  __shared__ float sel[64 * VPL];  // logits of the chosen experts (NaN: out of the choice)
-  const int lane = threadIdx.x;
-  const int e0 = lane * VPL;
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-  __syncthreads();  // the previous token's LDS is read out
-  float l[VPL];
-  load_row<VPL>(logits + t * E, E, l);
+struct SelectLds {
+  uint64_t key[64 * VPL];  // keys by expert; or the candidates' (key, expert)
+  float val[64 * VPL];     // chosen slots' logits (NaN: out of the choice); or the candidates'
+};
 
-  // scores and keys
+// Weights of chosen logits v (NaN or -inf: out of the choice) in fp32; a
+// renormalised weight is a ratio, formed from scores scaled by the largest
+// chosen one (mx). m, inv_z: the row's largest logit and 1 / sum exp(l - m).
+__device__ __forceinline__ float weigh(const SelectOpts& o, float v, float mx, float m, float inv_z) {
+  if (!live_value(v)) return 0.0f;
+  if (o.renorm) return o.sigmoid ? sigmoid_scaled(v, mx) : expf(v - mx);
+  return o.sigmoid ? sigmoidf(v) : expf(v - m) * inv_z;
+}
+__device__ __forceinline__ float weight_factor(const SelectOpts& o, float tot) {
+  return o.renorm ? (tot > 0.0f ? o.scale / tot : 0.0f) : o.scale;
+}
+
+// The selection by the definition, for any k: double keys, groups ranked from
+// LDS, then k rounds of a wave arg-max over (key, logit, lower expert).
+template <int VPL>
+__device__ __forceinline__ void select_exact(const SelectOpts& o, const float* __restrict__ row,
+                                             const float* __restrict__ bias, int E, int k,
+                                             int32_t* __restrict__ idx, float* __restrict__ w, SelectLds<VPL>& sh) {
+  const int lane = threadIdx.x & 63;
+  const int e0 = lane * VPL;
+  float l[VPL];
+  load_row<VPL>(row, E, l);
   uint64_t key[VPL];
   float m = l[0];
 #pragma unroll
@@ -91,7 +195,7 @@ __global__ __launch_bounds__(64) void select_kernel(SelectOpts o, const float* _
       z[i] = live_value(l[i]) ? exp(static_cast<double>(l[i]) - m) : 0.0;
       zs += z[i];
     }
-    zs = wave_sum(zs);
+    zs = wave_sum_any(zs);
   }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -103,16 +207,17 @@ __global__ __launch_bounds__(64) void select_kernel(SelectOpts o, const float* _
   }
 
   if (o.groups > 1) {
+    wave_lds_sync();
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) skey[e0 + i] = key[i];
-    __syncthreads();
+    for (int i = 0; i < VPL; ++i) sh.key[e0 + i] = key[i];
+    wave_lds_sync();
     const int per = E / o.groups;
     // lane g: group g's key, again as ordered bits (0: no live expert)
     uint64_t gk = 0;
     if (lane < o.groups) {
       uint64_t a = 0, b = 0;
       for (int e = lane * per; e < (lane + 1) * per; ++e) {
-        const uint64_t v = skey[e];
+        const uint64_t v = sh.key[e];
         if (v > a) { b = a; a = v; }
         else if (v > b) b = v;
       }
@@ -128,8 +233,8 @@ __global__ __launch_bounds__(64) void select_kernel(SelectOpts o, const float* _
     }
     int rank = 0;
     for (int g = 0; g < o.groups; ++g) {
-      const uint64_t v = (static_cast<uint64_t>(__shfl(static_cast<uint32_t>(gk >> 32), g)) << 32) |
-                         __shfl(static_cast<uint32_t>(gk), g);
+      const uint64_t v = (static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(gk >> 32), g)) << 32) |
+                         static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(gk), g));
       rank += v > gk || (v == gk && g < lane);
     }
     const uint64_t kept = __ballot(lane < o.groups && rank < o.topk_groups);
@@ -138,6 +243,7 @@ __global__ __launch_bounds__(64) void select_kernel(SelectOpts o, const float* _
       if (e0 + i < E && !((kept >> ((e0 + i) / per)) & 1)) key[i] = kKeyDead;
   }
 
+  wave_lds_sync();
   for (int j = 0; j < k; ++j) {
     uint64_t bk = kKeyTaken;
     float bl = 0.0f;
@@ -159,30 +265,287 @@ __global__ __launch_bounds__(64) void select_kernel(SelectOpts o, const float* _
     for (int i = 0; i < VPL; ++i)
       if (e0 + i == be) key[i] = kKeyTaken;
     if (lane == 0) {
-      idx[t * k + j] = be;
-      sel[j] = bk > kKeyDead ? bl : NAN;
+      idx[j] = be;
+      sh.val[j] = bk > kKeyDead ? bl : NAN;
     }
   }
-  __syncthreads();
+  wave_lds_sync();
 
-  // Weights in fp32 from the chosen logits; a renormalised weight is a ratio,
-  // formed from scores scaled by the largest chosen one.
   float mx = -INFINITY;
-  for (int j = lane; j < k; j += 64) mx = fmaxf(mx, live_value(sel[j]) ? sel[j] : -INFINITY);
+  for (int j = lane; j < k; j += 64) mx = fmaxf(mx, live_value(sh.val[j]) ? sh.val[j] : -INFINITY);
   mx = wave_max(mx);
   const float inv_z = o.sigmoid ? 1.0f : static_cast<float>(1.0 / zs);
-  auto score = [&](float v) {
-    if (!live_value(v)) return 0.0f;
-    if (o.renorm) return o.sigmoid ? sigmoid_scaled(v, mx) : expf(v - mx);
-    return o.sigmoid ? sigmoidf(v) : expf(v - m) * inv_z;
-  };
   float tot = 0.0f;
   if (o.renorm) {
-    for (int j = lane; j < k; j += 64) tot += score(sel[j]);
+    for (int j = lane; j < k; j += 64) tot += weigh(o, sh.val[j], mx, m, inv_z);
     tot = wave_sum(tot);
   }
-  const float f = o.renorm ? (tot > 0.0f ? o.scale / tot : 0.0f) : o.scale;
-  for (int j = lane; j < k; j += 64) w[t * k + j] = score(sel[j]) * f;
+  const float f = weight_factor(o, tot);
+  for (int j = lane; j < k; j += 64) w[j] = weigh(o, sh.val[j], mx, m, inv_z) * f;
+  wave_lds_sync();
+}
+
+// fp32 order bits: larger values, larger integers (-0 as +0).
+__device__ __forceinline__ uint32_t order32(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float order32_back(uint32_t q) {
+  return __uint_as_float(q ^ ((q >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+constexpr int kFastK = 8;
+// Error of an fp32 key c: less than kErr (1 + |c| / 8). A score is at most 1 and
+// comes out of an exponential, a reciprocal and (softmax) a sum over at most 16 +
+// 6 additions, each within 2^-23 or less of it; adding the bias rounds by 2^-24 |c|.
+constexpr float kErr = 0x1p-19f;
+__device__ __forceinline__ float margin(float c) { return 2.0f * kErr * (1.0f + 0.125f * fabsf(c)); }
+
+// Groups kept, as a mask with bit g * lpg set: 64 / groups lanes (lpg, a power of
+// two) scan a group's keys (c: this lane's, -inf out of the choice) and join.
+// `sure` turns false when fp32 keys cannot tell the last kept from the next.
+template <typename V, int VPL>
+__device__ __forceinline__ uint64_t keep_groups(const SelectOpts& o, const V (&c)[VPL], int per, int lpg, V* sh,
+                                                bool& sure) {
+  const int lane = threadIdx.x & 63;
+  wave_lds_sync();
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) sh[lane * VPL + i] = c[i];
+  wave_lds_sync();
+  const auto most = [](V x, V y) { return x > y ? x : y; };
+  const auto least = [](V x, V y) { return x > y ? y : x; };
+  const int g = lane / lpg, j = lane % lpg;
+  V a = -INFINITY, b = -INFINITY;
+  if (g < o.groups)
+    for (int e = j; e < per; e += lpg) {
+      const V v = sh[g * per + e];
+      b = most(b, least(a, v));
+      a = most(a, v);
+    }
+  auto join = [&](auto dist) {
+    constexpr int D = decltype(dist)::value;
+    if (lpg > D) {
+      V a0, a1, b0, b1;
+      partner_of<D>(a, a0, a1);
+      partner_of<D>(b, b0, b1);
+      b = most(least(a0, a1), most(b0, b1));
+      a = most(a0, a1);
+    }
+  };
+  join(std::integral_constant<int, 1>{});
+  join(std::integral_constant<int, 2>{});
+  join(std::integral_constant<int, 4>{});
+  join(std::integral_constant<int, 8>{});
+  join(std::integral_constant<int, 16>{});
+  join(std::integral_constant<int, 32>{});
+  V gk = a;
+  if (o.top2 && b > -INFINITY) gk = a + b;
+  const auto of_lane = [&](int at) -> V {
+    if constexpr (sizeof(V) == 4)
+      return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(gk), at));
+    else
+      return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(gk), at),
+                              __builtin_amdgcn_readlane(__double2loint(gk), at));
+  };
+  int rank = 0;
+  for (int q = 0; q < o.groups; ++q) {
+    const V v = of_lane(q * lpg);
+    rank += v > gk || (v == gk && q < g);
+  }
+  const bool head = j == 0 && g < o.groups;
+  if constexpr (sizeof(V) == 4) {
+    const float gl = of_lane(__ffsll(__ballot(head && rank == o.topk_groups - 1)) - 1);
+    const float gn = of_lane(__ffsll(__ballot(head && rank == o.topk_groups)) - 1);
+    sure = gl - gn > 2.0f * margin(gl);
+  }
+  return __ballot(head && rank < o.topk_groups);
+}
+
+// The same selection for k <= 8 from fp32 keys, one wave per token. Returns
+// false (nothing written) for rows with too few experts in the choice to bound
+// the candidates; the caller then takes select_exact.
+//
+// Candidates: the lanes fall into 8 classes (lane mod 8), and the smallest of
+// the classes' largest keys has at least 8 keys at or above it; only the keys
+// down to there (8 H_8 = 22 of them on average) are ranked, one per lane, by
+// counting the larger ones.
+//
+// Without bias and groups the key is the logit itself and the order exact. With
+// them it is the fp32 score plus the bias: where a chosen expert's key is within
+// its error of a lower one's (about one row in a hundred), the candidates' keys
+// are formed again in doubles and ranked by those; likewise the groups' keys
+// where the last kept and the next are that close.
+template <int VPL, bool kKeyed>
+__device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&raw)[VPL], const float* __restrict__ bias,
+                                            int E, int k, int32_t* __restrict__ idx, float* __restrict__ w,
+                                            SelectLds<VPL>& sh) {
+  const int lane = threadIdx.x & 63;
+  const int e0 = lane * VPL;
+  float l[VPL], c[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) l[i] = raw[i];
+  clean_row<VPL>(l);
+
+  // the row's largest logit and 1 / sum exp(l - m), where scores need them
+  float m = 0.0f, inv_z = 0.0f;
+  if (!o.sigmoid && (kKeyed || !o.renorm)) {
+    m = l[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+    m = wave_max(m);
+    float zs = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      c[i] = live_value(l[i]) ? expf(l[i] - m) : 0.0f;
+      zs += c[i];
+    }
+    zs = wave_sum(zs);
+    inv_z = zs > 0.0f ? 1.0f / zs : 0.0f;
+  }
+  // 1 / sum exp(l - m) in doubles, and a double key (for a live expert)
+  auto exact_inv_z = [&]() -> double {
+    double zs = 0.0;
+    if (!o.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (live_value(l[i])) zs += exp(static_cast<double>(l[i]) - m);
+      zs = wave_sum_any(zs);
+    }
+    return zs;
+  };
+  auto exact_key = [&](float v, float b, double zs) -> double {
+    return (o.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(v))) : exp(static_cast<double>(v) - m) / zs) + b;
+  };
+  // keys; -inf: out of the choice
+  if constexpr (kKeyed) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const float b = bias && e0 + i < E ? bias[e0 + i] : 0.0f;
+      const float s = o.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-l[i])) : c[i] * inv_z;
+      c[i] = live_value(l[i]) && live_value(b) ? s + b : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c[i] = l[i];
+  }
+
+  if (kKeyed && o.groups > 1) {
+    const int per = E / o.groups;
+    const int lpg = 1 << (31 - __clz(64 / o.groups));
+    bool sure = true;
+    uint64_t kept = keep_groups<float, VPL>(o, c, per, lpg, sh.val, sure);
+    if (!sure) {
+      const double zs = exact_inv_z();
+      double cd[VPL];
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        cd[i] = c[i] > -INFINITY ? exact_key(l[i], bias ? bias[e0 + i] : 0.0f, zs) : -INFINITY;
+      kept = keep_groups<double, VPL>(o, cd, per, lpg, reinterpret_cast<double*>(sh.key), sure);
+    }
+    const float inv_per = 1.0f / static_cast<float>(per);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int ge = static_cast<int>((static_cast<float>(e0 + i) + 0.5f) * inv_per);  // (e0 + i) / per, below 2^11
+      if (!((kept >> ((ge * lpg) & 63)) & 1)) c[i] = -INFINITY;
+    }
+  }
+
+  // candidates
+  uint32_t q[VPL], top = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    q[i] = e0 + i < E ? order32(c[i]) : 0;
+    top = q[i] > top ? q[i] : top;
+  }
+  top = max_step<8>(top);
+  top = max_step<16>(top);
+  top = max_step<32>(top);
+  top = min_step<1>(top);
+  top = min_step<2>(top);
+  top = min_step<4>(top);
+  float cut = order32_back(top);
+  if (kKeyed) cut -= margin(cut);
+  // (a cut of -inf stays so; NaN, from a class of no experts or +inf, admits all)
+  int n = 0;
+  wave_lds_sync();
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const bool in = e0 + i < E && !(c[i] < cut);
+    const uint64_t mask = __ballot(in);
+    const int at = n + lanes_below(mask);
+    if (in && at < 64) {
+      sh.key[at] = (static_cast<uint64_t>(q[i]) << 32) | static_cast<uint32_t>(E - 1 - (e0 + i));
+      sh.val[at] = l[i];
+    }
+    n += __popcll(mask);
+  }
+  if (n > 64) return false;
+  wave_lds_sync();
+  const bool mine = lane < n;
+  const uint64_t key = mine ? sh.key[lane] : 0;
+  float v = mine ? sh.val[lane] : -INFINITY;
+  const int e = E - 1 - static_cast<int>(static_cast<uint32_t>(key));
+  const float cv = order32_back(static_cast<uint32_t>(key >> 32));
+  const bool live = mine && cv > -INFINITY;
+  // larger candidates; in keyed form also those not clearly smaller
+  const float low = cv - margin(cv);
+  int rank = 0, near = 0;
+#pragma unroll 4
+  for (int r = 0; r < n; ++r) {
+    const uint64_t kr = sh.key[r];
+    rank += kr > key;
+    if constexpr (kKeyed) near += order32_back(static_cast<uint32_t>(kr >> 32)) >= low;
+  }
+  if constexpr (kKeyed) {
+    if (__ballot(live && rank < k && near != rank + 1)) {
+      const double zs = exact_inv_z();
+      uint64_t hi = kKeyTaken, lo = static_cast<uint32_t>(E - 1 - e);
+      if (mine) hi = live ? order_bits(exact_key(v, bias ? bias[e] : 0.0f, zs)) : kKeyDead;
+      if (live) lo |= static_cast<uint64_t>(order32(v)) << 32;
+      const auto of_lane = [](uint64_t x, int at) {
+        return (static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(x >> 32), at)) << 32) |
+               static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(x), at));
+      };
+      rank = 0;
+      for (int r = 0; r < n; ++r) {
+        const uint64_t h = of_lane(hi, r), x = of_lane(lo, r);
+        rank += h > hi || (h == hi && x > lo);
+      }
+    }
+  }
+  const bool chosen = mine && rank < k;
+  if (!chosen || !live) v = -INFINITY;
+  float mx = 0.0f, tot = 0.0f, f = o.scale;
+  if (o.renorm) mx = wave_max(v);
+  const float sc = weigh(o, v, mx, m, inv_z);
+  if (o.renorm) {
+    tot = wave_sum(sc);
+    f = weight_factor(o, tot);
+  }
+  if (chosen) {
+    idx[rank] = e;
+    w[rank] = sc * f;
+  }
+  wave_lds_sync();
+  return true;
+}
+
+template <int VPL, bool kKeyed, bool kFast>
+__global__ __launch_bounds__(256) void select_kernel(SelectOpts o, const float* __restrict__ logits,
+                                                     const float* __restrict__ bias, int T, int E, int k,
+                                                     int32_t* __restrict__ idx, float* __restrict__ w) {
+  __shared__ SelectLds<VPL> lds[4];
+  const int wv = threadIdx.x >> 6;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wv; t < T; t += 4 * static_cast<int64_t>(gridDim.x)) {
+    const float* row = logits + t * E;
+    int32_t* ti = idx + t * k;
+    float* tw = w + t * k;
+    if constexpr (kFast) {
+      float raw[VPL];
+      load_raw<VPL>(row, E, -INFINITY, raw);
+      if (select_fast<VPL, kKeyed>(o, raw, bias, E, k, ti, tw, lds[wv])) continue;
+    }
+    select_exact<VPL>(o, row, bias, E, k, ti, tw, lds[wv]);
   }
 }
 
@@ -343,12 +706,13 @@ __global__ __launch_bounds__(256) void balance_part_kernel(SelectOpts o, const f
                                                            const int32_t* __restrict__ idx,
                                                            const int32_t* __restrict__ seq_offsets, int T, int E, int k,
                                                            float* __restrict__ part_p, int32_t* __restrict__ part_f,
-                                                           double* __restrict__ part_z) {
+                                                           double* __restrict__ part_z, uint32_t* __restrict__ done) {
   __shared__ int32_t cnt[64 * VPL];
   __shared__ float psum[4][64 * VPL];
   __shared__ double zsum[4];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int r = blockIdx.x, s = blockIdx.y, parts = gridDim.x;
+  if (r == 0 && s == 0 && threadIdx.x == 0) *done = 0;
   const int a = seq_offsets ? clamp_off(seq_offsets[s], T) : 0, b = seq_offsets ? clamp_off(seq_offsets[s + 1], T) : T;
   const int64_t n = b > a ? b - a : 0;
   const int lo = a + static_cast<int>(n * r / parts), hi = a + static_cast<int>(n * (r + 1) / parts);
@@ -358,34 +722,59 @@ __global__ __launch_bounds__(256) void balance_part_kernel(SelectOpts o, const f
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
   double zacc = 0.0;
-  for (int t = lo + wv; t < hi; t += 4) {
-    float l[VPL], x[VPL];
-    load_row<VPL>(logits + static_cast<int64_t>(t) * E, E, l);
-    for (int j = lane; j < k; j += 64) {
-      const int e = idx[static_cast<int64_t>(t) * k + j];
-      if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
-    }
-    float m = l[0];
+  // two rows at a time: their loads and their reductions' latencies overlap
+  for (int t = lo + wv; t < hi; t += 8) {
+    float l[2][VPL], x[2][VPL], m[2], zs[2], tot[2];
+    int32_t e[2];
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
-    m = wave_max(m);
-    if (m == -INFINITY) continue;
-    float zs = 0.0f, tot = 0.0f;
+    for (int u = 0; u < 2; ++u) {
+      const bool on = t + 4 * u < hi;
+      const int64_t row = on ? t + 4 * u : t;
+      load_raw<VPL>(logits + row * E, E, -INFINITY, l[u]);
+      e[u] = on && lane < k ? idx[row * k + lane] : -1;
+      for (int j = lane + 64; on && j < k; j += 64) {
+        const int q = idx[row * k + j];
+        if (q >= 0 && q < E) atomicAdd(&cnt[q], 1);
+      }
+      if (!on) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      x[i] = live_value(l[i]) ? expf(l[i] - m) : 0.0f;
-      zs += x[i];
-      if (o.sigmoid) {
-        x[i] = live_value(l[i]) ? sigmoid_scaled(l[i], m) : 0.0f;
-        tot += x[i];
+        for (int i = 0; i < VPL; ++i) l[u][i] = -INFINITY;
       }
     }
-    zs = wave_sum(zs);
-    tot = 1.0f / (o.sigmoid ? wave_sum(tot) : zs);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) acc[i] += x[i] * tot;
-    const double lse = static_cast<double>(m) + logf(zs);
-    zacc += lse * lse;
+    for (int u = 0; u < 2; ++u) {
+      if (e[u] >= 0 && e[u] < E) atomicAdd(&cnt[e[u]], 1);
+      clean_row<VPL>(l[u]);
+      m[u] = l[u][0];
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) m[u] = fmaxf(m[u], l[u][i]);
+      m[u] = wave_max(m[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      zs[u] = tot[u] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        x[u][i] = live_value(l[u][i]) ? expf(l[u][i] - m[u]) : 0.0f;
+        zs[u] += x[u][i];
+        if (o.sigmoid) {
+          // sigmoid(l) / e^min(m, 0), from the same exponential where the row is not all negative
+          if (live_value(l[u][i])) x[u][i] = m[u] >= 0.0f ? sigmoidf(l[u][i]) : x[u][i] / (1.0f + expf(l[u][i]));
+          tot[u] += x[u][i];
+        }
+      }
+      zs[u] = wave_sum(zs[u]);
+      tot[u] = o.sigmoid ? wave_sum(tot[u]) : zs[u];
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (m[u] == -INFINITY) continue;  // nothing in the choice, or no row
+      const float r = 1.0f / tot[u];
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) acc[i] += x[u][i] * r;
+      const double lse = static_cast<double>(m[u]) + logf(zs[u]);
+      zacc += lse * lse;
+    }
   }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) psum[wv][lane * VPL + i] = acc[i];
@@ -402,76 +791,82 @@ __global__ __launch_bounds__(256) void balance_part_kernel(SelectOpts o, const f
 constexpr int kRedE = 16;  // experts per block of the part reduction
 
 // Block (eb, s): parts summed in order for kRedE experts (16 slices of parts,
-// then the slices in order), load[s][e] written, the experts' terms f * P added.
-// term[s][eb]; block 0's slot [s][blocks] holds the sequence's sum of lse^2.
+// then the slices in order), load[s][e] written, the experts' terms f * P added
+// into term[s][eb]; term[s][blocks] holds the sequence's sum of lse^2. The block
+// that finishes last (a counter the part kernel cleared) adds the terms in order:
+// B = 1/filled sum_s E / (k n_s^2) sum_e f P, Z = sum lse^2 / covered.
 __global__ __launch_bounds__(256) void balance_reduce_kernel(const float* __restrict__ part_p,
                                                              const int32_t* __restrict__ part_f,
-                                                             const double* __restrict__ part_z, int parts, int E,
-                                                             double* __restrict__ term, int32_t* __restrict__ load) {
+                                                             const double* __restrict__ part_z, int parts,
+                                                             const int32_t* __restrict__ seq_offsets, int n_seq, int T,
+                                                             int E, int k, double* term, int32_t* __restrict__ load,
+                                                             uint32_t* done, float* __restrict__ losses) {
   __shared__ double sp[16][kRedE];
   __shared__ int32_t sf[16][kRedE];
-  __shared__ double sz[256];
+  __shared__ double sz[4];
+  __shared__ bool last;
+  const int blocks = gridDim.x;
   const int s = blockIdx.y, el = threadIdx.x % kRedE, sl = threadIdx.x / kRedE;
   const int e = blockIdx.x * kRedE + el;
   double p = 0.0;
   int32_t f = 0;
-  if (e < E)
+  if (e < E) {
+    const int64_t base = static_cast<int64_t>(s) * parts * E + e;
+#pragma unroll 8
     for (int r = sl; r < parts; r += 16) {
-      const int64_t at = (static_cast<int64_t>(s) * parts + r) * E + e;
-      p += part_p[at];
-      f += part_f[at];
+      p += part_p[base + static_cast<int64_t>(r) * E];
+      f += part_f[base + static_cast<int64_t>(r) * E];
     }
+  }
   sp[sl][el] = p;
   sf[sl][el] = f;
   double z = 0.0;
-  if (blockIdx.x == 0)
+  if (blockIdx.x == 0) {
     for (int r = threadIdx.x; r < parts; r += 256) z += part_z[static_cast<int64_t>(s) * parts + r];
-  sz[threadIdx.x] = z;
+    z = wave_sum_any(z);
+    if ((threadIdx.x & 63) == 0) sz[threadIdx.x >> 6] = z;
+  }
   __syncthreads();
   if (threadIdx.x < kRedE) {
     double ps = 0.0;
     int32_t fs = 0;
+#pragma unroll
     for (int q = 0; q < 16; ++q) { ps += sp[q][threadIdx.x]; fs += sf[q][threadIdx.x]; }
     if (e < E) load[static_cast<int64_t>(s) * E + e] = fs;
-    sp[0][threadIdx.x] = ps * fs;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double v = 0.0;
-    for (int q = 0; q < kRedE; ++q) v += sp[0][q];
-    double* row = term + static_cast<int64_t>(s) * (gridDim.x + 1);
-    row[blockIdx.x] = v;
-    if (blockIdx.x == 0) {
-      double zt = 0.0;
-      for (int q = 0; q < 256; ++q) zt += sz[q];
-      row[gridDim.x] = zt;
+    double v = ps * fs;
+#pragma unroll
+    for (int off = kRedE / 2; off >= 1; off >>= 1) v += __shfl_xor(v, off, kRedE);
+    if (threadIdx.x == 0) {
+      double* row = term + static_cast<int64_t>(s) * (blocks + 1);
+      row[blockIdx.x] = v;
+      if (blockIdx.x == 0) row[blocks] = ((sz[0] + sz[1]) + sz[2]) + sz[3];
+      __threadfence();
+      last = atomicAdd(done, 1u) == gridDim.x * gridDim.y - 1;
     }
   }
-}
-
-// One wave: B = 1/filled sum_s E / (k n_s^2) sum_e f P, Z = sum lse^2 / covered.
-__global__ __launch_bounds__(64) void balance_final_kernel(const double* __restrict__ term,
-                                                           const int32_t* __restrict__ seq_offsets, int n_seq, int T,
-                                                           int E, int k, int blocks, float* __restrict__ losses) {
+  __syncthreads();
+  if (!last || threadIdx.x >= 64) return;
+  __threadfence();
+  const volatile double* terms = term;
   double bsum = 0.0, zsum = 0.0;
   int filled = 0, covered = 0;
-  for (int s = threadIdx.x; s < n_seq; s += 64) {
-    const int a = seq_offsets ? clamp_off(seq_offsets[s], T) : 0;
-    const int b = seq_offsets ? clamp_off(seq_offsets[s + 1], T) : T;
+  for (int q = threadIdx.x; q < n_seq; q += 64) {
+    const int a = seq_offsets ? clamp_off(seq_offsets[q], T) : 0;
+    const int b = seq_offsets ? clamp_off(seq_offsets[q + 1], T) : T;
     if (b <= a) continue;
     const double n = b - a;
     double v = 0.0;
-    const double* row = term + static_cast<int64_t>(s) * (blocks + 1);
-    for (int q = 0; q < blocks; ++q) v += row[q];
+    const volatile double* row = terms + static_cast<int64_t>(q) * (blocks + 1);
+    for (int x = 0; x < blocks; ++x) v += row[x];
     bsum += v * E / (k * n * n);
     zsum += row[blocks];
     filled += 1;
     covered += b - a;
   }
-  bsum = wave_sum(bsum);
-  zsum = wave_sum(zsum);
-  filled = wave_sum(filled);
-  covered = wave_sum(covered);
+  bsum = wave_sum_any(bsum);
+  zsum = wave_sum_any(zsum);
+  filled = wave_sum_any(filled);
+  covered = wave_sum_any(covered);
   if (threadIdx.x == 0) {
     losses[0] = filled ? static_cast<float>(bsum / filled) : 0.0f;
     losses[1] = covered ? static_cast<float>(zsum / covered) : 0.0f;
@@ -497,9 +892,19 @@ hipError_t by_width(int E, F&& f) {
 
 hipError_t launch_select(const SelectOpts& o, const float* logits, const float* balance_bias, int64_t T, int E, int k,
                          int32_t* idx, float* w, hipStream_t s) {
+  const dim3 grid(token_grid((T + 3) / 4));
+  const int Ti = static_cast<int>(T);
   return by_width(E, [&](auto v) {
-    hipLaunchKernelGGL((select_kernel<decltype(v)::value>), dim3(token_grid(T)), dim3(64), 0, s, o, logits,
-                       balance_bias, static_cast<int>(T), E, k, idx, w);
+    constexpr int VPL = decltype(v)::value;
+    if (k > kFastK)
+      hipLaunchKernelGGL((select_kernel<VPL, true, false>), grid, dim3(256), 0, s, o, logits, balance_bias, Ti, E, k,
+                         idx, w);
+    else if (balance_bias || o.groups > 1)
+      hipLaunchKernelGGL((select_kernel<VPL, true, true>), grid, dim3(256), 0, s, o, logits, balance_bias, Ti, E, k,
+                         idx, w);
+    else
+      hipLaunchKernelGGL((select_kernel<VPL, false, true>), grid, dim3(256), 0, s, o, logits, balance_bias, Ti, E, k,
+                         idx, w);
     return hipGetLastError();
   });
 }
@@ -527,19 +932,17 @@ int balance_blocks(int E) { return (E + kRedE - 1) / kRedE; }
 
 hipError_t launch_balance(const SelectOpts& o, const float* logits, const int32_t* idx, const int32_t* seq_offsets,
                           int n_seq, int64_t T, int E, int k, int parts, float* part_p, int32_t* part_f,
-                          double* part_z, double* term, float* losses, int32_t* load, hipStream_t s) {
+                          double* part_z, double* term, uint32_t* done, float* losses, int32_t* load,
+                          hipStream_t s) {
   const int Ti = static_cast<int>(T), blocks = balance_blocks(E);
   const hipError_t st = by_width(E, [&](auto v) {
     hipLaunchKernelGGL((balance_part_kernel<decltype(v)::value>), dim3(parts, n_seq), dim3(256), 0, s, o, logits, idx,
-                       seq_offsets, Ti, E, k, part_p, part_f, part_z);
+                       seq_offsets, Ti, E, k, part_p, part_f, part_z, done);
     return hipGetLastError();
   });
   if (st != hipSuccess) return st;
-  hipLaunchKernelGGL(balance_reduce_kernel, dim3(blocks, n_seq), dim3(256), 0, s, part_p, part_f, part_z, parts, E,
-                     term, load);
-  if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
-  hipLaunchKernelGGL(balance_final_kernel, dim3(1), dim3(64), 0, s, term, seq_offsets, n_seq, Ti, E, k, blocks,
-                     losses);
+  hipLaunchKernelGGL(balance_reduce_kernel, dim3(blocks, n_seq), dim3(256), 0, s, part_p, part_f, part_z, parts,
+                     seq_offsets, n_seq, Ti, E, k, term, load, done, losses);
   return hipGetLastError();
 }
 
