@@ -118,12 +118,33 @@ __device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int off) {
   return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
-__device__ __forceinline__ float sigmoidf(float l) { return 1.0f / (1.0f + expf(-l)); }
-// sigmoid(l) / exp(min(m, 0)) for l <= m: no underflow where all of a row's
-// scores are tiny, since only ratios of them are used.
-__device__ __forceinline__ float sigmoid_scaled(float l, float m) {
-  return m >= 0.0f ? sigmoidf(l) : expf(l - m) / (1.0f + expf(l));
+// e^x within 2 units in the last place for x <= 88 (0 below -200, -inf and NaN
+// included): 2^t of the rounded product t = x log2 e, corrected by what the
+// product lost.
+__device__ __forceinline__ float exp_fast(float x) {
+  x = fmaxf(x, -200.0f);
+  const float t = x * 1.44269504f;
+  float r = __builtin_fmaf(x, 1.44269504f, -t);
+  r = __builtin_fmaf(x, 1.92596299e-8f, r);
+  const float p = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(p * r, 0.69314718f, p);
 }
+// 1 / d for finite d >= 1: the hardware's reciprocal and one Newton step
+__device__ __forceinline__ float recip(float d) {
+  const float r = __builtin_amdgcn_rcpf(d);
+  return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+}
+// s = sigmoid(l) and 1 - s, neither by cancellation
+struct Sig {
+  float s, n;
+};
+__device__ __forceinline__ Sig sigmoid2(float l) {
+  const float t = exp_fast(-fabsf(l)), r = recip(1.0f + t), q = t * r;
+  return l >= 0.0f ? Sig{r, q} : Sig{q, r};
+}
+// sigmoid(l) / exp(min(m, 0)) for l <= m, with u = exp(l - m): no underflow
+// where all of a row's scores are tiny, since only ratios of them are used.
+__device__ __forceinline__ float sigmoid_scaled(const Sig& g, float u, float m) { return m >= 0.0f ? g.s : u * g.n; }
 
 // lane's experts: lane * VPL + i, i < VPL (so lower lanes hold lower experts)
 template <int VPL>
@@ -166,8 +187,11 @@ struct SelectLds {
 // chosen one (mx). m, inv_z: the row's largest logit and 1 / sum exp(l - m).
 __device__ __forceinline__ float weigh(const SelectOpts& o, float v, float mx, float m, float inv_z) {
   if (!live_value(v)) return 0.0f;
-  if (o.renorm) return o.sigmoid ? sigmoid_scaled(v, mx) : expf(v - mx);
-  return o.sigmoid ? sigmoidf(v) : expf(v - m) * inv_z;
+  if (o.renorm) {
+    const float u = exp_fast(v - mx);
+    return o.sigmoid ? sigmoid_scaled(sigmoid2(v), u, mx) : u;
+  }
+  return o.sigmoid ? sigmoid2(v).s : exp_fast(v - m) * inv_z;
 }
 __device__ __forceinline__ float weight_factor(const SelectOpts& o, float tot) {
   return o.renorm ? (tot > 0.0f ? o.scale / tot : 0.0f) : o.scale;
@@ -396,11 +420,11 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
     float zs = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      c[i] = live_value(l[i]) ? expf(l[i] - m) : 0.0f;
+      c[i] = exp_fast(l[i] - m);
       zs += c[i];
     }
     zs = wave_sum(zs);
-    inv_z = zs > 0.0f ? 1.0f / zs : 0.0f;
+    inv_z = zs > 0.0f ? recip(zs) : 0.0f;  // the largest term is 1
   }
   // 1 / sum exp(l - m) in doubles, and a double key (for a live expert)
   auto exact_inv_z = [&]() -> double {
@@ -418,11 +442,15 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
   };
   // keys; -inf: out of the choice
   if constexpr (kKeyed) {
+    float bv[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) bv[i] = 0.0f;
+    if (bias) load_raw<VPL>(bias, E, 0.0f, bv);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const float b = bias && e0 + i < E ? bias[e0 + i] : 0.0f;
+      const float b = bv[i];
       const float s = o.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-l[i])) : c[i] * inv_z;
-      c[i] = live_value(l[i]) && live_value(b) ? s + b : -INFINITY;
+      c[i] = live_value(fminf(l[i], b)) && b == b ? s + b : -INFINITY;
     }
   } else {
 #pragma unroll
@@ -488,13 +516,13 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
   const float cv = order32_back(static_cast<uint32_t>(key >> 32));
   const bool live = mine && cv > -INFINITY;
   // larger candidates; in keyed form also those not clearly smaller
-  const float low = cv - margin(cv);
+  const uint32_t low = order32(cv - margin(cv));
   int rank = 0, near = 0;
 #pragma unroll 4
   for (int r = 0; r < n; ++r) {
     const uint64_t kr = sh.key[r];
     rank += kr > key;
-    if constexpr (kKeyed) near += order32_back(static_cast<uint32_t>(kr >> 32)) >= low;
+    if constexpr (kKeyed) near += static_cast<uint32_t>(kr >> 32) >= low;
   }
   if constexpr (kKeyed) {
     if (__ballot(live && rank < k && near != rank + 1)) {
@@ -589,111 +617,150 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
                                                               const int32_t* __restrict__ load,
                                                               const int32_t* __restrict__ seq_offsets, int n_seq, int T,
                                                               int E, int k, float* __restrict__ dlogits) {
+  __shared__ float slots[4][64 * VPL];  // the chosen experts' part, by expert
   const int lane = threadIdx.x & 63;
   const int e0 = lane * VPL;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); t < T; t += 4 * static_cast<int64_t>(gridDim.x)) {
-  const int64_t row = t * E;
-  float l[VPL], dl[VPL], p[VPL];
-  load_row<VPL>(logits + row, E, l);
-  float m = l[0];
-#pragma unroll
-  for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
-  m = wave_max(m);
-  float zs = 0.0f;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    p[i] = live_value(l[i]) ? expf(l[i] - m) : 0.0f;
-    zs += p[i];
-    dl[i] = 0.0f;
-  }
-  zs = wave_sum(zs);
-  const float inv_z = zs > 0.0f ? 1.0f / zs : 0.0f;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) p[i] *= inv_z;
-
-  // the selection
-  if (dw) {
-    const int64_t a0 = t * k;
-    float dsum = 0.0f;
-    for (int j = lane; j < k; j += 64) {
-      const float wj = o.sigmoid || o.renorm ? 0.0f : w[a0 + j];
-      if (wj != 0.0f) dsum += wj * dw[a0 + j];  // a slot out of the choice adds nothing, whatever its dw
+  float* slot = slots[threadIdx.x >> 6];
+  const bool need_p = dlosses || !(o.sigmoid || o.renorm);  // softmax over the row
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); t < T;
+       t += 4 * static_cast<int64_t>(gridDim.x)) {
+    const int64_t row = t * E, a0 = t * k;
+    float l[VPL], dl[VPL], u[VPL];
+    Sig g[VPL];
+    load_raw<VPL>(logits + row, E, -INFINITY, l);
+    // the first 64 slots, loaded beside the row
+    int se = -1;
+    float sw = 0.0f, sd = 0.0f;
+    if (dw && lane < k) {
+      se = idx[a0 + lane];
+      sw = w[a0 + lane];
+      sd = dw[a0 + lane];
     }
-    dsum = wave_sum(dsum);
-    const float unit = o.renorm && o.scale != 0.0f ? 1.0f / o.scale : 0.0f;
-    for (int j0 = 0; j0 < k; j0 += 64) {
-      const int j = j0 + lane;
-      int e = -1;
-      float g = 0.0f;
-      if (j < k) {
-        e = idx[a0 + j];
-        const float wj = w[a0 + j];
-        if (wj != 0.0f) g = wj * dw[a0 + j];
-        if (o.renorm) {
-          // dw_j - sum_i v_i dw_i as sum_i v_i (dw_j - dw_i), v = w / scale summing to 1: nothing cancels
-          g = 0.0f;
-          for (int i = 0; i < k; ++i) {
-            const float wi = w[a0 + i];  // the same for every lane
-            if (wi != 0.0f && wj != 0.0f) g += wi * unit * (dw[a0 + j] - dw[a0 + i]);
-          }
-          g *= wj;
-        }
-      }
-      const int n = min(64, k - j0);
-      for (int q = 0; q < n; ++q) {
-        const int eq = __builtin_amdgcn_readlane(e, q);
-        const float gq = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), q));
+    clean_row<VPL>(l);
+    float m = 0.0f, zs = 0.0f, inv_z = 0.0f;
+    if (need_p) {
+      m = l[0];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (e0 + i == eq) dl[i] += gq;
+      for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+      m = wave_max(m);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        u[i] = exp_fast(l[i] - m);
+        zs += u[i];
       }
+      zs = wave_sum(zs);
+      inv_z = zs > 0.0f ? recip(zs) : 0.0f;
     }
     if (o.sigmoid) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (dl[i] != 0.0f) dl[i] *= sigmoidf(-l[i]);
-    } else if (!o.renorm) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) dl[i] -= p[i] * dsum;
+      for (int i = 0; i < VPL; ++i) g[i] = live_value(l[i]) ? sigmoid2(l[i]) : Sig{0.0f, 0.0f};
     }
-  }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) dl[i] = 0.0f;
 
-  // the losses
-  if (dlosses) {
-    const Seq q = find_seq(seq_offsets, n_seq, static_cast<int>(t), T);
-    if (q.id >= 0 && m > -INFINITY) {
-      const float cb = static_cast<float>(static_cast<double>(dlosses[0]) * E /
-                                          (static_cast<double>(k) * q.len * q.len * q.filled));
-      float sh[VPL], tot = 0.0f, dot = 0.0f;
+    // the selection
+    if (dw) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        sh[i] = o.sigmoid ? (live_value(l[i]) ? sigmoid_scaled(l[i], m) : 0.0f) : p[i];
-        tot += sh[i];
+      for (int i = 0; i < VPL; ++i) slot[e0 + i] = 0.0f;
+      wave_lds_sync();
+      const float unit = o.renorm && o.scale != 0.0f ? 1.0f / o.scale : 0.0f;
+      float dsum = 0.0f;
+      for (int j0 = 0; j0 < k; j0 += 64) {
+        if (j0 > 0) {
+          const bool in = j0 + lane < k;
+          se = in ? idx[a0 + j0 + lane] : -1;
+          sw = in ? w[a0 + j0 + lane] : 0.0f;
+          sd = in ? dw[a0 + j0 + lane] : 0.0f;
+        }
+        // a slot of weight 0 passes nothing on, whatever its dw
+        float v = sw != 0.0f ? sw * sd : 0.0f;
+        dsum += v;
+        if (o.renorm) {
+          // dw_j - sum_i v_i dw_i as sum_i v_i (dw_j - dw_i), v = w / scale summing to 1: nothing cancels
+          float acc = 0.0f;
+          for (int i0 = 0; i0 < k; i0 += 64) {
+            const bool in = i0 + lane < k;
+            float wi = sw, di = sd;
+            if (i0 != j0) {
+              wi = in ? w[a0 + i0 + lane] : 0.0f;
+              di = in ? dw[a0 + i0 + lane] : 0.0f;
+            }
+            if (wi == 0.0f) di = 0.0f;
+            const int n = min(64, k - i0);
+            for (int q = 0; q < n; ++q) {
+              const float wq = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wi), q));
+              const float dq = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(di), q));
+              acc += wq * (sd - dq);
+            }
+          }
+          v = sw != 0.0f ? sw * (acc * unit) : 0.0f;
+        }
+        if (se >= 0 && se < E) atomicAdd(&slot[se], v);
       }
+      wave_lds_sync();
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) dl[i] = slot[e0 + i];
       if (o.sigmoid) {
-        tot = 1.0f / wave_sum(tot);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) sh[i] *= tot;
-      }
-      float g[VPL];
+        for (int i = 0; i < VPL; ++i) dl[i] *= g[i].n;
+      } else if (!o.renorm) {
+        dsum = wave_sum(dsum) * inv_z;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        g[i] = e0 + i < E ? cb * static_cast<float>(load[static_cast<int64_t>(q.id) * E + e0 + i]) : 0.0f;
-        dot += sh[i] * g[i];
-      }
-      dot = wave_sum(dot);
-      const float cz = dlosses[1] * 2.0f / static_cast<float>(q.covered) * (m + logf(zs));
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        float v = sh[i] * (g[i] - dot);
-        if (o.sigmoid && sh[i] != 0.0f) v *= sigmoidf(-l[i]);
-        dl[i] += v + cz * p[i];
+        for (int i = 0; i < VPL; ++i) dl[i] -= u[i] * dsum;
       }
     }
-  }
+
+    // the losses
+    if (dlosses) {
+      const Seq q = find_seq(seq_offsets, n_seq, static_cast<int>(t), T);
+      if (q.id >= 0 && m > -INFINITY) {
+        const float n = static_cast<float>(q.len);
+        const float cb = dlosses[0] * static_cast<float>(E) / (static_cast<float>(k) * static_cast<float>(q.filled)) / n / n;
+        float f[VPL];  // the loads' bits
+        load_raw<VPL>(reinterpret_cast<const float*>(load + static_cast<int64_t>(q.id) * E), E, 0.0f, f);
+        // shares p~, up to the factor r
+        float sh[VPL], r = inv_z;
+        if (o.sigmoid) {
+          float tot = 0.0f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    if (e0 + i < E) dlogits[row + e0 + i] = dl[i];
+          for (int i = 0; i < VPL; ++i) {
+            sh[i] = sigmoid_scaled(g[i], u[i], m);
+            tot += sh[i];
+          }
+          r = 1.0f / wave_sum(tot);
+        } else {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) sh[i] = u[i];
+        }
+        float gl[VPL], dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          sh[i] *= r;
+          gl[i] = cb * static_cast<float>(__float_as_int(f[i]));
+          dot += sh[i] * gl[i];
+        }
+        dot = wave_sum(dot);
+        const float cz = dlosses[1] * 2.0f / static_cast<float>(q.covered) * (m + logf(zs)) * inv_z;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          float v = sh[i] * (gl[i] - dot);
+          if (o.sigmoid) v *= g[i].n;
+          dl[i] += v + cz * u[i];
+        }
+      }
+    }
+    if constexpr (VPL >= 4) {
+      if (E % 4 == 0 && (reinterpret_cast<uintptr_t>(dlogits) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < VPL; i += 4)
+          if (e0 + i < E)
+            *reinterpret_cast<f32x4_t*>(dlogits + row + e0 + i) = f32x4_t{dl[i], dl[i + 1], dl[i + 2], dl[i + 3]};
+        continue;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (e0 + i < E) dlogits[row + e0 + i] = dl[i];
   }
 }
 
@@ -755,11 +822,10 @@ __global__ __launch_bounds__(256) void balance_part_kernel(SelectOpts o, const f
       zs[u] = tot[u] = 0.0f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        x[u][i] = live_value(l[u][i]) ? expf(l[u][i] - m[u]) : 0.0f;
+        x[u][i] = exp_fast(l[u][i] - m[u]);
         zs[u] += x[u][i];
         if (o.sigmoid) {
-          // sigmoid(l) / e^min(m, 0), from the same exponential where the row is not all negative
-          if (live_value(l[u][i])) x[u][i] = m[u] >= 0.0f ? sigmoidf(l[u][i]) : x[u][i] / (1.0f + expf(l[u][i]));
+          x[u][i] = live_value(l[u][i]) ? sigmoid_scaled(sigmoid2(l[u][i]), x[u][i], m[u]) : 0.0f;
           tot[u] += x[u][i];
         }
       }
@@ -845,31 +911,42 @@ __global__ __launch_bounds__(256) void balance_reduce_kernel(const float* __rest
     }
   }
   __syncthreads();
-  if (!last || threadIdx.x >= 64) return;
+  if (!last) return;
   __threadfence();
-  const volatile double* terms = term;
   double bsum = 0.0, zsum = 0.0;
   int filled = 0, covered = 0;
-  for (int q = threadIdx.x; q < n_seq; q += 64) {
+  const int64_t terms = static_cast<int64_t>(n_seq) * (blocks + 1);
+  for (int64_t x = threadIdx.x; x < terms; x += 256) {
+    const int q = static_cast<int>(x / (blocks + 1)), at = static_cast<int>(x % (blocks + 1));
     const int a = seq_offsets ? clamp_off(seq_offsets[q], T) : 0;
     const int b = seq_offsets ? clamp_off(seq_offsets[q + 1], T) : T;
     if (b <= a) continue;
+    const double v = __hip_atomic_load(term + x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const double n = b - a;
-    double v = 0.0;
-    const volatile double* row = terms + static_cast<int64_t>(q) * (blocks + 1);
-    for (int x = 0; x < blocks; ++x) v += row[x];
-    bsum += v * E / (k * n * n);
-    zsum += row[blocks];
-    filled += 1;
-    covered += b - a;
+    if (at < blocks) {
+      bsum += v * E / (k * n * n);
+    } else {
+      zsum += v;
+      filled += 1;
+      covered += b - a;
+    }
   }
+  __shared__ double sb[4], sv[4];
+  __shared__ int si[4], sc[4];
   bsum = wave_sum_any(bsum);
   zsum = wave_sum_any(zsum);
   filled = wave_sum_any(filled);
   covered = wave_sum_any(covered);
+  if ((threadIdx.x & 63) == 0) {
+    const int q = threadIdx.x >> 6;
+    sb[q] = bsum; sv[q] = zsum; si[q] = filled; sc[q] = covered;
+  }
+  __syncthreads();
   if (threadIdx.x == 0) {
-    losses[0] = filled ? static_cast<float>(bsum / filled) : 0.0f;
-    losses[1] = covered ? static_cast<float>(zsum / covered) : 0.0f;
+    filled = ((si[0] + si[1]) + si[2]) + si[3];
+    covered = ((sc[0] + sc[1]) + sc[2]) + sc[3];
+    losses[0] = filled ? static_cast<float>((((sb[0] + sb[1]) + sb[2]) + sb[3]) / filled) : 0.0f;
+    losses[1] = covered ? static_cast<float>((((sv[0] + sv[1]) + sv[2]) + sv[3]) / covered) : 0.0f;
   }
 }
 
