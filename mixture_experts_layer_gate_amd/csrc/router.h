@@ -14,6 +14,9 @@ struct SelectOpts {
   int top2;         // group key: 1 sum of its two largest keys, 0 its largest
   int renorm;       // weights divided by their sum
   float scale;      // weight factor
+  int per;          // experts per group
+  int lpg_log2;     // log2 of the wave lanes that scan one group: the most that 64 / groups allows
+  float inv_per;    // 1 / per
 };
 constexpr int kMaxGroups = 64;   // one wave lane per group
 constexpr int kMaxSeqs = 65535;  // one grid row per sequence

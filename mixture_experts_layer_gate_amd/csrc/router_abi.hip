@@ -29,6 +29,10 @@ int check_opts(const moe_dims_t* dm, const moe_route_opts_t* op, SelectOpts* o) 
   o->top2 = op->group_rule == MOE_GROUP_TOP2;
   o->renorm = op->renormalise;
   o->scale = op->scale;
+  o->per = dm->E / o->groups;
+  o->lpg_log2 = 0;
+  while ((2 << o->lpg_log2) * o->groups <= 64) ++o->lpg_log2;
+  o->inv_per = 1.0f / static_cast<float>(o->per);
   return MOE_OK;
 }
 

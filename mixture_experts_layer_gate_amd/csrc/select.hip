@@ -235,7 +235,7 @@ __device__ __forceinline__ void select_exact(const SelectOpts& o, const float* _
 #pragma unroll
     for (int i = 0; i < VPL; ++i) sh.key[e0 + i] = key[i];
     wave_lds_sync();
-    const int per = E / o.groups;
+    const int per = o.per;
     // lane g: group g's key, again as ordered bits (0: no live expert)
     uint64_t gk = 0;
     if (lane < o.groups) {
@@ -338,7 +338,7 @@ __device__ __forceinline__ uint64_t keep_groups(const SelectOpts& o, const V (&c
   wave_lds_sync();
   const auto most = [](V x, V y) { return x > y ? x : y; };
   const auto least = [](V x, V y) { return x > y ? y : x; };
-  const int g = lane / lpg, j = lane % lpg;
+  const int g = lane >> o.lpg_log2, j = lane & (lpg - 1);
   V a = -INFINITY, b = -INFINITY;
   if (g < o.groups)
     for (int e = j; e < per; e += lpg) {
@@ -458,8 +458,7 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
   }
 
   if (kKeyed && o.groups > 1) {
-    const int per = E / o.groups;
-    const int lpg = 1 << (31 - __clz(64 / o.groups));
+    const int per = o.per, lpg = 1 << o.lpg_log2;
     bool sure = true;
     uint64_t kept = keep_groups<float, VPL>(o, c, per, lpg, sh.val, sure);
     if (!sure) {
@@ -470,11 +469,10 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
         cd[i] = c[i] > -INFINITY ? exact_key(l[i], bias ? bias[e0 + i] : 0.0f, zs) : -INFINITY;
       kept = keep_groups<double, VPL>(o, cd, per, lpg, reinterpret_cast<double*>(sh.key), sure);
     }
-    const float inv_per = 1.0f / static_cast<float>(per);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int ge = static_cast<int>((static_cast<float>(e0 + i) + 0.5f) * inv_per);  // (e0 + i) / per, below 2^11
-      if (!((kept >> ((ge * lpg) & 63)) & 1)) c[i] = -INFINITY;
+      const int ge = static_cast<int>((static_cast<float>(e0 + i) + 0.5f) * o.inv_per);  // (e0 + i) / per, below 2^11
+      if (!((kept >> ((ge << o.lpg_log2) & 63)) & 1)) c[i] = -INFINITY;
     }
   }
 
@@ -558,23 +556,25 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
   return true;
 }
 
+// One wave per token (a loop over tokens would put the rare paths' constants and
+// divisions in front of every wave: 400 instructions, as many as a row takes).
 template <int VPL, bool kKeyed, bool kFast>
 __global__ __launch_bounds__(256) void select_kernel(SelectOpts o, const float* __restrict__ logits,
                                                      const float* __restrict__ bias, int T, int E, int k,
                                                      int32_t* __restrict__ idx, float* __restrict__ w) {
   __shared__ SelectLds<VPL> lds[4];
   const int wv = threadIdx.x >> 6;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wv; t < T; t += 4 * static_cast<int64_t>(gridDim.x)) {
-    const float* row = logits + t * E;
-    int32_t* ti = idx + t * k;
-    float* tw = w + t * k;
-    if constexpr (kFast) {
-      float raw[VPL];
-      load_raw<VPL>(row, E, -INFINITY, raw);
-      if (select_fast<VPL, kKeyed>(o, raw, bias, E, k, ti, tw, lds[wv])) continue;
-    }
-    select_exact<VPL>(o, row, bias, E, k, ti, tw, lds[wv]);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wv;
+  if (t >= T) return;
+  const float* row = logits + t * E;
+  int32_t* ti = idx + t * k;
+  float* tw = w + t * k;
+  if constexpr (kFast) {
+    float raw[VPL];
+    load_raw<VPL>(row, E, -INFINITY, raw);
+    if (select_fast<VPL, kKeyed>(o, raw, bias, E, k, ti, tw, lds[wv])) return;
   }
+  select_exact<VPL>(o, row, bias, E, k, ti, tw, lds[wv]);
 }
 
 // Sequence bounds of row t: its start, length, id, and the number of sequences
@@ -615,153 +615,153 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
                                                               const float* __restrict__ dw,
                                                               const float* __restrict__ dlosses,
                                                               const int32_t* __restrict__ load,
-                                                              const int32_t* __restrict__ seq_offsets, int n_seq, int T,
-                                                              int E, int k, float* __restrict__ dlogits) {
+                                                              const int32_t* __restrict__ seq_offsets, int n_seq,
+                                                              int64_t t0, int T, int E, int k,
+                                                              float* __restrict__ dlogits) {
   __shared__ float slots[4][64 * VPL];  // the chosen experts' part, by expert
   const int lane = threadIdx.x & 63;
   const int e0 = lane * VPL;
   float* slot = slots[threadIdx.x >> 6];
   const bool need_p = dlosses || !(o.sigmoid || o.renorm);  // softmax over the row
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); t < T;
-       t += 4 * static_cast<int64_t>(gridDim.x)) {
-    const int64_t row = t * E, a0 = t * k;
-    float l[VPL], dl[VPL], u[VPL];
-    Sig g[VPL];
-    load_raw<VPL>(logits + row, E, -INFINITY, l);
-    // the first 64 slots, loaded beside the row
-    int se = -1;
-    float sw = 0.0f, sd = 0.0f;
-    if (dw && lane < k) {
-      se = idx[a0 + lane];
-      sw = w[a0 + lane];
-      sd = dw[a0 + lane];
+  const int64_t t = t0 + static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;
+  const int64_t row = t * E, a0 = t * k;
+  float l[VPL], dl[VPL], u[VPL];
+  Sig g[VPL];
+  load_raw<VPL>(logits + row, E, -INFINITY, l);
+  // the first 64 slots, loaded beside the row
+  int se = -1;
+  float sw = 0.0f, sd = 0.0f;
+  if (dw && lane < k) {
+    se = idx[a0 + lane];
+    sw = w[a0 + lane];
+    sd = dw[a0 + lane];
+  }
+  clean_row<VPL>(l);
+  float m = 0.0f, zs = 0.0f, inv_z = 0.0f;
+  if (need_p) {
+    m = l[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+    m = wave_max(m);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      u[i] = exp_fast(l[i] - m);
+      zs += u[i];
     }
-    clean_row<VPL>(l);
-    float m = 0.0f, zs = 0.0f, inv_z = 0.0f;
-    if (need_p) {
-      m = l[0];
+    zs = wave_sum(zs);
+    inv_z = zs > 0.0f ? recip(zs) : 0.0f;
+  }
+  if (o.sigmoid) {
 #pragma unroll
-      for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
-      m = wave_max(m);
+    for (int i = 0; i < VPL; ++i) g[i] = live_value(l[i]) ? sigmoid2(l[i]) : Sig{0.0f, 0.0f};
+  }
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        u[i] = exp_fast(l[i] - m);
-        zs += u[i];
+  for (int i = 0; i < VPL; ++i) dl[i] = 0.0f;
+
+  // the selection
+  if (dw) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) slot[e0 + i] = 0.0f;
+    wave_lds_sync();
+    const float unit = o.renorm && o.scale != 0.0f ? 1.0f / o.scale : 0.0f;
+    float dsum = 0.0f;
+    for (int j0 = 0; j0 < k; j0 += 64) {
+      if (j0 > 0) {
+        const bool in = j0 + lane < k;
+        se = in ? idx[a0 + j0 + lane] : -1;
+        sw = in ? w[a0 + j0 + lane] : 0.0f;
+        sd = in ? dw[a0 + j0 + lane] : 0.0f;
       }
-      zs = wave_sum(zs);
-      inv_z = zs > 0.0f ? recip(zs) : 0.0f;
+      // a slot of weight 0 passes nothing on, whatever its dw
+      float v = sw != 0.0f ? sw * sd : 0.0f;
+      dsum += v;
+      if (o.renorm) {
+        // dw_j - sum_i v_i dw_i as sum_i v_i (dw_j - dw_i), v = w / scale summing to 1: nothing cancels
+        float acc = 0.0f;
+        for (int i0 = 0; i0 < k; i0 += 64) {
+          const bool in = i0 + lane < k;
+          float wi = sw, di = sd;
+          if (i0 != j0) {
+            wi = in ? w[a0 + i0 + lane] : 0.0f;
+            di = in ? dw[a0 + i0 + lane] : 0.0f;
+          }
+          if (wi == 0.0f) di = 0.0f;
+          const int n = min(64, k - i0);
+          for (int q = 0; q < n; ++q) {
+            const float wq = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wi), q));
+            const float dq = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(di), q));
+            acc += wq * (sd - dq);
+          }
+        }
+        v = sw != 0.0f ? sw * (acc * unit) : 0.0f;
+      }
+      if (se >= 0 && se < E) atomicAdd(&slot[se], v);
     }
+    wave_lds_sync();
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) dl[i] = slot[e0 + i];
     if (o.sigmoid) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) g[i] = live_value(l[i]) ? sigmoid2(l[i]) : Sig{0.0f, 0.0f};
+      for (int i = 0; i < VPL; ++i) dl[i] *= g[i].n;
+    } else if (!o.renorm) {
+      dsum = wave_sum(dsum) * inv_z;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) dl[i] -= u[i] * dsum;
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) dl[i] = 0.0f;
-
-    // the selection
-    if (dw) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) slot[e0 + i] = 0.0f;
-      wave_lds_sync();
-      const float unit = o.renorm && o.scale != 0.0f ? 1.0f / o.scale : 0.0f;
-      float dsum = 0.0f;
-      for (int j0 = 0; j0 < k; j0 += 64) {
-        if (j0 > 0) {
-          const bool in = j0 + lane < k;
-          se = in ? idx[a0 + j0 + lane] : -1;
-          sw = in ? w[a0 + j0 + lane] : 0.0f;
-          sd = in ? dw[a0 + j0 + lane] : 0.0f;
-        }
-        // a slot of weight 0 passes nothing on, whatever its dw
-        float v = sw != 0.0f ? sw * sd : 0.0f;
-        dsum += v;
-        if (o.renorm) {
-          // dw_j - sum_i v_i dw_i as sum_i v_i (dw_j - dw_i), v = w / scale summing to 1: nothing cancels
-          float acc = 0.0f;
-          for (int i0 = 0; i0 < k; i0 += 64) {
-            const bool in = i0 + lane < k;
-            float wi = sw, di = sd;
-            if (i0 != j0) {
-              wi = in ? w[a0 + i0 + lane] : 0.0f;
-              di = in ? dw[a0 + i0 + lane] : 0.0f;
-            }
-            if (wi == 0.0f) di = 0.0f;
-            const int n = min(64, k - i0);
-            for (int q = 0; q < n; ++q) {
-              const float wq = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wi), q));
-              const float dq = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(di), q));
-              acc += wq * (sd - dq);
-            }
-          }
-          v = sw != 0.0f ? sw * (acc * unit) : 0.0f;
-        }
-        if (se >= 0 && se < E) atomicAdd(&slot[se], v);
-      }
-      wave_lds_sync();
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) dl[i] = slot[e0 + i];
-      if (o.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) dl[i] *= g[i].n;
-      } else if (!o.renorm) {
-        dsum = wave_sum(dsum) * inv_z;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) dl[i] -= u[i] * dsum;
-      }
-    }
-
-    // the losses
-    if (dlosses) {
-      const Seq q = find_seq(seq_offsets, n_seq, static_cast<int>(t), T);
-      if (q.id >= 0 && m > -INFINITY) {
-        const float n = static_cast<float>(q.len);
-        const float cb = dlosses[0] * static_cast<float>(E) / (static_cast<float>(k) * static_cast<float>(q.filled)) / n / n;
-        float f[VPL];  // the loads' bits
-        load_raw<VPL>(reinterpret_cast<const float*>(load + static_cast<int64_t>(q.id) * E), E, 0.0f, f);
-        // shares p~, up to the factor r
-        float sh[VPL], r = inv_z;
-        if (o.sigmoid) {
-          float tot = 0.0f;
-#pragma unroll
-          for (int i = 0; i < VPL; ++i) {
-            sh[i] = sigmoid_scaled(g[i], u[i], m);
-            tot += sh[i];
-          }
-          r = 1.0f / wave_sum(tot);
-        } else {
-#pragma unroll
-          for (int i = 0; i < VPL; ++i) sh[i] = u[i];
-        }
-        float gl[VPL], dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          sh[i] *= r;
-          gl[i] = cb * static_cast<float>(__float_as_int(f[i]));
-          dot += sh[i] * gl[i];
-        }
-        dot = wave_sum(dot);
-        const float cz = dlosses[1] * 2.0f / static_cast<float>(q.covered) * (m + logf(zs)) * inv_z;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          float v = sh[i] * (gl[i] - dot);
-          if (o.sigmoid) v *= g[i].n;
-          dl[i] += v + cz * u[i];
-        }
-      }
-    }
-    if constexpr (VPL >= 4) {
-      if (E % 4 == 0 && (reinterpret_cast<uintptr_t>(dlogits) & 15) == 0) {
-#pragma unroll
-        for (int i = 0; i < VPL; i += 4)
-          if (e0 + i < E)
-            *reinterpret_cast<f32x4_t*>(dlogits + row + e0 + i) = f32x4_t{dl[i], dl[i + 1], dl[i + 2], dl[i + 3]};
-        continue;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (e0 + i < E) dlogits[row + e0 + i] = dl[i];
   }
+
+  // the losses
+  if (dlosses) {
+    const Seq q = find_seq(seq_offsets, n_seq, static_cast<int>(t), T);
+    if (q.id >= 0 && m > -INFINITY) {
+      const float n = static_cast<float>(q.len);
+      const float cb = dlosses[0] * static_cast<float>(E) / (static_cast<float>(k) * static_cast<float>(q.filled)) / n / n;
+      float f[VPL];  // the loads' bits
+      load_raw<VPL>(reinterpret_cast<const float*>(load + static_cast<int64_t>(q.id) * E), E, 0.0f, f);
+      // shares p~, up to the factor r
+      float sh[VPL], r = inv_z;
+      if (o.sigmoid) {
+        float tot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          sh[i] = sigmoid_scaled(g[i], u[i], m);
+          tot += sh[i];
+        }
+        r = 1.0f / wave_sum(tot);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) sh[i] = u[i];
+      }
+      float gl[VPL], dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        sh[i] *= r;
+        gl[i] = cb * static_cast<float>(__float_as_int(f[i]));
+        dot += sh[i] * gl[i];
+      }
+      dot = wave_sum(dot);
+      const float cz = dlosses[1] * 2.0f / static_cast<float>(q.covered) * (m + logf(zs)) * inv_z;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        float v = sh[i] * (gl[i] - dot);
+        if (o.sigmoid) v *= g[i].n;
+        dl[i] += v + cz * u[i];
+      }
+    }
+  }
+  if constexpr (VPL >= 4) {
+    if (E % 4 == 0 && (reinterpret_cast<uintptr_t>(dlogits) & 15) == 0) {
+#pragma unroll
+      for (int i = 0; i < VPL; i += 4)
+        if (e0 + i < E)
+          *reinterpret_cast<f32x4_t*>(dlogits + row + e0 + i) = f32x4_t{dl[i], dl[i + 1], dl[i + 2], dl[i + 3]};
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (e0 + i < E) dlogits[row + e0 + i] = dl[i];
 }
 
 // ---------------------------------------------------------------- losses ----
@@ -951,11 +951,19 @@ __global__ __launch_bounds__(256) void balance_reduce_kernel(const float* __rest
 }
 
 // VPL: experts per lane, the least power of two that covers E with 64 lanes.
-// Workgroups of a launch over tokens: more rows than this are walked in strides
-// (a launch holds fewer than 2^32 threads).
-constexpr int64_t kMaxGrid = int64_t(1) << 20;
-unsigned token_grid(int64_t n) { return static_cast<unsigned>(n < kMaxGrid ? n : kMaxGrid); }
+// Tokens of one launch (it holds fewer than 2^32 threads, 64 to a token); a
+// larger batch takes several.
+constexpr int64_t kLaunchTokens = int64_t(1) << 25;
+template <typename F>
+hipError_t by_tokens(int64_t T, F&& f) {
+  for (int64_t t0 = 0; t0 < T; t0 += kLaunchTokens) {
+    const int64_t n = T - t0 < kLaunchTokens ? T - t0 : kLaunchTokens;
+    if (const hipError_t st = f(t0, static_cast<int>(n)); st != hipSuccess) return st;
+  }
+  return hipSuccess;
+}
 
+// VPL: experts per lane, the least power of two that covers E with 64 lanes.
 template <typename F>
 hipError_t by_width(int E, F&& f) {
   if (E <= 64) return f(std::integral_constant<int, 1>{});
@@ -969,20 +977,21 @@ hipError_t by_width(int E, F&& f) {
 
 hipError_t launch_select(const SelectOpts& o, const float* logits, const float* balance_bias, int64_t T, int E, int k,
                          int32_t* idx, float* w, hipStream_t s) {
-  const dim3 grid(token_grid((T + 3) / 4));
-  const int Ti = static_cast<int>(T);
-  return by_width(E, [&](auto v) {
-    constexpr int VPL = decltype(v)::value;
-    if (k > kFastK)
-      hipLaunchKernelGGL((select_kernel<VPL, true, false>), grid, dim3(256), 0, s, o, logits, balance_bias, Ti, E, k,
-                         idx, w);
-    else if (balance_bias || o.groups > 1)
-      hipLaunchKernelGGL((select_kernel<VPL, true, true>), grid, dim3(256), 0, s, o, logits, balance_bias, Ti, E, k,
-                         idx, w);
-    else
-      hipLaunchKernelGGL((select_kernel<VPL, false, true>), grid, dim3(256), 0, s, o, logits, balance_bias, Ti, E, k,
-                         idx, w);
-    return hipGetLastError();
+  return by_tokens(T, [&](int64_t t0, int n) {
+    const dim3 grid((n + 3) / 4);
+    const float* l = logits + t0 * E;
+    int32_t* ti = idx + t0 * k;
+    float* tw = w + t0 * k;
+    return by_width(E, [&](auto v) {
+      constexpr int VPL = decltype(v)::value;
+      if (k > kFastK)
+        hipLaunchKernelGGL((select_kernel<VPL, true, false>), grid, dim3(256), 0, s, o, l, balance_bias, n, E, k, ti, tw);
+      else if (balance_bias || o.groups > 1)
+        hipLaunchKernelGGL((select_kernel<VPL, true, true>), grid, dim3(256), 0, s, o, l, balance_bias, n, E, k, ti, tw);
+      else
+        hipLaunchKernelGGL((select_kernel<VPL, false, true>), grid, dim3(256), 0, s, o, l, balance_bias, n, E, k, ti, tw);
+      return hipGetLastError();
+    });
   });
 }
 
@@ -990,11 +999,12 @@ hipError_t launch_select_backward(const SelectOpts& o, const float* logits, cons
                                   const float* dw, const float* dlosses, const int32_t* load,
                                   const int32_t* seq_offsets, int n_seq, int64_t T, int E, int k, float* dlogits,
                                   hipStream_t s) {
-  return by_width(E, [&](auto v) {
-    hipLaunchKernelGGL((select_backward_kernel<decltype(v)::value>), dim3(token_grid((T + 3) / 4)),
-                       dim3(256), 0, s, o, logits, idx, w, dw, dlosses, load, seq_offsets, n_seq, static_cast<int>(T),
-                       E, k, dlogits);
-    return hipGetLastError();
+  return by_tokens(T, [&](int64_t t0, int n) {
+    return by_width(E, [&](auto v) {
+      hipLaunchKernelGGL((select_backward_kernel<decltype(v)::value>), dim3((n + 3) / 4), dim3(256), 0, s, o, logits,
+                         idx, w, dw, dlosses, load, seq_offsets, n_seq, t0, static_cast<int>(T), E, k, dlogits);
+      return hipGetLastError();
+    });
   });
 }
 
