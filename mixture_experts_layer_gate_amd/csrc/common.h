@@ -38,6 +38,40 @@ template <> struct Elt<1> {  // bf16
   static constexpr int kBytes = 2;
 };
 
+// ---------------- LDS-staged matrix products ----------------
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0),
+                                           static_cast<int>(bytes), 0x00020000);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+}
+
+// Every LDS read of this wave has returned (lgkmcnt 0; vmcnt and expcnt left alone).
+__device__ __forceinline__ void wait_lds_reads() { __builtin_amdgcn_s_waitcnt(0xC07F); }
+
+// Workgroup barrier without the memory fence __syncthreads() carries: that fence
+// makes the compiler wait for every outstanding load, including the LDS stages
+// still being prefetched. LDS readiness is handled by explicit vmcnt waits
+// before the barrier; the empty asm keeps the compiler from moving memory
+// operations across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Swizzle of the 16-byte chunks of row k of a [K][256] bf16 LDS stage: chunk c
+// of row k sits in slot c ^ f(k). The transposing reads of a B fragment touch
+// 16 rows k = 8g + 4h + i (g, i in 0..3) at the same columns; f spreads every
+// half-wave over all 64 banks.
+__device__ __forceinline__ int kn_swz(int k) { return (k % 4) * 4 + (k / 4) % 4; }
+
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+
 __device__ __forceinline__ float silu_mul(float g, float u) {
   // SiLU(g) * u = g / (1 + exp(-g)) * u
   return g / (1.0f + __expf(-g)) * u;

@@ -346,11 +346,6 @@ __global__ __launch_bounds__(kThreads, kDtype == 1 ? 2 : 1) void grouped_gemm_ke
 // Per-tile buffer descriptors give 32-bit row offsets, keep the K advance in
 // the scalar offset, and return zeros outside the tensor (num_records).
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0),
-                                           static_cast<int>(bytes), 0x00020000);
-}
-
 // Scheduling pattern for M MFMAs, R LDS reads and V global loads in one basic
 // block: max(M, R) groups, MFMAs and reads each spread evenly over them, the
 // loads spread over the first VG groups, MFMAs first in every group.
@@ -365,26 +360,6 @@ __device__ __forceinline__ void interleave_mfma_ds_vmem(std::integer_sequence<in
   ((sched_group<0x008, ((I + 1) * M) / G - (I * M) / G>(), sched_group<0x100, ((I + 1) * R) / G - (I * R) / G>(),
     sched_group<0x020, (I < VG ? ((I + 1) * V) / VG - (I * V) / VG : 0)>()),
    ...);
-}
-
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
-}
-
-// Every LDS read of this wave has returned (lgkmcnt 0; vmcnt and expcnt left alone).
-__device__ __forceinline__ void wait_lds_reads() { __builtin_amdgcn_s_waitcnt(0xC07F); }
-
-// Workgroup barrier without the memory fence __syncthreads() carries: that fence
-// makes the compiler wait for every outstanding load, including the LDS stages
-// still being prefetched. LDS readiness is handled by explicit vmcnt waits
-// before the barrier; the empty asm keeps the compiler from moving memory
-// operations across it.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_barrier" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
 }
 
 // What a large-tile launch computes. Every form is C = A B^T over 64-wide K
@@ -403,14 +378,6 @@ __host__ __device__ constexpr bool mode_gather(int m) { return m == kModeFc1 || 
 __host__ __device__ constexpr bool mode_f32_out(int m) { return m >= kModeBwdQ; }
 // B stored [K][N] (rows N-contiguous): the weights read by the backward's DGrad
 __host__ __device__ constexpr bool mode_b_kn(int m) { return m == kModeBwdQ || m == kModeBwdDx; }
-
-// Swizzle of the 16-byte chunks of row k of a [K][256] bf16 LDS stage: chunk c
-// of row k sits in slot c ^ f(k). The transposing reads of a B fragment touch
-// 16 rows k = 8g + 4h + i (g, i in 0..3) at the same columns; f spreads every
-// half-wave over all 64 banks.
-__device__ __forceinline__ int kn_swz(int k) { return (k % 4) * 4 + (k / 4) % 4; }
-
-typedef short i16x4_t __attribute__((ext_vector_type(4)));
 
 // One tile of a large-tile GEMM form (the kernel's loop body): tile index ->
 // (m-block, n-block), operand descriptors, the pipelined K loop and the

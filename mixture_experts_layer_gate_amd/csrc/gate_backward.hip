@@ -10,9 +10,13 @@
 // fp32. dx is a bf16 result and takes the first two: what it drops is below
 // 2^-16 of each term, where its final rounding is up to 2^-8 of the sum.
 //
-// dWg sums over tokens, and both its operands are stored with the token as the
-// slow index; the fragments' eight consecutive tokens per lane come from
-// transposing LDS reads (ds_read_b64_tr_b16), as Wg's do in dx.
+// dWg sums over tokens, and both its operands come with the token as the slow
+// index: the planes are written transposed as well, and x's fragments (eight
+// consecutive tokens per lane) come from transposing LDS reads
+// (ds_read_b64_tr_b16), as Wg's do in dx. Those reads are written as assembly
+// that waits for its own results: for the builtin the compiler waits until no
+// load into LDS is in flight, which takes the loads' lead away (dWg 73 us at
+// 4096 x 7168 x 256 where this form takes TIME_DWG).
 #include "common.h"
 #include "router.h"
 
@@ -20,158 +24,265 @@ namespace moe {
 
 namespace {
 
-typedef short i16x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) char lds_char;
-
-constexpr int kStep = 32;   // K per step (one MFMA)
-constexpr int kCols = 128;  // output columns per workgroup
-constexpr int kRowsX = 128; // tokens per dx workgroup
+constexpr int kStep = 32;    // K per step (one MFMA)
+constexpr int kRowsX = 128;  // tokens per dx workgroup
+constexpr int kColsX = 128;  // columns per dx workgroup
 
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
-// experts per dWg workgroup
-int dwg_rows(int E) { return E <= 64 ? 32 : 128; }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t bytes) {
-  const uint32_t n = bytes <= 0 ? 0u : (bytes > 0xfffffff0ll ? 0xfffffff0u : static_cast<uint32_t>(bytes));
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0), static_cast<int>(n),
-                                           0x00020000);
+  return make_rsrc(base, bytes <= 0 ? 0u : (bytes > 0xfffffff0ll ? 0xfffffff0u : static_cast<uint32_t>(bytes)));
 }
 // 64 lanes x 16 bytes into LDS at dst (wave-uniform), lane order; zeros past the descriptor's end
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, char* dst, uint32_t off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(dst), 16, off, 0, 0, 0);
 }
 
-// Slot of 16-byte chunk c of row k, for transposing reads (rows of 256 or 64
-// bytes): each half-wave of a read then touches all 64 banks once.
+// Four fragments of 16 columns (col0, col0 + 16, ..) x 32 rows of a [32][CPR * 8]
+// bf16 tile whose 16-byte chunk c of row k sits in slot c ^ kn_swz(k): lane l
+// gets column l % 16, rows 8 (l / 16) .. + 7 of each. `at` holds the lane's byte
+// offsets inside the tile (fixed through the K loop).
 template <int CPR>
-__device__ __forceinline__ int tr_swz(int k) {
-  return CPR == 16 ? (k % 4) * 4 + (k / 4) % 4 : ((k / 8) & 1) * 2;
-}
-// Fragment of 16 columns (from column col0) x 32 rows of a [32][CPR * 8] bf16
-// tile: lane l gets column col0 + l % 16, rows 8 (l / 16) .. + 7.
-template <int CPR>
-__device__ __forceinline__ bf16x8_t frag_tr(const char* tile, int col0) {
+__device__ __forceinline__ void tr_offsets(int col0, uint32_t (&at)[8]) {
+  static_assert(CPR == 16 || CPR == 32, "rows of 256 or 512 bytes");
   const int lane = threadIdx.x & 63;
-  const int c = col0 / 8 + (lane % 4) / 2;
-  i16x4_t half[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int k = 8 * (lane / 16) + 4 * h + (lane % 16) / 4;
-    const char* p = tile + k * (CPR * 16) + (c ^ tr_swz<CPR>(k)) * 16 + (lane % 2) * 8;
-    half[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(p));
-  }
-  return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
-}
-
-// dl -> planes [3][Tp][Ep] (zero past T and E) and column sums of 16-row blocks.
-constexpr int kSplitRows = 16;
-__global__ __launch_bounds__(256) void split_kernel(const float* __restrict__ dl, int64_t T, int E, int64_t Tp, int Ep,
-                                                    bf16_t* __restrict__ planes, float* __restrict__ bpart) {
-  const int64_t plane = Tp * Ep;
-  for (int64_t blk = blockIdx.x; blk < Tp / kSplitRows; blk += gridDim.x)
-    for (int e = threadIdx.x; e < Ep; e += 256) {
-      float v[kSplitRows], sum = 0.0f;
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int r = 0; r < kSplitRows; ++r) {
-        const int64_t t = blk * kSplitRows + r;
-        v[r] = t < T && e < E ? dl[t * E + e] : 0.0f;
-      }
-#pragma unroll
-      for (int r = 0; r < kSplitRows; ++r) {
-        const int64_t at = (blk * kSplitRows + r) * Ep + e;
-        // hi by truncation: never past the largest finite value, exact remainder
-        const uint32_t hb = __float_as_uint(v[r]) & 0xffff0000u;
-        const bool fin = (hb & 0x7f800000u) != 0x7f800000u;
-        const float r1 = fin ? v[r] - __uint_as_float(hb) : 0.0f;
-        const uint32_t mb = __float_as_uint(r1) & 0xffff0000u;
-        const float r2 = r1 - __uint_as_float(mb);
-        // a NaN keeps a set mantissa bit
-        const uint32_t h16 = (hb >> 16) | (v[r] != v[r] ? 0x40u : 0u);
-        planes[at] = static_cast<bf16_t>(h16);
-        planes[plane + at] = static_cast<bf16_t>(mb >> 16);
-        planes[2 * plane + at] = static_cast<bf16_t>(f32_to_bf16_bits(r2));
-        sum += v[r];
-      }
-      if (e < E) bpart[blk * E + e] = sum;
+    for (int h = 0; h < 2; ++h) {
+      const int c = (col0 + i * 16) / 8 + (lane % 4) / 2;
+      const int k = 8 * (lane / 16) + 4 * h + (lane % 16) / 4;
+      at[2 * i + h] = static_cast<uint32_t>(k * (CPR * 16) + ((c ^ kn_swz(k)) % CPR) * 16 + (lane % 2) * 8);
     }
 }
+__device__ __forceinline__ void tr_read(const char* tile, const uint32_t (&at)[8], bf16x8_t (&frag)[4]) {
+  const uint32_t base =
+      static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)(tile)));
+  i16x4_t r[8];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8\n\t"
+      "ds_read_b64_tr_b16 %1, %9\n\t"
+      "ds_read_b64_tr_b16 %2, %10\n\t"
+      "ds_read_b64_tr_b16 %3, %11\n\t"
+      "ds_read_b64_tr_b16 %4, %12\n\t"
+      "ds_read_b64_tr_b16 %5, %13\n\t"
+      "ds_read_b64_tr_b16 %6, %14\n\t"
+      "ds_read_b64_tr_b16 %7, %15\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]), "=&v"(r[7])
+      : "v"(base + at[0]), "v"(base + at[1]), "v"(base + at[2]), "v"(base + at[3]), "v"(base + at[4]),
+        "v"(base + at[5]), "v"(base + at[6]), "v"(base + at[7])
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    frag[i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(r[2 * i], r[2 * i + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+// Rows of 64 bytes (32 K values): chunk c of row r in slot c ^ (r / 4) % 4, so
+// that 16 rows' reads of one chunk touch all banks.
+__device__ __forceinline__ int row_swz(int r) { return (r / 4) % 4; }
+__device__ __forceinline__ bf16x8_t row_frag(const char* tile, int row0) {
+  const int lane = threadIdx.x & 63, r = row0 + lane % 16;
+  return *reinterpret_cast<const bf16x8_t*>(tile + r * (kStep * 2) + ((lane / 16) ^ row_swz(r)) * 16);
+}
 
-// One BM-expert x 128-column tile of part blockIdx.z of the tokens.
-template <int BM>
-__global__ __launch_bounds__(256) void dwg_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ planes,
-                                                  int64_t T, int64_t d, int E, int64_t Tp, int Ep, int64_t steps,
-                                                  float* __restrict__ out) {
-  constexpr int ACPR = BM / 8;                // 16-byte chunks per plane row
-  constexpr int kA = 3 * kStep * BM * 2, kB = kStep * kCols * 2, kStage = kA + kB;
-  constexpr int AI = kA / 1024, LI = kStage / 1024;  // load instructions of a stage: the planes', all
-  constexpr int WM = BM == 128 ? 2 : 1, WN = 4 / WM;
-  constexpr int MI = BM / WM / 16, NJ = kCols / WN / 16;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+// acc[i][j] += b[i] x (row fragment j), summed over the planes, the smallest
+// first; a plane's fragments are read while the one before it multiplies.
+template <int kPlanes>
+__device__ __forceinline__ void plane_products(const char* tile, int plane_bytes, int row0, const bf16x8_t (&b)[4],
+                                               f32x4_t (&acc)[4][4]) {
+  bf16x8_t a[2][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) a[0][j] = row_frag(tile + (kPlanes - 1) * plane_bytes, row0 + j * 16);
+#pragma unroll
+  for (int p = 0; p < kPlanes; ++p) {
+    if (p + 1 < kPlanes) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[(p + 1) & 1][j] = row_frag(tile + (kPlanes - 2 - p) * plane_bytes, row0 + j * 16);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i], a[p & 1][j], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// Tile of workgroup `id` of n: consecutive tiles on one XCD (workgroup id runs
+// on XCD id mod 8), so that tiles sharing an operand share an L2.
+__device__ __forceinline__ int xcd_tile(int id, int n) {
+  const int per = n / 8;
+  return id < 8 * per ? (id % 8) * per + id / 8 : id;
+}
+
+// One pipelined K loop: `issue(step, buffer)` starts a step's loads (PER of them
+// per wave) into one of NST stage buffers, `work(buffer)` multiplies it. The
+// loads run NST - 1 steps ahead; a step's own are the oldest in flight.
+template <int NST, int PER, int kStage, typename Issue, typename Work>
+__device__ __forceinline__ void pipeline(int steps, char* lds, Issue&& issue, Work&& work) {
+#pragma unroll
+  for (int p = 0; p < NST - 1; ++p)
+    if (p < steps) issue(p, lds + p * kStage);
+  int buf = 0, ahead = NST - 1;
+  for (int st = 0; st < steps; ++st) {
+    if (st + NST - 2 < steps)
+      wait_vmcnt<(NST - 2) * PER>();
+    else
+      wait_vmcnt<0>();
+    wait_lds_reads();  // of the step before: its buffer is refilled below
+    lds_barrier();
+    if (st + NST - 1 < steps) issue(st + NST - 1, lds + ahead * kStage);
+    work(lds + buf * kStage);
+    buf = buf + 1 == NST ? 0 : buf + 1;
+    ahead = ahead + 1 == NST ? 0 : ahead + 1;
+  }
+}
+
+// One 64-token x 64-expert block: dl -> rows [2][Tp][Ep] (hi, mid: dx's operand)
+// and cols [3][Ep][Tp] (all planes, transposed through LDS: dWg's), zero past T
+// and E, and the block's column sums.
+constexpr int kBlk = 64;
+__global__ __launch_bounds__(256) void split_kernel(const float* __restrict__ dl, int64_t T, int E, int64_t Tp, int Ep,
+                                                    bf16_t* __restrict__ rows, bf16_t* __restrict__ cols,
+                                                    float* __restrict__ bpart) {
+  constexpr int kPitch = kBlk + 8;
+  __shared__ __attribute__((aligned(16))) bf16_t tr[3][kBlk * kPitch];
+  __shared__ float part[16][kBlk];
+  const int64_t tb = static_cast<int64_t>(blockIdx.y) * kBlk;
+  const int eb = blockIdx.x * kBlk;
+  const int cg = (threadIdx.x % 16) * 4, rg = (threadIdx.x / 16) * 4;  // 4 rows x 4 columns of the block
+  const bool vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(dl) & 15) == 0;
+  const int e = eb + cg;
+  float v[4][4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int64_t t = tb + rg + r;
+    if (vec) {
+      const f32x4_t u = t < T && e < E ? *reinterpret_cast<const f32x4_t*>(dl + t * E + e) : f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[r][c] = u[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[r][c] = t < T && e + c < E ? dl[t * E + e + c] : 0.0f;
+    }
+  }
+  uint32_t p[3][4][4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      // hi by truncation: never past the largest finite value, exact remainder
+      const uint32_t hb = __float_as_uint(v[r][c]) & 0xffff0000u;
+      const bool fin = (hb & 0x7f800000u) != 0x7f800000u;
+      const float r1 = fin ? v[r][c] - __uint_as_float(hb) : 0.0f;
+      const uint32_t mb = __float_as_uint(r1) & 0xffff0000u;
+      p[0][r][c] = (hb >> 16) | (v[r][c] != v[r][c] ? 0x40u : 0u);  // a NaN keeps a set mantissa bit
+      p[1][r][c] = mb >> 16;
+      p[2][r][c] = f32_to_bf16_bits(r1 - __uint_as_float(mb));
+    }
+#pragma unroll
+  for (int pl = 0; pl < 2; ++pl)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<uint2*>(rows + (pl * Tp + tb + rg + r) * Ep + e) =
+          make_uint2(p[pl][r][0] | (p[pl][r][1] << 16), p[pl][r][2] | (p[pl][r][3] << 16));
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+#pragma unroll
+    for (int pl = 0; pl < 3; ++pl)
+      *reinterpret_cast<uint2*>(&tr[pl][(cg + c) * kPitch + rg]) =
+          make_uint2(p[pl][0][c] | (p[pl][1][c] << 16), p[pl][2][c] | (p[pl][3][c] << 16));
+    part[threadIdx.x / 16][cg + c] = ((v[0][c] + v[1][c]) + v[2][c]) + v[3][c];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int pl = 0; pl < 3; ++pl)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int r = q * 32 + threadIdx.x / 8, c = (threadIdx.x % 8) * 8;
+      *reinterpret_cast<u32x4_t*>(cols + (static_cast<int64_t>(pl) * Ep + eb + r) * Tp + tb + c) =
+          *reinterpret_cast<const u32x4_t*>(&tr[pl][r * kPitch + c]);
+    }
+  if (threadIdx.x < kBlk && eb + static_cast<int>(threadIdx.x) < E) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) sum += part[q][threadIdx.x];
+    bpart[static_cast<int64_t>(blockIdx.y) * E + eb + threadIdx.x] = sum;
+  }
+}
+
+// A BM-expert x BN-column tile of one part of the tokens: out[part][e][n].
+// WM x WN waves, each 64 experts x 64 columns.
+template <int BM, int BN, int NST>
+__global__ __launch_bounds__(BM / 64 * (BN / 64) * 64, 1) void dwg_kernel(const bf16_t* __restrict__ x,
+                                                                       const bf16_t* __restrict__ cols, int64_t T,
+                                                                       int64_t d, int E, int64_t Tp, int Ep,
+                                                                       int steps, int etiles, int parts,
+                                                                       float* __restrict__ out) {
+  constexpr int WN = BN / 64, NW = BM / 64 * WN;
+  constexpr int BCPR = BN / 8;  // 16-byte chunks of a stage row of x
+  constexpr int kPlane = kStep * BM * 2, kA = 3 * kPlane, kB = kStep * BN * 2, kStage = kA + kB;
+  constexpr int AI = kA / 1024 / NW, BI = kB / 1024 / NW, PER = AI + BI;  // load instructions of a wave
+  static_assert(AI * NW * 1024 == kA && BI * NW * 1024 == kB, "every wave loads as much");
+  __shared__ __attribute__((aligned(1024))) char lds[NST * kStage];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv / WN, wn = wv % WN;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kCols;
-  const int e0 = blockIdx.y * BM;
-  const int64_t s0 = steps * blockIdx.z / gridDim.z, s1 = steps * (blockIdx.z + 1) / gridDim.z;
+  // expert tiles of one column block next to each other: they read the same x
+  const int tile = xcd_tile(blockIdx.x, gridDim.x);
+  const int e0 = tile % etiles * BM;
+  const int part = tile / etiles % parts;
+  const int64_t n0 = static_cast<int64_t>(tile / etiles / parts) * BN;
+  // the first steps % parts parts take one step more
+  const int s0 = part * (steps / parts) + min(part, steps % parts);
+  const int n_steps = steps / parts + (part < steps % parts);
 
-  auto issue = [&](int64_t st, char* dst) {
-    const int64_t t = st * kStep;
+  auto issue = [&](int st, char* dst) {
+    const int64_t t = static_cast<int64_t>(s0 + st) * kStep;
     const __amdgpu_buffer_rsrc_t rx = rsrc(x + t * d + n0, ((T - t) * d - n0) * 2);
 #pragma unroll
-    for (int q0 = 0; q0 < LI; q0 += 4) {
-      const int q = q0 + wv;  // wave-uniform
-      if (q < AI) {
-        constexpr int RPI = 64 / ACPR;  // plane rows per instruction
-        const int r = (q * RPI) % kStep + lane / ACPR;
-        const int c = (lane % ACPR) ^ tr_swz<ACPR>(r);
-        const bf16_t* base = planes + (static_cast<int64_t>((q * RPI) / kStep) * Tp + t) * Ep + e0;
-        load_lds16(rsrc(base, (static_cast<int64_t>(kStep) * Ep) * 2), dst + q * 1024,
-                   static_cast<uint32_t>((r * Ep + c * 8) * 2));
-      } else if (q < LI) {
-        const int r = (q - AI) * 4 + lane / 16, c = (lane % 16) ^ tr_swz<16>(r);
-        load_lds16(rx, dst + q * 1024, static_cast<uint32_t>(r * d * 2 + c * 16));
-      }
+    for (int i = 0; i < AI; ++i) {
+      constexpr int IPP = BM / 16;  // instructions per plane, 16 rows of 64 bytes each
+      const int q = wv * AI + i, pl = q / IPP, r = (q % IPP) * 16 + lane / 4;
+      const bf16_t* base = cols + (static_cast<int64_t>(pl) * Ep + e0) * Tp + t;
+      load_lds16(rsrc(base, (static_cast<int64_t>(BM) * Tp - t) * 2), dst + q * 1024,
+                 static_cast<uint32_t>(r * Tp * 2 + ((lane % 4) ^ row_swz(r)) * 16));
+    }
+#pragma unroll
+    for (int i = 0; i < BI; ++i) {
+      constexpr int RPI = 64 / BCPR;
+      const int q = wv * BI + i;
+      const int r = q * RPI + lane / BCPR, c = ((lane % BCPR) ^ kn_swz(r)) % BCPR;
+      load_lds16(rx, dst + kA + q * 1024, static_cast<uint32_t>(r * d * 2 + c * 16));
     }
   };
-
-  f32x4_t acc[MI][NJ];
+  f32x4_t acc[4][4];  // [column block][expert block]
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  if (s0 < s1) issue(s0, lds);
-  for (int64_t st = s0; st < s1; ++st) {
-    char* cur = lds + ((st - s0) & 1) * kStage;
-    char* nxt = lds + ((st - s0 + 1) & 1) * kStage;
-    __syncthreads();  // stage st has landed for every wave, and every wave has read stage st - 1 out
-    if (st + 1 < s1) issue(st + 1, nxt);
-    bf16x8_t b[NJ];
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  uint32_t at[8];
+  tr_offsets<BCPR>(wn * 64, at);
+  pipeline<NST, PER, kStage>(n_steps, lds, issue, [&](const char* cur) {
+    bf16x8_t b[4];
+    tr_read(cur + kA, at, b);
+    plane_products<3>(cur, kPlane, wm * 64, b, acc);
+  });
+  // accumulator of lane l: columns 4 (l / 16) .. + 3 of expert l % 16
+  float* o = out + static_cast<int64_t>(part) * E * d;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) b[j] = frag_tr<16>(cur + kA, wn * (NJ * 16) + j * 16);
+  for (int j = 0; j < 4; ++j) {
+    const int e = e0 + wm * 64 + j * 16 + lane % 16;
+    if (e >= E) continue;
 #pragma unroll
-    for (int pl = 2; pl >= 0; --pl)
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const bf16x8_t a = frag_tr<ACPR>(cur + pl * (kStep * BM * 2), wm * (MI * 16) + i * 16);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[j], acc[i][j], 0, 0, 0);
-      }
-  }
-  float* o = out + static_cast<int64_t>(blockIdx.z) * E * d;
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int e = e0 + wm * (MI * 16) + i * 16 + 4 * (lane / 16) + v;
-      if (e >= E) continue;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int64_t n = n0 + wn * (NJ * 16) + j * 16 + lane % 16;
-        if (n < d) o[e * d + n] = acc[i][j][v];
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int64_t n = n0 + wn * 64 + i * 16 + 4 * (lane / 16);
+      if (n < d) *reinterpret_cast<f32x4_t*>(o + e * d + n) = acc[i][j];
     }
+  }
 }
 
-// Parts summed in order (parts > 0), and dbias from the 16-row blocks' sums.
+// Parts summed in order (parts > 1), and dbias from the 64-row blocks' sums.
 __global__ __launch_bounds__(256) void dwg_sum_kernel(const float* __restrict__ part, int parts, int64_t n4,
                                                       float* __restrict__ dwg, const float* __restrict__ bpart,
                                                       int64_t blocks, int E, float* __restrict__ dbias,
@@ -203,85 +314,87 @@ __global__ __launch_bounds__(256) void dwg_sum_kernel(const float* __restrict__ 
 }
 
 // One 128-token x 128-column tile of dx: K = the experts, planes hi and mid.
-__global__ __launch_bounds__(256) void gate_dx_kernel(const bf16_t* __restrict__ planes, const bf16_t* __restrict__ wg,
+template <int NST>
+__global__ __launch_bounds__(256) void gate_dx_kernel(const bf16_t* __restrict__ rows, const bf16_t* __restrict__ wg,
                                                       const bf16_t* dx_in, int64_t T, int64_t d, int E, int64_t Tp,
                                                       int Ep, bf16_t* dx) {
-  constexpr int kA = 2 * kRowsX * kStep * 2, kB = kStep * kCols * 2, kStage = kA + kB;
-  constexpr int AI = kA / 1024, LI = kStage / 1024;
-  constexpr int MI = 4, NJ = 4;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  constexpr int kPlane = kRowsX * kStep * 2, kA = 2 * kPlane, kB = kStep * kColsX * 2, kStage = kA + kB;
+  constexpr int AI = kA / 1024 / 4, BI = kB / 1024 / 4, PER = AI + BI, BCPR = kColsX / 8;
+  __shared__ __attribute__((aligned(1024))) char lds[NST * kStage];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv / 2, wn = wv % 2;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kCols;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kColsX;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * kRowsX;
-  const int steps = (E + kStep - 1) / kStep;
 
   auto issue = [&](int st, char* dst) {
     const int k0 = st * kStep;
-    const __amdgpu_buffer_rsrc_t rw =
-        rsrc(wg + static_cast<int64_t>(k0) * d + n0, (static_cast<int64_t>(E - k0) * d - n0) * 2);
+    const __amdgpu_buffer_rsrc_t rw = rsrc(wg + k0 * d + n0, ((E - k0) * d - n0) * 2);
 #pragma unroll
-    for (int q0 = 0; q0 < LI; q0 += 4) {
-      const int q = q0 + wv;
-      if (q < AI) {
-        // 16 rows of 64 bytes; chunk c of row r in slot c ^ (r / 4) % 4
-        const int pl = q / (AI / 2), r = (q % (AI / 2)) * 16 + lane / 4, c = (lane % 4) ^ ((r / 4) % 4);
-        const bf16_t* base = planes + (static_cast<int64_t>(pl) * Tp + t0) * Ep + k0;
-        load_lds16(rsrc(base, (static_cast<int64_t>(kRowsX) * Ep) * 2), dst + q * 1024,
-                   static_cast<uint32_t>((r * Ep + c * 8) * 2));
-      } else {
-        const int r = (q - AI) * 4 + lane / 16, c = (lane % 16) ^ tr_swz<16>(r);
-        load_lds16(rw, dst + q * 1024, static_cast<uint32_t>(r * d * 2 + c * 16));
-      }
+    for (int i = 0; i < AI; ++i) {
+      const int q = wv * AI + i, pl = q / (2 * AI);
+      const int r = (q % (2 * AI)) * 16 + lane / 4, c = (lane % 4) ^ row_swz(r);
+      const bf16_t* base = rows + (static_cast<int64_t>(pl) * Tp + t0) * Ep + k0;
+      load_lds16(rsrc(base, (static_cast<int64_t>(kRowsX) * Ep - k0) * 2), dst + q * 1024,
+                 static_cast<uint32_t>((r * Ep + c * 8) * 2));
+    }
+#pragma unroll
+    for (int i = 0; i < BI; ++i) {
+      constexpr int RPI = 64 / BCPR;
+      const int q = wv * BI + i;
+      const int r = q * RPI + lane / BCPR, c = ((lane % BCPR) ^ kn_swz(r)) % BCPR;
+      load_lds16(rw, dst + kA + q * 1024, static_cast<uint32_t>(r * d * 2 + c * 16));
     }
   };
-
-  f32x4_t acc[MI][NJ];
+  f32x4_t acc[4][4];  // [column block][token block]
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  issue(0, lds);
-  for (int st = 0; st < steps; ++st) {
-    char* cur = lds + (st & 1) * kStage;
-    char* nxt = lds + ((st + 1) & 1) * kStage;
-    __syncthreads();
-    if (st + 1 < steps) issue(st + 1, nxt);
-    bf16x8_t b[NJ];
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  uint32_t at[8];
+  tr_offsets<BCPR>(wn * 64, at);
+  pipeline<NST, PER, kStage>((E + kStep - 1) / kStep, lds, issue, [&](const char* cur) {
+    bf16x8_t b[4];
+    tr_read(cur + kA, at, b);
+    plane_products<2>(cur, kPlane, wm * 64, b, acc);
+  });
+  // accumulator of lane l: columns 4 (l / 16) .. + 3 of token l % 16
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) b[j] = frag_tr<16>(cur + kA, wn * 64 + j * 16);
+  for (int j = 0; j < 4; ++j) {
+    const int64_t t = t0 + wm * 64 + j * 16 + lane % 16;
+    if (t >= T) continue;
+    uint2 in[4];
 #pragma unroll
-    for (int pl = 1; pl >= 0; --pl)
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const int r = wm * 64 + i * 16 + lane % 16, c = (lane / 16) ^ ((r / 4) % 4);
-        const bf16x8_t a =
-            *reinterpret_cast<const bf16x8_t*>(cur + pl * (kRowsX * kStep * 2) + r * (kStep * 2) + c * 16);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[j], acc[i][j], 0, 0, 0);
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t t = t0 + wm * 64 + i * 16 + 4 * (lane / 16) + v;
-      if (t >= T) continue;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int64_t n = n0 + wn * 64 + j * 16 + lane % 16;
-        if (n >= d) continue;
-        float r = acc[i][j][v];
-        if (dx_in) r += __uint_as_float(static_cast<uint32_t>(dx_in[t * d + n]) << 16);
-        reinterpret_cast<__bf16*>(dx)[t * d + n] = static_cast<__bf16>(r);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int64_t n = n0 + wn * 64 + i * 16 + 4 * (lane / 16);
+      in[i] = make_uint2(0, 0);
+      if (dx_in && n < d) in[i] = *reinterpret_cast<const uint2*>(dx_in + t * d + n);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t n = n0 + wn * 64 + i * 16 + 4 * (lane / 16);
+      if (n >= d) continue;
+      typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4_t;
+      const bf16x4_t r = {static_cast<__bf16>(acc[i][j][0] + bf16_lo(in[i].x)),
+                          static_cast<__bf16>(acc[i][j][1] + bf16_hi(in[i].x)),
+                          static_cast<__bf16>(acc[i][j][2] + bf16_lo(in[i].y)),
+                          static_cast<__bf16>(acc[i][j][3] + bf16_hi(in[i].y))};
+      *reinterpret_cast<bf16x4_t*>(dx + t * d + n) = r;
+    }
+  }
 }
 
+// Tile forms of dWg: up to 64 experts, 64 x 256 with four waves (x streamed
+// once, the padding experts' products are cheap beside it); beyond, 128 x 256
+// with eight.
+constexpr int kColsW = 256;
+int dwg_rows(int E) { return E <= 64 ? 64 : 128; }
+constexpr int kStagesW = 3, kStagesX = 3;
+
 struct GateWs {
-  int64_t Tp, blocks, steps;
+  int64_t Tp, blocks, steps, ncols;
   int Ep, bm, parts;
-  bf16_t* planes;
+  bf16_t* rows;  // [2][Tp][Ep]
+  bf16_t* cols;  // [3][Ep][Tp]
   float* bpart;
   float* part;  // null when one part: the sums go straight to dwg
 };
@@ -292,15 +405,18 @@ size_t layout(int64_t T, int64_t d, int E, void* ws, GateWs* g) {
   g->bm = dwg_rows(E);
   g->Ep = static_cast<int>(up(E, g->bm));
   g->Tp = up(T, kRowsX);
-  g->blocks = g->Tp / kSplitRows;
+  g->blocks = g->Tp / kBlk;
   g->steps = (T + kStep - 1) / kStep;
-  // token parts: about one round of workgroups, at least 8 steps to each
-  const int64_t tiles = (d + kCols - 1) / kCols * (g->Ep / g->bm);
-  int64_t parts = (256 + tiles - 1) / tiles;
-  if (parts > g->steps / 8) parts = g->steps / 8;
+  g->ncols = (d + kColsW - 1) / kColsW;
+  // token parts: as many as one round of 256 workgroups takes, at least 4 steps to each
+  const int64_t tiles = g->ncols * (g->Ep / g->bm);
+  int64_t parts = 256 / tiles;
+  if (parts > g->steps / 4) parts = g->steps / 4;
   g->parts = parts < 1 ? 1 : static_cast<int>(parts);
   size_t off = 0;
-  g->planes = reinterpret_cast<bf16_t*>(at(off));
+  g->rows = reinterpret_cast<bf16_t*>(at(off));
+  off += pad(size_t(2) * g->Tp * g->Ep * 2);
+  g->cols = reinterpret_cast<bf16_t*>(at(off));
   off += pad(size_t(3) * g->Tp * g->Ep * 2);
   g->bpart = reinterpret_cast<float*>(at(off));
   off += pad(size_t(g->blocks) * E * 4);
@@ -321,16 +437,17 @@ hipError_t launch_gate_backward(const void* x, const void* wg, const float* dlog
   GateWs g{};
   layout(T, d, E, ws, &g);
   const bf16_t* xb = static_cast<const bf16_t*>(x);
-  const unsigned ncols = static_cast<unsigned>((d + kCols - 1) / kCols);
-  hipLaunchKernelGGL(split_kernel, dim3(static_cast<unsigned>(g.blocks < (1 << 20) ? g.blocks : (1 << 20))), dim3(256),
-                     0, s, dlogits, T, E, g.Tp, g.Ep, g.planes, g.bpart);
+  hipLaunchKernelGGL(split_kernel, dim3(g.Ep / kBlk, static_cast<unsigned>(g.blocks)), dim3(256), 0, s, dlogits, T, E,
+                     g.Tp, g.Ep, g.rows, g.cols, g.bpart);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   float* o = g.parts > 1 ? g.part : dwg;
-  const dim3 grid(ncols, g.Ep / g.bm, g.parts);
-  if (g.bm == 32)
-    hipLaunchKernelGGL(dwg_kernel<32>, grid, dim3(256), 0, s, xb, g.planes, T, d, E, g.Tp, g.Ep, g.steps, o);
-  else
-    hipLaunchKernelGGL(dwg_kernel<128>, grid, dim3(256), 0, s, xb, g.planes, T, d, E, g.Tp, g.Ep, g.steps, o);
+  const int etiles = g.Ep / g.bm;
+  const dim3 grid(static_cast<unsigned>(g.ncols * etiles * g.parts));
+  if (g.bm == 64) {
+    hipLaunchKernelGGL((dwg_kernel<64, kColsW, kStagesW>), grid, dim3(256), 0, s, xb, g.cols, T, d, E, g.Tp, g.Ep, static_cast<int>(g.steps), etiles, g.parts, o);
+  } else {
+    hipLaunchKernelGGL((dwg_kernel<128, kColsW, kStagesW>), grid, dim3(512), 0, s, xb, g.cols, T, d, E, g.Tp, g.Ep, static_cast<int>(g.steps), etiles, g.parts, o);
+  }
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   const int bias_groups = (E + 15) / 16;
   const int64_t n4 = static_cast<int64_t>(E) * d / 4;
@@ -338,9 +455,10 @@ hipError_t launch_gate_backward(const void* x, const void* wg, const float* dlog
   hipLaunchKernelGGL(dwg_sum_kernel, dim3(static_cast<unsigned>(bias_groups + sum_groups)), dim3(256), 0, s, g.part,
                      g.parts, n4, dwg, g.bpart, g.blocks, E, dbias, bias_groups);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
-  hipLaunchKernelGGL(gate_dx_kernel, dim3(ncols, static_cast<unsigned>(g.Tp / kRowsX)), dim3(256), 0, s, g.planes,
-                     static_cast<const bf16_t*>(wg), static_cast<const bf16_t*>(dx_in), T, d, E, g.Tp, g.Ep,
-                     static_cast<bf16_t*>(dx));
+  hipLaunchKernelGGL(gate_dx_kernel<kStagesX>,
+                     dim3(static_cast<unsigned>((d + kColsX - 1) / kColsX), static_cast<unsigned>(g.Tp / kRowsX)),
+                     dim3(256), 0, s, g.rows, static_cast<const bf16_t*>(wg), static_cast<const bf16_t*>(dx_in), T,
+                     d, E, g.Tp, g.Ep, static_cast<bf16_t*>(dx));
   return hipGetLastError();
 }
 

@@ -50,8 +50,8 @@ hipError_t launch_dropout_backward(int dtype, const DropArgs& a, const void* dou
                                    hipStream_t s);
 
 // Gate gradients (bf16 x and wg, fp32 dlogits). ws: gate_backward_ws bytes.
-// T at most kGateMaxT (grid rows of 128 tokens), d at most kGateMaxD (32-bit row offsets).
-constexpr int64_t kGateMaxT = 65535 * int64_t(128);
+// T at most kGateMaxT (grid rows of 64 tokens), d at most kGateMaxD (32-bit row offsets).
+constexpr int64_t kGateMaxT = 65534 * int64_t(64);
 constexpr int64_t kGateMaxD = int64_t(1) << 24;
 size_t gate_backward_ws(int64_t T, int64_t d, int E);
 hipError_t launch_gate_backward(const void* x, const void* wg, const float* dlogits, const void* dx_in, void* dx,

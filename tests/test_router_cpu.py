@@ -192,7 +192,7 @@ def test_pointer_and_shape_refusals():
     assert gate(d(), A, A, A, None, None, A, A, A, need, None) == 1
     assert gate(d(dtype=0), A, A, A, None, A, A, A, A, need, None) == 2
     assert gate(d(d=100), A, A, A, None, A, A, A, A, 1 << 40, None) == 2
-    assert gate(d(T=8388481, E=8), A, A, A, None, A, A, A, A, 1 << 50, None) == 2
+    assert gate(d(T=4194177, E=8), A, A, A, None, A, A, A, A, 1 << 50, None) == 2
     # dropout
     for p in (-0.1, 1.1, math.nan):
         assert lib.moe_combine_dropout(d(), p, A, A, A, A, None, A, None) == 1
