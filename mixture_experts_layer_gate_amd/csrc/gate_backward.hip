@@ -24,7 +24,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kStep = 32;    // K per step (one MFMA)
+constexpr int kSub = 32;     // K of one MFMA
 constexpr int kRowsX = 128;  // tokens per dx workgroup
 constexpr int kColsX = 128;  // columns per dx workgroup
 
@@ -77,35 +77,47 @@ __device__ __forceinline__ void tr_read(const char* tile, const uint32_t (&at)[8
   for (int i = 0; i < 4; ++i)
     frag[i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(r[2 * i], r[2 * i + 1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
-// Rows of 64 bytes (32 K values): chunk c of row r in slot c ^ (r / 4) % 4, so
-// that 16 rows' reads of one chunk touch all banks.
-__device__ __forceinline__ int row_swz(int r) { return (r / 4) % 4; }
-__device__ __forceinline__ bf16x8_t row_frag(const char* tile, int row0) {
+// Rows of CPR 16-byte chunks (8 K values each): chunk c of row r in slot
+// c ^ row_swz(r), so that 16 rows' reads of one chunk touch all banks.
+template <int CPR>
+__device__ __forceinline__ int row_swz(int r) {
+  static_assert(CPR == 4 || CPR == 8, "rows of 64 or 128 bytes");
+  return (r / (16 / CPR)) % CPR;
+}
+template <int CPR>
+__device__ __forceinline__ bf16x8_t row_frag(const char* tile, int row0, int sub) {
   const int lane = threadIdx.x & 63, r = row0 + lane % 16;
-  return *reinterpret_cast<const bf16x8_t*>(tile + r * (kStep * 2) + ((lane / 16) ^ row_swz(r)) * 16);
+  return *reinterpret_cast<const bf16x8_t*>(tile + r * (CPR * 16) + ((4 * sub + lane / 16) ^ row_swz<CPR>(r)) * 16);
 }
 
-// acc[i][j] += b[i] x (row fragment j), summed over the planes, the smallest
-// first; a plane's fragments are read while the one before it multiplies.
-template <int kPlanes>
-__device__ __forceinline__ void plane_products(const char* tile, int plane_bytes, int row0, const bf16x8_t (&b)[4],
-                                               f32x4_t (&acc)[4][4]) {
-  bf16x8_t a[2][4];
+// One step's products: acc[i][j] += (transposed fragment i) x (row fragment j)
+// over kSteps / 32 sub-steps, summed over the planes, the smallest first; a
+// plane's fragments are read while the one before it multiplies.
+template <int kPlanes, int kStep, int BCPR>
+__device__ __forceinline__ void step_products(const char* rows, int plane_bytes, int row0, const char* cols,
+                                              const uint32_t (&at)[8], f32x4_t (&acc)[4][4]) {
+  constexpr int CPR = kStep / 8;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) a[0][j] = row_frag(tile + (kPlanes - 1) * plane_bytes, row0 + j * 16);
+  for (int s = 0; s < kStep / kSub; ++s) {
+    bf16x8_t b[4], a[2][4];
+    tr_read(cols + s * (kSub * BCPR * 16), at, b);
 #pragma unroll
-  for (int p = 0; p < kPlanes; ++p) {
-    if (p + 1 < kPlanes) {
+    for (int j = 0; j < 4; ++j) a[0][j] = row_frag<CPR>(rows + (kPlanes - 1) * plane_bytes, row0 + j * 16, s);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a[(p + 1) & 1][j] = row_frag(tile + (kPlanes - 2 - p) * plane_bytes, row0 + j * 16);
+    for (int p = 0; p < kPlanes; ++p) {
+      if (p + 1 < kPlanes) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          a[(p + 1) & 1][j] = row_frag<CPR>(rows + (kPlanes - 2 - p) * plane_bytes, row0 + j * 16, s);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i], a[p & 1][j], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i], a[p & 1][j], acc[i][j], 0, 0, 0);
-    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -214,7 +226,7 @@ __global__ __launch_bounds__(256) void split_kernel(const float* __restrict__ dl
 
 // A BM-expert x BN-column tile of one part of the tokens: out[part][e][n].
 // WM x WN waves, each 64 experts x 64 columns.
-template <int BM, int BN, int NST>
+template <int BM, int BN, int kStep, int NST>
 __global__ __launch_bounds__(BM / 64 * (BN / 64) * 64, 1) void dwg_kernel(const bf16_t* __restrict__ x,
                                                                        const bf16_t* __restrict__ cols, int64_t T,
                                                                        int64_t d, int E, int64_t Tp, int Ep,
@@ -228,11 +240,14 @@ __global__ __launch_bounds__(BM / 64 * (BN / 64) * 64, 1) void dwg_kernel(const 
   __shared__ __attribute__((aligned(1024))) char lds[NST * kStage];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv / WN, wn = wv % WN;
-  // expert tiles of one column block next to each other: they read the same x
+  // expert tiles of one column block next to each other (they read the same x),
+  // parts outermost (an XCD's tiles then read one or two parts of the planes,
+  // which its L2 holds)
   const int tile = xcd_tile(blockIdx.x, gridDim.x);
   const int e0 = tile % etiles * BM;
-  const int part = tile / etiles % parts;
-  const int64_t n0 = static_cast<int64_t>(tile / etiles / parts) * BN;
+  const int ncols = static_cast<int>((d + BN - 1) / BN);
+  const int64_t n0 = static_cast<int64_t>(tile / etiles % ncols) * BN;
+  const int part = tile / etiles / ncols;
   // the first steps % parts parts take one step more
   const int s0 = part * (steps / parts) + min(part, steps % parts);
   const int n_steps = steps / parts + (part < steps % parts);
@@ -242,11 +257,11 @@ __global__ __launch_bounds__(BM / 64 * (BN / 64) * 64, 1) void dwg_kernel(const 
     const __amdgpu_buffer_rsrc_t rx = rsrc(x + t * d + n0, ((T - t) * d - n0) * 2);
 #pragma unroll
     for (int i = 0; i < AI; ++i) {
-      constexpr int IPP = BM / 16;  // instructions per plane, 16 rows of 64 bytes each
-      const int q = wv * AI + i, pl = q / IPP, r = (q % IPP) * 16 + lane / 4;
+      constexpr int CPR = kStep / 8, RPI = 64 / CPR, IPP = BM / RPI;  // rows per instruction, instructions per plane
+      const int q = wv * AI + i, pl = q / IPP, r = (q % IPP) * RPI + lane / CPR;
       const bf16_t* base = cols + (static_cast<int64_t>(pl) * Ep + e0) * Tp + t;
       load_lds16(rsrc(base, (static_cast<int64_t>(BM) * Tp - t) * 2), dst + q * 1024,
-                 static_cast<uint32_t>(r * Tp * 2 + ((lane % 4) ^ row_swz(r)) * 16));
+                 static_cast<uint32_t>(r * Tp * 2 + ((lane % CPR) ^ row_swz<CPR>(r)) * 16));
     }
 #pragma unroll
     for (int i = 0; i < BI; ++i) {
@@ -264,9 +279,7 @@ __global__ __launch_bounds__(BM / 64 * (BN / 64) * 64, 1) void dwg_kernel(const 
   uint32_t at[8];
   tr_offsets<BCPR>(wn * 64, at);
   pipeline<NST, PER, kStage>(n_steps, lds, issue, [&](const char* cur) {
-    bf16x8_t b[4];
-    tr_read(cur + kA, at, b);
-    plane_products<3>(cur, kPlane, wm * 64, b, acc);
+    step_products<3, kStep, BCPR>(cur, kPlane, wm * 64, cur + kA, at, acc);
   });
   // accumulator of lane l: columns 4 (l / 16) .. + 3 of expert l % 16
   float* o = out + static_cast<int64_t>(part) * E * d;
@@ -314,7 +327,7 @@ __global__ __launch_bounds__(256) void dwg_sum_kernel(const float* __restrict__ 
 }
 
 // One 128-token x 128-column tile of dx: K = the experts, planes hi and mid.
-template <int NST>
+template <int kStep, int NST>
 __global__ __launch_bounds__(256) void gate_dx_kernel(const bf16_t* __restrict__ rows, const bf16_t* __restrict__ wg,
                                                       const bf16_t* dx_in, int64_t T, int64_t d, int E, int64_t Tp,
                                                       int Ep, bf16_t* dx) {
@@ -331,8 +344,9 @@ __global__ __launch_bounds__(256) void gate_dx_kernel(const bf16_t* __restrict__
     const __amdgpu_buffer_rsrc_t rw = rsrc(wg + k0 * d + n0, ((E - k0) * d - n0) * 2);
 #pragma unroll
     for (int i = 0; i < AI; ++i) {
+      constexpr int CPR = kStep / 8, RPI = 64 / CPR;
       const int q = wv * AI + i, pl = q / (2 * AI);
-      const int r = (q % (2 * AI)) * 16 + lane / 4, c = (lane % 4) ^ row_swz(r);
+      const int r = (q % (2 * AI)) * RPI + lane / CPR, c = (lane % CPR) ^ row_swz<CPR>(r);
       const bf16_t* base = rows + (static_cast<int64_t>(pl) * Tp + t0) * Ep + k0;
       load_lds16(rsrc(base, (static_cast<int64_t>(kRowsX) * Ep - k0) * 2), dst + q * 1024,
                  static_cast<uint32_t>((r * Ep + c * 8) * 2));
@@ -353,9 +367,7 @@ __global__ __launch_bounds__(256) void gate_dx_kernel(const bf16_t* __restrict__
   uint32_t at[8];
   tr_offsets<BCPR>(wn * 64, at);
   pipeline<NST, PER, kStage>((E + kStep - 1) / kStep, lds, issue, [&](const char* cur) {
-    bf16x8_t b[4];
-    tr_read(cur + kA, at, b);
-    plane_products<2>(cur, kPlane, wm * 64, b, acc);
+    step_products<2, kStep, BCPR>(cur, kPlane, wm * 64, cur + kA, at, acc);
   });
   // Accumulator of lane l: columns 4 (l / 16) .. + 3 of token l % 16. Through the
   // stage buffers (a wave's own 16 x 64 block at a time) to eight consecutive
@@ -409,7 +421,7 @@ __global__ __launch_bounds__(256) void gate_dx_kernel(const bf16_t* __restrict__
 // with eight.
 constexpr int kColsW = 256;
 int dwg_rows(int E) { return E <= 64 ? 64 : 128; }
-constexpr int kStagesW = 3, kStagesX = 3;
+constexpr int kStepW = 64, kStagesW = 2, kStepX = 32, kStagesX = 3;
 
 struct GateWs {
   int64_t Tp, blocks, steps, ncols;
@@ -427,7 +439,7 @@ size_t layout(int64_t T, int64_t d, int E, void* ws, GateWs* g) {
   g->Ep = static_cast<int>(up(E, g->bm));
   g->Tp = up(T, kRowsX);
   g->blocks = g->Tp / kBlk;
-  g->steps = (T + kStep - 1) / kStep;
+  g->steps = (T + kStepW - 1) / kStepW;
   g->ncols = (d + kColsW - 1) / kColsW;
   // token parts: as many as one round of 256 workgroups takes, at least 4 steps to each
   const int64_t tiles = g->ncols * (g->Ep / g->bm);
@@ -465,9 +477,9 @@ hipError_t launch_gate_backward(const void* x, const void* wg, const float* dlog
   const int etiles = g.Ep / g.bm;
   const dim3 grid(static_cast<unsigned>(g.ncols * etiles * g.parts));
   if (g.bm == 64) {
-    hipLaunchKernelGGL((dwg_kernel<64, kColsW, kStagesW>), grid, dim3(256), 0, s, xb, g.cols, T, d, E, g.Tp, g.Ep, static_cast<int>(g.steps), etiles, g.parts, o);
+    hipLaunchKernelGGL((dwg_kernel<64, kColsW, kStepW, kStagesW>), grid, dim3(256), 0, s, xb, g.cols, T, d, E, g.Tp, g.Ep, static_cast<int>(g.steps), etiles, g.parts, o);
   } else {
-    hipLaunchKernelGGL((dwg_kernel<128, kColsW, kStagesW>), grid, dim3(512), 0, s, xb, g.cols, T, d, E, g.Tp, g.Ep, static_cast<int>(g.steps), etiles, g.parts, o);
+    hipLaunchKernelGGL((dwg_kernel<128, kColsW, kStepW, kStagesW>), grid, dim3(512), 0, s, xb, g.cols, T, d, E, g.Tp, g.Ep, static_cast<int>(g.steps), etiles, g.parts, o);
   }
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   const int bias_groups = (E + 15) / 16;
@@ -476,7 +488,7 @@ hipError_t launch_gate_backward(const void* x, const void* wg, const float* dlog
   hipLaunchKernelGGL(dwg_sum_kernel, dim3(static_cast<unsigned>(bias_groups + sum_groups)), dim3(256), 0, s, g.part,
                      g.parts, n4, dwg, g.bpart, g.blocks, E, dbias, bias_groups);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
-  hipLaunchKernelGGL(gate_dx_kernel<kStagesX>,
+  hipLaunchKernelGGL((gate_dx_kernel<kStepX, kStagesX>),
                      dim3(static_cast<unsigned>((d + kColsX - 1) / kColsX), static_cast<unsigned>(g.Tp / kRowsX)),
                      dim3(256), 0, s, g.rows, static_cast<const bf16_t*>(wg), static_cast<const bf16_t*>(dx_in), T,
                      d, E, g.Tp, g.Ep, static_cast<bf16_t*>(dx));
