@@ -81,25 +81,28 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
 // be NaN), hence a choice and not a product.
 __device__ __forceinline__ float dropped(float v, float f) { return f != 0.0f ? v * f : 0.0f; }
 
-// One workgroup per token, eight columns per thread, as the plain combine. out
-// may be residual: each thread reads its elements before it writes them.
+// 256 threads of eight columns each to a (token, column band). out may be
+// residual: each thread reads its elements before it writes them.
 template <int kDtype>
 __global__ __launch_bounds__(256) void combine_dropout_kernel(DropArgs a, const void* __restrict__ y,
                                                               const int32_t* __restrict__ inv_perm,
                                                               const float* __restrict__ w, const void* residual,
-                                                              void* out, int64_t T, int64_t d, int k) {
+                                                              void* out, int64_t t0, int64_t T, int64_t d, int k,
+                                                              int bands) {
   const int64_t nvec = d / 8;
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x)
-    for (int64_t c = threadIdx.x; c < nvec; c += 256) {
-      const int64_t i = t * nvec + c;
-      float acc[8], f[8], r[8];
-      if (residual) load8<kDtype>(residual, i, r);
-      combine_sum<kDtype>(y, inv_perm, w, d, k, T * k, t, c, acc);
-      drop8(a, i, f);
+  const int64_t t = t0 + blockIdx.x / bands;
+  const int64_t c = static_cast<int64_t>(blockIdx.x % bands) * 256 + threadIdx.x;
+  if (c >= nvec) return;
+  const int64_t i = t * nvec + c;
+  float acc[8], f[8], r[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] = dropped(acc[j], f[j]) + (residual ? r[j] : 0.0f);
-      store8<kDtype>(out, i, acc);
-    }
+  for (int j = 0; j < 8; ++j) r[j] = 0.0f;
+  if (residual) load8<kDtype>(residual, i, r);
+  combine_sum<kDtype>(y, inv_perm, w, d, k, T * k, t, c, acc);
+  drop8(a, i, f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = dropped(acc[j], f[j]) + r[j];
+  store8<kDtype>(out, i, acc);
 }
 
 template <int kDtype>
@@ -121,12 +124,20 @@ unsigned capped(int64_t n, int64_t most) { return static_cast<unsigned>(n < most
 
 hipError_t launch_combine_dropout(int dtype, const DropArgs& a, const void* y, const int32_t* inv_perm, const float* w,
                                   const void* residual, void* out, int64_t T, int64_t d, int k, hipStream_t s) {
-  const dim3 grid(capped(T, int64_t(1) << 22));
-  if (dtype == 1)
-    hipLaunchKernelGGL((combine_dropout_kernel<1>), grid, dim3(256), 0, s, a, y, inv_perm, w, residual, out, T, d, k);
-  else
-    hipLaunchKernelGGL((combine_dropout_kernel<0>), grid, dim3(256), 0, s, a, y, inv_perm, w, residual, out, T, d, k);
-  return hipGetLastError();
+  // 256 columns of eight to a workgroup; a launch holds fewer than 2^32 threads
+  const int64_t bands = (d / 8 + 255) / 256, most = int64_t(1) << 23;
+  const int64_t chunk = most > bands ? most / bands : 1;
+  for (int64_t t0 = 0; t0 < T; t0 += chunk) {
+    const dim3 grid(static_cast<unsigned>((T - t0 < chunk ? T - t0 : chunk) * bands));
+    if (dtype == 1)
+      hipLaunchKernelGGL((combine_dropout_kernel<1>), grid, dim3(256), 0, s, a, y, inv_perm, w, residual, out, t0, T, d,
+                         k, static_cast<int>(bands));
+    else
+      hipLaunchKernelGGL((combine_dropout_kernel<0>), grid, dim3(256), 0, s, a, y, inv_perm, w, residual, out, t0, T, d,
+                         k, static_cast<int>(bands));
+    if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_dropout_backward(int dtype, const DropArgs& a, const void* dout, void* dy, int64_t T, int64_t d,

@@ -50,9 +50,10 @@ hipError_t launch_dropout_backward(int dtype, const DropArgs& a, const void* dou
                                    hipStream_t s);
 
 // Gate gradients (bf16 x and wg, fp32 dlogits). ws: gate_backward_ws bytes.
-// T at most kGateMaxT (grid rows of 64 tokens), d at most kGateMaxD (32-bit row offsets).
-constexpr int64_t kGateMaxT = 65534 * int64_t(64);
-constexpr int64_t kGateMaxD = int64_t(1) << 24;
+// T in grid rows of 64 tokens, 32-bit row offsets of d, and one launch of 128 x 128 tiles.
+inline bool gate_backward_fits(int64_t T, int64_t d) {
+  return T <= 65534 * int64_t(64) && d <= (int64_t(1) << 24) && (T / 128 + 1) * (d / 128 + 1) < (int64_t(1) << 23);
+}
 size_t gate_backward_ws(int64_t T, int64_t d, int E);
 hipError_t launch_gate_backward(const void* x, const void* wg, const float* dlogits, const void* dx_in, void* dx,
                                 float* dwg, float* dbias, int64_t T, int64_t d, int E, void* ws, hipStream_t s);

@@ -164,7 +164,7 @@ int moe_route_select_backward(const moe_dims_t* dm, const moe_route_opts_t* opts
 }
 
 size_t moe_gate_backward_workspace_bytes(const moe_dims_t* dm) {
-  if (check_dims(dm) != MOE_OK || dm->T > kGateMaxT || dm->d > kGateMaxD) return 0;
+  if (check_dims(dm) != MOE_OK || !gate_backward_fits(dm->T, dm->d)) return 0;
   return gate_backward_ws(dm->T, dm->d, dm->E);
 }
 
@@ -173,8 +173,7 @@ int moe_gate_backward(const moe_dims_t* dm, const void* x, const void* wg, const
   if (int st = check_dims(dm)) return st;
   if (!ok16(wg) || !ok16(dwg) || !ok4(dbias)) return MOE_ERR_INVALID;
   if (dm->T > 0 && (!ok16(x) || !ok4(dlogits) || !ok16(dx) || (dx_in && !ok16(dx_in)))) return MOE_ERR_INVALID;
-  if (dm->dtype != MOE_DTYPE_BF16 || dm->d % 8 != 0 || dm->T > kGateMaxT || dm->d > kGateMaxD)
-    return MOE_ERR_UNSUPPORTED;
+  if (dm->dtype != MOE_DTYPE_BF16 || dm->d % 8 != 0 || !gate_backward_fits(dm->T, dm->d)) return MOE_ERR_UNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
   StageScope sc(MOE_STAGE_GATE_BWD, s);
   if (dm->T == 0) {
