@@ -63,6 +63,14 @@ class Dims:
     def c(self) -> _Dims:
         return _Dims(self.T, self.d, self.f, self.E, self.k, MOE_DTYPE.get(self.dtype, -1))
 
+    def ref(self):
+        """A reference to the C struct, made once (the fields are frozen and the library only reads it)."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = ctypes.byref(self.c())
+            object.__setattr__(self, "_ref", r)
+        return r
+
 
 class _RouteOpts(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
@@ -92,6 +100,14 @@ class RouteOptions:
     def c(self) -> _RouteOpts:
         return _RouteOpts(int(self.score == "sigmoid"), self.groups, self.topk_groups, int(self.group_rule == "top2"),
                           int(bool(self.renormalise)), self.scale)
+
+    def ref(self):
+        """A reference to the C struct, made once (the fields are frozen and the library only reads it)."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = ctypes.byref(self.c())
+            object.__setattr__(self, "_ref", r)
+        return r
 
 
 def library_path() -> str:
@@ -562,43 +578,55 @@ def layer_backward(dims: Dims, x, wg, w1, w3, w2, routing: dict, dout, ws=None, 
 
 
 # ---- scored router, its losses and gradients, dropout beside the combine ----
-class _on:
-    """Scope of a call on its tensors' device: that device is made current, and with a
-    stream of the caller's that stream too, so that outputs and workspaces made here
-    belong to the stream the call runs on."""
+# These calls run on their tensors' device and are short on the GPU (a few
+# microseconds for a decode step), so their checks are kept to one comparison
+# per property and tensor.
+_one_device = None
 
-    def __init__(self, name: str, dev: torch.device, stream, *others):
-        if dev.type != "cuda":
-            raise ValueError(f"{name} must be a GPU tensor")
-        for n, t in others:
-            if t is not None and t.device != dev:
-                raise ValueError(f"{n} is on {t.device}, {name} on {dev}")
-        if stream is not None and stream.device != dev:
+
+def _enter(name: str, dev: torch.device, stream):
+    """Makes the tensors' device current, and a stream of the caller's too, so that
+    outputs and workspaces made here belong to the stream the call runs on. Returns a
+    scope to leave, or None."""
+    global _one_device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    if stream is not None:
+        if stream.device != dev:
             raise ValueError(f"stream is on {stream.device}, {name} on {dev}")
-        self.scope = None
-        if stream is not None:
-            self.scope = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != dev.index:
-            self.scope = torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.scope is not None:
-            self.scope.__enter__()
-
-    def __exit__(self, *exc):
-        if self.scope is not None:
-            self.scope.__exit__(*exc)
+        scope = torch.cuda.stream(stream)
+    else:
+        if _one_device is None:
+            _one_device = torch.cuda.device_count() == 1
+        if _one_device or torch.cuda.current_device() == dev.index:
+            return None
+        scope = torch.cuda.device(dev)
+    scope.__enter__()
+    return scope
 
 
-def _out(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, dev):
+def _in(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev) -> int:
+    """The pointer of an input or output tensor, checked."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        _need(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+def _opt(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, dev) -> Optional[int]:
+    return None if t is None else _in(t, name, dtype, shape, dev)
+
+
+def _new(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, dev) -> torch.Tensor:
     """The caller's output tensor, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, name, dtype, shape)
+    _in(t, name, dtype, shape, dev)
     return t
 
 
-def _scratch(ws: Optional[torch.Tensor], nbytes: int, dev):
+def _scratch(ws: Optional[torch.Tensor], nbytes: int, dev) -> torch.Tensor:
     """The caller's workspace, or a new one of nbytes. A tensor made here may be freed
     when the call returns: torch's allocator hands it out again in stream order."""
     if ws is None:
@@ -608,23 +636,43 @@ def _scratch(ws: Optional[torch.Tensor], nbytes: int, dev):
     return ws
 
 
+# torch's raw query of a device's current stream, where this torch has it: it makes
+# no Stream object (0.1 us instead of 2)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _here(dev: torch.device) -> int:
+    """The current stream of the (current) device."""
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _leave(scope):
+    if scope is not None:
+        scope.__exit__(None, None, None)
+
+
 def route_select(dims: Dims, opts: RouteOptions, logits, balance_bias=None, topk_idx=None, topk_w=None, stream=None):
     """Experts chosen from gate logits [T][E] (fp32) by their scores. balance_bias [E]
     (fp32) is added to the scores for the choice only; an expert whose logit or bias is
     -inf (or NaN) is out of the choice. Returns (topk_idx [T][k] int32, topk_w [T][k]
     fp32); slots left over when fewer than k experts are in the choice hold the other
     experts in ascending order with weight 0."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = logits.device
-    with _on("logits", dev, stream, ("balance_bias", balance_bias), ("topk_idx", topk_idx), ("topk_w", topk_w)):
-        _need(logits, "logits", torch.float32, (dims.T, dims.E))
-        if balance_bias is not None:
-            _need(balance_bias, "balance_bias", torch.float32, (dims.E,))
-        idx = _out(topk_idx, "topk_idx", torch.int32, (dims.T, dims.k), dev)
-        w = _out(topk_w, "topk_w", torch.float32, (dims.T, dims.k), dev)
-        _check("moe_route_select", lib.moe_route_select(
-            ctypes.byref(dims.c()), ctypes.byref(opts.c()), _ptr(logits), _ptr(balance_bias), _ptr(idx), _ptr(w),
-            _stream(None)))
+    scope = _enter("logits", dev, stream)
+    try:
+        T, E, k = dims.T, dims.E, dims.k
+        pl = _in(logits, "logits", torch.float32, (T, E), dev)
+        pb = _opt(balance_bias, "balance_bias", torch.float32, (E,), dev)
+        idx = _new(topk_idx, "topk_idx", torch.int32, (T, k), dev)
+        w = _new(topk_w, "topk_w", torch.float32, (T, k), dev)
+        st = lib.moe_route_select(dims.ref(), opts.ref(), pl, pb, idx.data_ptr(), w.data_ptr(), _here(dev))
+    finally:
+        _leave(scope)
+    if st:
+        _check("moe_route_select", st)
     return idx, w
 
 
@@ -632,21 +680,24 @@ def route_scored(dims: Dims, opts: RouteOptions, x, wg, bias=None, balance_bias=
                  topk_w=None, stream=None):
     """Gate logits (those of route, bit for bit) and the selection of route_select.
     Returns (logits, topk_idx, topk_w)."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = x.device
-    with _on("x", dev, stream, ("wg", wg), ("bias", bias), ("balance_bias", balance_bias), ("logits", logits),
-             ("topk_idx", topk_idx), ("topk_w", topk_w)):
-        _need(x, "x", dims.dtype, (dims.T, dims.d))
-        _need(wg, "wg", dims.dtype, (dims.E, dims.d))
-        for name, b in (("bias", bias), ("balance_bias", balance_bias)):
-            if b is not None:
-                _need(b, name, torch.float32, (dims.E,))
-        lg = _out(logits, "logits", torch.float32, (dims.T, dims.E), dev)
-        idx = _out(topk_idx, "topk_idx", torch.int32, (dims.T, dims.k), dev)
-        w = _out(topk_w, "topk_w", torch.float32, (dims.T, dims.k), dev)
-        _check("moe_route_scored", lib.moe_route_scored(
-            ctypes.byref(dims.c()), ctypes.byref(opts.c()), _ptr(x), _ptr(wg), _ptr(bias), _ptr(balance_bias),
-            _ptr(lg), _ptr(idx), _ptr(w), _stream(None)))
+    scope = _enter("x", dev, stream)
+    try:
+        T, d, E, k = dims.T, dims.d, dims.E, dims.k
+        px = _in(x, "x", dims.dtype, (T, d), dev)
+        pg = _in(wg, "wg", dims.dtype, (E, d), dev)
+        pb = _opt(bias, "bias", torch.float32, (E,), dev)
+        pbb = _opt(balance_bias, "balance_bias", torch.float32, (E,), dev)
+        lg = _new(logits, "logits", torch.float32, (T, E), dev)
+        idx = _new(topk_idx, "topk_idx", torch.int32, (T, k), dev)
+        w = _new(topk_w, "topk_w", torch.float32, (T, k), dev)
+        st = lib.moe_route_scored(dims.ref(), opts.ref(), px, pg, pb, pbb, lg.data_ptr(), idx.data_ptr(),
+                                  w.data_ptr(), _here(dev))
+    finally:
+        _leave(scope)
+    if st:
+        _check("moe_route_scored", st)
     return lg, idx, w
 
 
@@ -655,12 +706,22 @@ def _seqs(seq_offsets):
         return 1
     if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
         raise ValueError("seq_offsets must be a vector of at least two offsets")
-    _need(seq_offsets, "seq_offsets", torch.int32, tuple(seq_offsets.shape))
     return seq_offsets.numel() - 1
 
 
+def _sized(dims: Dims, key, query) -> int:
+    """query(), asked once per Dims object and key (the sizes depend on nothing else)."""
+    sizes = dims.__dict__.get("_sizes")
+    if sizes is None:
+        sizes = {}
+        object.__setattr__(dims, "_sizes", sizes)
+    if key not in sizes:
+        sizes[key] = int(query())
+    return sizes[key]
+
+
 def balance_workspace_bytes(dims: Dims, n_seq: int = 1) -> int:
-    return int(load_library().moe_balance_workspace_bytes(ctypes.byref(dims.c()), n_seq))
+    return _sized(dims, ("balance", n_seq), lambda: load_library().moe_balance_workspace_bytes(dims.ref(), n_seq))
 
 
 def balance_loss(dims: Dims, opts: RouteOptions, logits, topk_idx, seq_offsets=None, losses=None, load=None, ws=None,
@@ -669,18 +730,24 @@ def balance_loss(dims: Dims, opts: RouteOptions, logits, topk_idx, seq_offsets=N
     for one sequence of all rows). Returns (losses [2] fp32: the balance loss and the mean
     squared log-sum-exp of the logits; load [S][E] int32: how often each sequence chose
     each expert)."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = logits.device
-    with _on("logits", dev, stream, ("topk_idx", topk_idx), ("seq_offsets", seq_offsets), ("losses", losses), ("load", load)):
-        _need(logits, "logits", torch.float32, (dims.T, dims.E))
-        _need(topk_idx, "topk_idx", torch.int32, (dims.T, dims.k))
+    scope = _enter("logits", dev, stream)
+    try:
+        T, E, k = dims.T, dims.E, dims.k
         n_seq = _seqs(seq_offsets)
-        lo = _out(losses, "losses", torch.float32, (2,), dev)
-        ld = _out(load, "load", torch.int32, (n_seq, dims.E), dev)
-        w = _scratch(ws, balance_workspace_bytes(dims, n_seq), dev)
-        _check("moe_balance_loss", lib.moe_balance_loss(
-            ctypes.byref(dims.c()), ctypes.byref(opts.c()), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), n_seq,
-            _ptr(lo), _ptr(ld), _ptr(w), w.numel() * w.element_size(), _stream(None)))
+        pl = _in(logits, "logits", torch.float32, (T, E), dev)
+        pi = _in(topk_idx, "topk_idx", torch.int32, (T, k), dev)
+        ps = _opt(seq_offsets, "seq_offsets", torch.int32, (n_seq + 1,), dev)
+        lo = _new(losses, "losses", torch.float32, (2,), dev)
+        ld = _new(load, "load", torch.int32, (n_seq, E), dev)
+        w = _scratch(ws, balance_workspace_bytes(dims, n_seq) if ws is None else 0, dev)
+        st = lib.moe_balance_loss(dims.ref(), opts.ref(), pl, pi, ps, n_seq, lo.data_ptr(), ld.data_ptr(),
+                                  w.data_ptr(), w.numel() * w.element_size(), _here(dev))
+    finally:
+        _leave(scope)
+    if st:
+        _check("moe_balance_loss", st)
     return lo, ld
 
 
@@ -689,53 +756,60 @@ def route_select_backward(dims: Dims, opts: RouteOptions, logits, topk_idx, topk
     """Gradient with respect to the logits of route_select's weights (upstream gradient
     dtopk_w [T][k], None for none) and of balance_loss (upstream gradients dlosses [2],
     None for none; load and seq_offsets as balance_loss had them). Returns dlogits [T][E]."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = logits.device
-    with _on("logits", dev, stream, ("topk_idx", topk_idx), ("topk_w", topk_w), ("dtopk_w", dtopk_w), ("dlosses", dlosses),
-             ("load", load), ("seq_offsets", seq_offsets), ("dlogits", dlogits)):
-        _need(logits, "logits", torch.float32, (dims.T, dims.E))
-        for name, t, dt in (("topk_idx", topk_idx, torch.int32), ("topk_w", topk_w, torch.float32),
-                            ("dtopk_w", dtopk_w, torch.float32)):
-            if t is not None:
-                _need(t, name, dt, (dims.T, dims.k))
-        n_seq = 1
+    scope = _enter("logits", dev, stream)
+    try:
+        T, E, k = dims.T, dims.E, dims.k
+        pl = _in(logits, "logits", torch.float32, (T, E), dev)
+        pi = _opt(topk_idx, "topk_idx", torch.int32, (T, k), dev)
+        pw = _opt(topk_w, "topk_w", torch.float32, (T, k), dev)
+        pd = _opt(dtopk_w, "dtopk_w", torch.float32, (T, k), dev)
+        n_seq, pu, pf, ps = 1, None, None, None
         if dlosses is not None:
-            n_seq = _seqs(seq_offsets)
-            _need(dlosses, "dlosses", torch.float32, (2,))
             if load is None:
                 raise ValueError("dlosses needs load, as balance_loss returned it")
-            _need(load, "load", torch.int32, (n_seq, dims.E))
-        dl = _out(dlogits, "dlogits", torch.float32, (dims.T, dims.E), dev)
-        _check("moe_route_select_backward", lib.moe_route_select_backward(
-            ctypes.byref(dims.c()), ctypes.byref(opts.c()), _ptr(logits), _ptr(topk_idx), _ptr(topk_w),
-            _ptr(dtopk_w), _ptr(dlosses), _ptr(load), _ptr(seq_offsets), n_seq, _ptr(dl), _stream(None)))
+            n_seq = _seqs(seq_offsets)
+            pu = _in(dlosses, "dlosses", torch.float32, (2,), dev)
+            pf = _in(load, "load", torch.int32, (n_seq, E), dev)
+            ps = _opt(seq_offsets, "seq_offsets", torch.int32, (n_seq + 1,), dev)
+        dl = _new(dlogits, "dlogits", torch.float32, (T, E), dev)
+        st = lib.moe_route_select_backward(dims.ref(), opts.ref(), pl, pi, pw, pd, pu, pf, ps, n_seq, dl.data_ptr(),
+                                           _here(dev))
+    finally:
+        _leave(scope)
+    if st:
+        _check("moe_route_select_backward", st)
     return dl
 
 
 def gate_backward_workspace_bytes(dims: Dims) -> int:
-    return int(load_library().moe_gate_backward_workspace_bytes(ctypes.byref(dims.c())))
+    return _sized(dims, "gate", lambda: load_library().moe_gate_backward_workspace_bytes(dims.ref()))
 
 
 def gate_backward(dims: Dims, x, wg, dlogits, dx_in=None, dx=None, dwg=None, dbias=None, ws=None, stream=None):
     """Gradients of the gate GEMM for a dense dlogits [T][E] (fp32): dx [T][d] = dx_in +
     dlogits wg (bf16; dx may be dx_in), dwg [E][d] and dbias [E] (fp32). bf16 layers.
     Returns (dx, dwg, dbias)."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = x.device
-    with _on("x", dev, stream, ("wg", wg), ("dlogits", dlogits), ("dx_in", dx_in), ("dx", dx), ("dwg", dwg),
-             ("dbias", dbias)):
-        _need(x, "x", dims.dtype, (dims.T, dims.d))
-        _need(wg, "wg", dims.dtype, (dims.E, dims.d))
-        _need(dlogits, "dlogits", torch.float32, (dims.T, dims.E))
-        if dx_in is not None:
-            _need(dx_in, "dx_in", dims.dtype, (dims.T, dims.d))
-        ox = _out(dx, "dx", dims.dtype, (dims.T, dims.d), dev)
-        ow = _out(dwg, "dwg", torch.float32, (dims.E, dims.d), dev)
-        ob = _out(dbias, "dbias", torch.float32, (dims.E,), dev)
-        w = _scratch(ws, gate_backward_workspace_bytes(dims), dev)
-        _check("moe_gate_backward", lib.moe_gate_backward(
-            ctypes.byref(dims.c()), _ptr(x), _ptr(wg), _ptr(dlogits), _ptr(dx_in), _ptr(ox), _ptr(ow), _ptr(ob),
-            _ptr(w), w.numel() * w.element_size(), _stream(None)))
+    scope = _enter("x", dev, stream)
+    try:
+        T, d, E = dims.T, dims.d, dims.E
+        px = _in(x, "x", dims.dtype, (T, d), dev)
+        pg = _in(wg, "wg", dims.dtype, (E, d), dev)
+        pl = _in(dlogits, "dlogits", torch.float32, (T, E), dev)
+        pi = _opt(dx_in, "dx_in", dims.dtype, (T, d), dev)
+        ox = _new(dx, "dx", dims.dtype, (T, d), dev)
+        ow = _new(dwg, "dwg", torch.float32, (E, d), dev)
+        ob = _new(dbias, "dbias", torch.float32, (E,), dev)
+        w = _scratch(ws, gate_backward_workspace_bytes(dims) if ws is None else 0, dev)
+        st = lib.moe_gate_backward(dims.ref(), px, pg, pl, pi, ox.data_ptr(), ow.data_ptr(), ob.data_ptr(),
+                                   w.data_ptr(), w.numel() * w.element_size(), _here(dev))
+    finally:
+        _leave(scope)
+    if st:
+        _check("moe_gate_backward", st)
     return ox, ow, ob
 
 
@@ -744,37 +818,32 @@ def experts_backward(dims: Dims, x, w1, w3, w2, routing: dict, dout, ws=None, st
     """The experts' part of layer_backward, for a router whose gradient is taken by
     route_select_backward and gate_backward: routing and options as there. Returns a dict
     with dx (the experts' part), dw1, dw3, dw2 and dtopk_w [T][k]."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = x.device
-    g = dict(grads or {})
-    with _on("x", dev, stream, ("w1", w1), ("w3", w3), ("w2", w2), ("dout", dout), ("gu", gu), *routing.items(), *g.items()):
-        _need(x, "x", dims.dtype, (dims.T, dims.d))
-        _need(dout, "dout", dims.dtype, (dims.T, dims.d))
-        for name, w, shp in (("w1", w1, (dims.E, dims.f, dims.d)), ("w3", w3, (dims.E, dims.f, dims.d)),
-                             ("w2", w2, (dims.E, dims.d, dims.f))):
-            _need(w, name, dims.dtype, shp)
-        n = dims.T * dims.k
-        for name, dt, shp in (("topk_idx", torch.int32, (dims.T, dims.k)),
-                              ("topk_w", torch.float32, (dims.T, dims.k)), ("counts", torch.int32, (dims.E,)),
-                              ("offsets", torch.int32, (dims.E + 1,)), ("perm", torch.int32, (n,)),
-                              ("inv_perm", torch.int32, (n,))):
-            _need(routing[name], name, dt, shp)
-        if wgrad_dtype not in (torch.float32, torch.bfloat16):
-            raise ValueError("wgrad_dtype must be torch.float32 or torch.bfloat16")
-        if gu is not None:
-            _need(gu, "gu", dims.dtype, (n, 2 * dims.f))
-        for name, shp, dt in (("dx", (dims.T, dims.d), dims.dtype), ("dw1", (dims.E, dims.f, dims.d), wgrad_dtype),
-                              ("dw3", (dims.E, dims.f, dims.d), wgrad_dtype),
-                              ("dw2", (dims.E, dims.d, dims.f), wgrad_dtype),
-                              ("dtopk_w", (dims.T, dims.k), torch.float32)):
-            g[name] = _out(g.get(name), name, dt, shp, dev)
-        w = _scratch(ws, backward_workspace_bytes(dims), dev)
-        r = routing
-        _check("moe_experts_backward", lib.moe_experts_backward(
-            ctypes.byref(dims.c()), _ptr(x), _ptr(w1), _ptr(w3), _ptr(w2), _ptr(r["topk_idx"]), _ptr(r["topk_w"]),
-            _ptr(r["counts"]), _ptr(r["offsets"]), _ptr(r["perm"]), _ptr(r["inv_perm"]), _ptr(dout), _ptr(gu),
-            MOE_DTYPE[wgrad_dtype], _ptr(g["dx"]), _ptr(g["dw1"]), _ptr(g["dw3"]), _ptr(g["dw2"]),
-            _ptr(g["dtopk_w"]), _ptr(w), w.numel() * w.element_size(), _stream(None)))
+    if wgrad_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("wgrad_dtype must be torch.float32 or torch.bfloat16")
+    scope = _enter("x", dev, stream)
+    try:
+        T, d, f, E, k, n = dims.T, dims.d, dims.f, dims.E, dims.k, dims.T * dims.k
+        g, r, i32, f32 = dict(grads or {}), routing, torch.int32, torch.float32
+        head = [_in(x, "x", dims.dtype, (T, d), dev), _in(w1, "w1", dims.dtype, (E, f, d), dev),
+                _in(w3, "w3", dims.dtype, (E, f, d), dev), _in(w2, "w2", dims.dtype, (E, d, f), dev)]
+        head += [_in(r[name], name, dt, shp, dev) for name, dt, shp in (
+            ("topk_idx", i32, (T, k)), ("topk_w", f32, (T, k)), ("counts", i32, (E,)), ("offsets", i32, (E + 1,)),
+            ("perm", i32, (n,)), ("inv_perm", i32, (n,)))]
+        head += [_in(dout, "dout", dims.dtype, (T, d), dev), _opt(gu, "gu", dims.dtype, (n, 2 * f), dev)]
+        for name, shp, dt in (("dx", (T, d), dims.dtype), ("dw1", (E, f, d), wgrad_dtype),
+                              ("dw3", (E, f, d), wgrad_dtype), ("dw2", (E, d, f), wgrad_dtype),
+                              ("dtopk_w", (T, k), f32)):
+            g[name] = _new(g.get(name), name, dt, shp, dev)
+        w = _scratch(ws, backward_workspace_bytes(dims) if ws is None else 0, dev)
+        st = lib.moe_experts_backward(dims.ref(), *head, MOE_DTYPE[wgrad_dtype], g["dx"].data_ptr(),
+                                      g["dw1"].data_ptr(), g["dw3"].data_ptr(), g["dw2"].data_ptr(),
+                                      g["dtopk_w"].data_ptr(), w.data_ptr(), w.numel() * w.element_size(), _here(dev))
+    finally:
+        _leave(scope)
+    if st:
+        _check("moe_experts_backward", st)
     return g
 
 
@@ -783,34 +852,40 @@ def combine_dropout(dims: Dims, p: float, rng, y_sorted, inv_perm, topk_w, resid
     [T][d] added: residual + keep / (1 - p) * sum. rng: int64 tensor [2] on the GPU, seed
     and offset; the same pair draws the same decisions (dropout_backward takes it again).
     out may be residual. Returns out [T][d]."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = y_sorted.device
-    with _on("y_sorted", dev, stream, ("rng", rng), ("inv_perm", inv_perm), ("topk_w", topk_w), ("residual", residual),
-             ("out", out)):
-        _need(rng, "rng", torch.int64, (2,))
-        _need(y_sorted, "y_sorted", dims.dtype, (dims.T * dims.k, dims.d))
-        _need(inv_perm, "inv_perm", torch.int32, (dims.T * dims.k,))
-        _need(topk_w, "topk_w", torch.float32, (dims.T, dims.k))
-        if residual is not None:
-            _need(residual, "residual", dims.dtype, (dims.T, dims.d))
-        o = _out(out, "out", dims.dtype, (dims.T, dims.d), dev)
-        _check("moe_combine_dropout", lib.moe_combine_dropout(
-            ctypes.byref(dims.c()), p, _ptr(rng), _ptr(y_sorted), _ptr(inv_perm), _ptr(topk_w), _ptr(residual),
-            _ptr(o), _stream(None)))
+    scope = _enter("y_sorted", dev, stream)
+    try:
+        T, d, k, n = dims.T, dims.d, dims.k, dims.T * dims.k
+        pr = _in(rng, "rng", torch.int64, (2,), dev)
+        py = _in(y_sorted, "y_sorted", dims.dtype, (n, d), dev)
+        pi = _in(inv_perm, "inv_perm", torch.int32, (n,), dev)
+        pw = _in(topk_w, "topk_w", torch.float32, (T, k), dev)
+        ps = _opt(residual, "residual", dims.dtype, (T, d), dev)
+        o = _new(out, "out", dims.dtype, (T, d), dev)
+        st = lib.moe_combine_dropout(dims.ref(), p, pr, py, pi, pw, ps, o.data_ptr(), _here(dev))
+    finally:
+        _leave(scope)
+    if st:
+        _check("moe_combine_dropout", st)
     return o
 
 
 def dropout_backward(dims: Dims, p: float, rng, dout, dy=None, stream=None):
     """Gradient of combine_dropout's combined rows: keep / (1 - p) * dout with the decisions
     of the same p and rng. dy may be dout. Returns dy [T][d]."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = dout.device
-    with _on("dout", dev, stream, ("rng", rng), ("dy", dy)):
-        _need(rng, "rng", torch.int64, (2,))
-        _need(dout, "dout", dims.dtype, (dims.T, dims.d))
-        o = _out(dy, "dy", dims.dtype, (dims.T, dims.d), dev)
-        _check("moe_dropout_backward", lib.moe_dropout_backward(
-            ctypes.byref(dims.c()), p, _ptr(rng), _ptr(dout), _ptr(o), _stream(None)))
+    scope = _enter("dout", dev, stream)
+    try:
+        pr = _in(rng, "rng", torch.int64, (2,), dev)
+        pd = _in(dout, "dout", dims.dtype, (dims.T, dims.d), dev)
+        o = _new(dy, "dy", dims.dtype, (dims.T, dims.d), dev)
+        st = lib.moe_dropout_backward(dims.ref(), p, pr, pd, o.data_ptr(), _here(dev))
+    finally:
+        _leave(scope)
+    if st:
+        _check("moe_dropout_backward", st)
     return o
 
 

@@ -30,7 +30,7 @@ hipError_t launch_select_backward(const SelectOpts& o, const float* logits, cons
                                   hipStream_t s);
 
 // Balance losses: row parts per sequence, and the workspace pieces they need.
-int balance_parts(int64_t T, int n_seq);
+int balance_parts(int64_t T, int n_seq, int E);
 int balance_blocks(int E);  // expert blocks of the part reduction
 hipError_t launch_balance(const SelectOpts& o, const float* logits, const int32_t* idx, const int32_t* seq_offsets,
                           int n_seq, int64_t T, int E, int k, int parts, float* part_p, int32_t* part_f,

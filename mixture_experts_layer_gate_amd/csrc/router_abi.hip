@@ -58,7 +58,7 @@ struct BalanceWs {
 size_t balance_ws(const moe_dims_t* dm, int n_seq, void* ws, BalanceWs* out) {
   Carver c(ws);
   BalanceWs r{};
-  r.parts = balance_parts(dm->T, n_seq);
+  r.parts = balance_parts(dm->T, n_seq, dm->E);
   const size_t np = size_t(n_seq) * r.parts;
   r.p = c.take<float>(sizeof(float) * np * dm->E);
   r.f = c.take<int32_t>(sizeof(int32_t) * np * dm->E);
