@@ -790,7 +790,7 @@ __global__ __launch_bounds__(256) void balance_part_kernel(SelectOpts o, const f
   for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
   double zacc = 0.0;
   // two rows at a time: their loads and their reductions' latencies overlap
-  for (int t = lo + wv; t < hi; t += 8) {
+  for (int64_t t = lo + wv; t < hi; t += 8) {
     float l[2][VPL], x[2][VPL], m[2], zs[2], tot[2];
     int32_t e[2];
 #pragma unroll

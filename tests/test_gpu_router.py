@@ -634,6 +634,80 @@ def test_step_in_a_graph(rng):
             assert torch.equal(kept[n], want[n]), (it, n)
 
 
+def test_tensors_off_their_alignment(rng):
+    """fp32 and int32 tensors that start one element past a 16-byte boundary: the same bits."""
+    T, E, k = 37, 64, 8
+    l, b = _logits(rng, T, E, "plain"), _bias(rng, E, "small")
+    spec = ro.RouteSpec("sigmoid", 8, 4, "top2", True, 2.5)
+    dims, opts = moe.Dims(T, 64, 64, E, k, torch.bfloat16), _opts(spec)
+
+    def shifted(t):
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        buf[1:].copy_(t.reshape(-1))
+        return buf[1:].view(t.shape)
+
+    def step(mv):
+        tl, tb = mv(torch.from_numpy(l).cuda()), mv(torch.from_numpy(b).cuda())
+        idx, w = mv(torch.zeros((T, k), dtype=torch.int32, device="cuda")), mv(torch.zeros((T, k), device="cuda"))
+        moe.route_select(dims, opts, tl, tb, topk_idx=idx, topk_w=w)
+        dw, up = mv(torch.ones((T, k), device="cuda").cumsum(1)), mv(torch.tensor([0.5, 0.25], device="cuda"))
+        seq = mv(torch.tensor([0, 9, T], dtype=torch.int32, device="cuda"))
+        load = mv(torch.zeros((2, E), dtype=torch.int32, device="cuda"))
+        losses, _ = moe.balance_loss(dims, opts, tl, idx, seq, load=load, losses=mv(torch.zeros(2, device="cuda")))
+        dl = moe.route_select_backward(dims, opts, tl, idx, w, dw, up, load, seq,
+                                       dlogits=mv(torch.zeros((T, E), device="cuda")))
+        x = torch.ones((T, 64), dtype=torch.bfloat16, device="cuda")
+        wg = torch.ones((E, 64), dtype=torch.bfloat16, device="cuda")
+        _, dwg, db = moe.gate_backward(dims, x, wg, dl, dbias=mv(torch.zeros(E, device="cuda")))
+        return idx, w, losses, load, dl, dwg, db
+    for a, c in zip(step(lambda t: t), step(shifted)):
+        assert torch.equal(a, c)
+
+
+def test_more_tokens_than_one_launch_holds():
+    """Batches that take several launches: selection (2^25 tokens each) and the combine (2^23 workgroups each)."""
+    T = 2 ** 25 + 5
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    l = torch.randn((T, 2), generator=gen, device="cuda")
+    dims = moe.Dims(T, 64, 64, 2, 1)
+    idx, w = moe.route_select(dims, moe.RouteOptions(), l)
+    assert torch.equal(idx[:, 0], (l[:, 1] > l[:, 0]).int()) and bool((w == 1).all())
+    losses, load = moe.balance_loss(dims, moe.RouteOptions(), l, idx)
+    assert torch.equal(load[0].long(), torch.bincount(idx[:, 0].long(), minlength=2))
+    # p of the chosen expert minus 1 for it, plus p for the other, on every row
+    dl = moe.route_select_backward(dims, moe.RouteOptions(renormalise=False), l, idx, torch.softmax(l, 1).gather(
+        1, idx.long()), torch.ones((T, 1), device="cuda"))
+    p = torch.softmax(l, 1)
+    torch.testing.assert_close(dl.gather(1, idx.long())[:, 0], (p[:, 0] * p[:, 1]), rtol=0, atol=64 * U)
+    del l, dl, p, idx, w
+    T = 2 ** 23 + 3
+    dims = moe.Dims(T, 8, 64, 8, 1)
+    y = torch.randn((T, 8), generator=gen, device="cuda").bfloat16()
+    r = torch.tensor([3, 4], dtype=torch.int64, device="cuda")
+    out = moe.combine_dropout(dims, 0.5, r, y, torch.arange(T, dtype=torch.int32, device="cuda"),
+                              torch.ones((T, 1), device="cuda"))
+    assert torch.equal(out, moe.dropout_backward(dims, 0.5, r, y))
+
+
+def test_two_steps_at_once(rng):
+    """Two steps on two streams at the same time, each with its own buffers: each as when alone."""
+    a, b = _step_inputs(300, 256, 256, 8, 2, 11), _step_inputs(210, 256, 256, 8, 2, 12)
+    want = [_training_step(a[0], SCORED[0], 0.1, a[1]), _training_step(b[0], SCORED[1], 0.3, b[1])]
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(3):
+        got = []
+        with torch.cuda.stream(s):
+            got.append(_training_step(a[0], SCORED[0], 0.1, a[1]))
+        with torch.cuda.stream(t):
+            got.append(_training_step(b[0], SCORED[1], 0.3, b[1]))
+    torch.cuda.synchronize()
+    for x, y in zip(want, got):
+        for n in x:
+            assert torch.equal(x[n], y[n]), n
+
+
 def test_gpu_refusals():
     dims = moe.Dims(4, 64, 64, 8, 2)
     l = torch.zeros((4, 8), device="cuda")
