@@ -15,8 +15,12 @@
 // consecutive tokens per lane) come from transposing LDS reads
 // (ds_read_b64_tr_b16), as Wg's do in dx. Those reads are written as assembly
 // that waits for its own results: for the builtin the compiler waits until no
-// load into LDS is in flight, which takes the loads' lead away (dWg 73 us at
-// 4096 x 7168 x 256 where this form takes TIME_DWG).
+// load into LDS is in flight, which takes the loads' lead away.
+//
+// Measured at 4096 x 7168 x 256: dWg 46 us (45 GFLOP in bf16, 980 TFLOP/s; its
+// matrix products alone take 20 us of matrix-core time, the loads alone about 26
+// us, and they overlap in part), dx with dWg's parts 39 us (118 MB, 3.0 TB/s; 30
+// GFLOP), the split 6 us.
 #include "common.h"
 #include "router.h"
 
@@ -24,7 +28,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kSub = 32;     // K of one MFMA
+constexpr int kStep = 32;    // K of one step (one MFMA)
 constexpr int kRowsX = 128;  // tokens per dx workgroup
 constexpr int kColsX = 128;  // columns per dx workgroup
 
@@ -77,47 +81,44 @@ __device__ __forceinline__ void tr_read(const char* tile, const uint32_t (&at)[8
   for (int i = 0; i < 4; ++i)
     frag[i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(r[2 * i], r[2 * i + 1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
-// Rows of CPR 16-byte chunks (8 K values each): chunk c of row r in slot
-// c ^ row_swz(r), so that 16 rows' reads of one chunk touch all banks.
-template <int CPR>
+// Stage rows of 32 K values, four 16-byte chunks: chunk c of row r in slot
+// c ^ row_swz(r), so that a fragment's reads (lane l: row l % 16, chunk l / 16)
+// touch all banks evenly, both for 16 consecutive lanes and for the lanes the
+// hardware takes together in a 16-byte read (0-3, 12-15, 20-27; 4-11, 16-19,
+// 28-31; the same above 32): no conflicts counted, where c ^ (r / 4) % 4 doubled
+// the reads' time.
 __device__ __forceinline__ int row_swz(int r) {
-  static_assert(CPR == 4 || CPR == 8, "rows of 64 or 128 bytes");
-  return (r / (16 / CPR)) % CPR;
+  const int q = (r / 4) % 4;  // 0, 2, 3, 1 for q = 0 .. 3
+  return (q >> 1) | (((q ^ (q >> 1)) & 1) << 1);
 }
-template <int CPR>
-__device__ __forceinline__ bf16x8_t row_frag(const char* tile, int row0, int sub) {
+__device__ __forceinline__ bf16x8_t row_frag(const char* tile, int row0) {
   const int lane = threadIdx.x & 63, r = row0 + lane % 16;
-  return *reinterpret_cast<const bf16x8_t*>(tile + r * (CPR * 16) + ((4 * sub + lane / 16) ^ row_swz<CPR>(r)) * 16);
+  return *reinterpret_cast<const bf16x8_t*>(tile + r * (kStep * 2) + ((lane / 16) ^ row_swz(r)) * 16);
 }
 
-// One step's products: acc[i][j] += (transposed fragment i) x (row fragment j)
-// over kSteps / 32 sub-steps, summed over the planes, the smallest first; a
-// plane's fragments are read while the one before it multiplies.
-template <int kPlanes, int kStep, int BCPR>
+// One step's products: acc[i][j] += (transposed fragment i) x (row fragment j),
+// summed over the planes, the smallest first; a plane's fragments are read while
+// the one before it multiplies.
+template <int kPlanes>
 __device__ __forceinline__ void step_products(const char* rows, int plane_bytes, int row0, const char* cols,
                                               const uint32_t (&at)[8], f32x4_t (&acc)[4][4]) {
-  constexpr int CPR = kStep / 8;
+  bf16x8_t b[4], a[2][4];
+  tr_read(cols, at, b);
 #pragma unroll
-  for (int s = 0; s < kStep / kSub; ++s) {
-    bf16x8_t b[4], a[2][4];
-    tr_read(cols + s * (kSub * BCPR * 16), at, b);
+  for (int j = 0; j < 4; ++j) a[0][j] = row_frag(rows + (kPlanes - 1) * plane_bytes, row0 + j * 16);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) a[0][j] = row_frag<CPR>(rows + (kPlanes - 1) * plane_bytes, row0 + j * 16, s);
+  for (int p = 0; p < kPlanes; ++p) {
+    if (p + 1 < kPlanes) {
 #pragma unroll
-    for (int p = 0; p < kPlanes; ++p) {
-      if (p + 1 < kPlanes) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          a[(p + 1) & 1][j] = row_frag<CPR>(rows + (kPlanes - 2 - p) * plane_bytes, row0 + j * 16, s);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i], a[p & 1][j], acc[i][j], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < 4; ++j) a[(p + 1) & 1][j] = row_frag(rows + (kPlanes - 2 - p) * plane_bytes, row0 + j * 16);
     }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i], a[p & 1][j], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -128,14 +129,14 @@ __device__ __forceinline__ int xcd_tile(int id, int n) {
   return id < 8 * per ? (id % 8) * per + id / 8 : id;
 }
 
-// One pipelined K loop: `issue(step, buffer)` starts a step's loads (PER of them
+// One pipelined K loop: `issue(buffer)` starts the next step's loads (PER of them
 // per wave) into one of NST stage buffers, `work(buffer)` multiplies it. The
 // loads run NST - 1 steps ahead; a step's own are the oldest in flight.
 template <int NST, int PER, int kStage, typename Issue, typename Work>
 __device__ __forceinline__ void pipeline(int steps, char* lds, Issue&& issue, Work&& work) {
 #pragma unroll
   for (int p = 0; p < NST - 1; ++p)
-    if (p < steps) issue(p, lds + p * kStage);
+    if (p < steps) issue(lds + p * kStage);
   int buf = 0, ahead = NST - 1;
   for (int st = 0; st < steps; ++st) {
     if (st + NST - 2 < steps)
@@ -144,16 +145,19 @@ __device__ __forceinline__ void pipeline(int steps, char* lds, Issue&& issue, Wo
       wait_vmcnt<0>();
     wait_lds_reads();  // of the step before: its buffer is refilled below
     lds_barrier();
-    if (st + NST - 1 < steps) issue(st + NST - 1, lds + ahead * kStage);
+    if (st + NST - 1 < steps) issue(lds + ahead * kStage);
     work(lds + buf * kStage);
     buf = buf + 1 == NST ? 0 : buf + 1;
     ahead = ahead + 1 == NST ? 0 : ahead + 1;
   }
 }
 
-// One 64-token x 64-expert block: dl -> rows [2][Tp][Ep] (hi, mid: dx's operand)
-// and cols [3][Ep][Tp] (all planes, transposed through LDS: dWg's), zero past T
-// and E, and the block's column sums.
+// One 64-token x 64-expert block: dl -> rows [Ep / 32][2][Tp][32] (hi, mid by
+// blocks of 32 experts: dx's operand) and cols [Tp / 32][3][Ep][32] (all planes
+// by blocks of 32 tokens, transposed through LDS: dWg's), zero past T and E, and
+// the block's column sums. A step's operand is thus one contiguous piece per
+// plane; in plain rows a tile's 128 rows lie a power of two apart and meet in
+// few of the L2's channels.
 constexpr int kBlk = 64;
 __global__ __launch_bounds__(256) void split_kernel(const float* __restrict__ dl, int64_t T, int E, int64_t Tp, int Ep,
                                                     bf16_t* __restrict__ rows, bf16_t* __restrict__ cols,
@@ -197,7 +201,7 @@ __global__ __launch_bounds__(256) void split_kernel(const float* __restrict__ dl
   for (int pl = 0; pl < 2; ++pl)
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      *reinterpret_cast<uint2*>(rows + (pl * Tp + tb + rg + r) * Ep + e) =
+      *reinterpret_cast<uint2*>(rows + ((e / kStep * 2 + pl) * Tp + tb + rg + r) * kStep + e % kStep) =
           make_uint2(p[pl][r][0] | (p[pl][r][1] << 16), p[pl][r][2] | (p[pl][r][3] << 16));
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -213,7 +217,7 @@ __global__ __launch_bounds__(256) void split_kernel(const float* __restrict__ dl
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int r = q * 32 + threadIdx.x / 8, c = (threadIdx.x % 8) * 8;
-      *reinterpret_cast<u32x4_t*>(cols + (static_cast<int64_t>(pl) * Ep + eb + r) * Tp + tb + c) =
+      *reinterpret_cast<u32x4_t*>(cols + (((tb + c) / kStep * 3 + pl) * Ep + eb + r) * kStep + c % kStep) =
           *reinterpret_cast<const u32x4_t*>(&tr[pl][r * kPitch + c]);
     }
   if (threadIdx.x < kBlk && eb + static_cast<int>(threadIdx.x) < E) {
@@ -225,8 +229,8 @@ __global__ __launch_bounds__(256) void split_kernel(const float* __restrict__ dl
 }
 
 // A BM-expert x BN-column tile of one part of the tokens: out[part][e][n].
-// WM x WN waves, each 64 experts x 64 columns.
-template <int BM, int BN, int kStep, int NST>
+// BM / 64 x BN / 64 waves, each 64 experts x 64 columns.
+template <int BM, int BN, int NST>
 __global__ __launch_bounds__(BM / 64 * (BN / 64) * 64, 1) void dwg_kernel(const bf16_t* __restrict__ x,
                                                                        const bf16_t* __restrict__ cols, int64_t T,
                                                                        int64_t d, int E, int64_t Tp, int Ep,
@@ -252,24 +256,37 @@ __global__ __launch_bounds__(BM / 64 * (BN / 64) * 64, 1) void dwg_kernel(const 
   const int s0 = part * (steps / parts) + min(part, steps % parts);
   const int n_steps = steps / parts + (part < steps % parts);
 
-  auto issue = [&](int st, char* dst) {
-    const int64_t t = static_cast<int64_t>(s0 + st) * kStep;
-    const __amdgpu_buffer_rsrc_t rx = rsrc(x + t * d + n0, ((T - t) * d - n0) * 2);
+  // Operand bases of the next step to load, advanced as steps are issued (in
+  // order): one 64-bit addition each in front of a step's loads.
+  const int64_t t0 = static_cast<int64_t>(s0) * kStep;
+  const bf16_t* xb = x + t0 * d + n0;
+  int64_t x_bytes = ((T - t0) * d - n0) * 2;  // to x's end: rows past T read as zeros
+  const bf16_t* cb = cols + (static_cast<int64_t>(s0) * 3 * Ep + e0) * kStep;
+  uint32_t aoff[AI], boff[BI];
+#pragma unroll
+  for (int i = 0; i < AI; ++i) {
+    constexpr int IPP = BM / 16;  // instructions per plane, 16 rows of 64 bytes each
+    const int r = ((wv * AI + i) % IPP) * 16 + lane / 4;
+    aoff[i] = static_cast<uint32_t>((r * 4 + ((lane % 4) ^ row_swz(r))) * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < BI; ++i) {
+    constexpr int RPI = 64 / BCPR;
+    const int r = (wv * BI + i) * RPI + lane / BCPR;
+    boff[i] = static_cast<uint32_t>(r * d * 2 + (((lane % BCPR) ^ kn_swz(r)) % BCPR) * 16);
+  }
+  auto issue = [&](char* dst) {
+    const __amdgpu_buffer_rsrc_t rx = rsrc(xb, x_bytes);
 #pragma unroll
     for (int i = 0; i < AI; ++i) {
-      constexpr int CPR = kStep / 8, RPI = 64 / CPR, IPP = BM / RPI;  // rows per instruction, instructions per plane
-      const int q = wv * AI + i, pl = q / IPP, r = (q % IPP) * RPI + lane / CPR;
-      const bf16_t* base = cols + (static_cast<int64_t>(pl) * Ep + e0) * Tp + t;
-      load_lds16(rsrc(base, (static_cast<int64_t>(BM) * Tp - t) * 2), dst + q * 1024,
-                 static_cast<uint32_t>(r * Tp * 2 + ((lane % CPR) ^ row_swz<CPR>(r)) * 16));
+      const int q = wv * AI + i, pl = q / (BM / 16);
+      load_lds16(rsrc(cb + pl * Ep * kStep, BM * kStep * 2), dst + q * 1024, aoff[i]);
     }
 #pragma unroll
-    for (int i = 0; i < BI; ++i) {
-      constexpr int RPI = 64 / BCPR;
-      const int q = wv * BI + i;
-      const int r = q * RPI + lane / BCPR, c = ((lane % BCPR) ^ kn_swz(r)) % BCPR;
-      load_lds16(rx, dst + kA + q * 1024, static_cast<uint32_t>(r * d * 2 + c * 16));
-    }
+    for (int i = 0; i < BI; ++i) load_lds16(rx, dst + kA + (wv * BI + i) * 1024, boff[i]);
+    xb += kStep * d;
+    x_bytes -= kStep * d * 2;
+    cb += 3 * Ep * kStep;
   };
   f32x4_t acc[4][4];  // [column block][expert block]
 #pragma unroll
@@ -279,7 +296,7 @@ __global__ __launch_bounds__(BM / 64 * (BN / 64) * 64, 1) void dwg_kernel(const 
   uint32_t at[8];
   tr_offsets<BCPR>(wn * 64, at);
   pipeline<NST, PER, kStage>(n_steps, lds, issue, [&](const char* cur) {
-    step_products<3, kStep, BCPR>(cur, kPlane, wm * 64, cur + kA, at, acc);
+    step_products<3>(cur, kPlane, wm * 64, cur + kA, at, acc);
   });
   // accumulator of lane l: columns 4 (l / 16) .. + 3 of expert l % 16
   float* o = out + static_cast<int64_t>(part) * E * d;
@@ -334,7 +351,7 @@ __device__ __forceinline__ void sum_group(const SumArgs& a, int group, int E, ch
 }
 
 // One 128-token x 128-column tile of dx: K = the experts, planes hi and mid.
-template <int kStep, int NST>
+template <int NST>
 __global__ __launch_bounds__(256) void gate_dx_kernel(const bf16_t* __restrict__ rows, const bf16_t* __restrict__ wg,
                                                       const bf16_t* dx_in, int64_t T, int64_t d, int E, int64_t Tp,
                                                       int Ep, bf16_t* dx, int ncols, int tiles, SumArgs sum) {
@@ -348,25 +365,34 @@ __global__ __launch_bounds__(256) void gate_dx_kernel(const bf16_t* __restrict__
   const int64_t n0 = static_cast<int64_t>(tile % ncols) * kColsX;
   const int64_t t0 = static_cast<int64_t>(tile / ncols) * kRowsX;
 
-  auto issue = [&](int st, char* dst) {
-    const int k0 = st * kStep;
-    const __amdgpu_buffer_rsrc_t rw = rsrc(wg + k0 * d + n0, ((E - k0) * d - n0) * 2);
+  // operand bases of the next step to load, as in dwg_kernel
+  const bf16_t* wb = wg + n0;
+  int64_t w_bytes = (E * d - n0) * 2;  // rows past E read as zeros
+  const bf16_t* rb = rows + t0 * kStep;
+  uint32_t aoff[AI], boff[BI];
+#pragma unroll
+  for (int i = 0; i < AI; ++i) {
+    const int r = ((wv * AI + i) % (2 * AI)) * 16 + lane / 4;
+    aoff[i] = static_cast<uint32_t>((r * 4 + ((lane % 4) ^ row_swz(r))) * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < BI; ++i) {
+    constexpr int RPI = 64 / BCPR;
+    const int r = (wv * BI + i) * RPI + lane / BCPR;
+    boff[i] = static_cast<uint32_t>(r * d * 2 + (((lane % BCPR) ^ kn_swz(r)) % BCPR) * 16);
+  }
+  auto issue = [&](char* dst) {
+    const __amdgpu_buffer_rsrc_t rw = rsrc(wb, w_bytes);
 #pragma unroll
     for (int i = 0; i < AI; ++i) {
-      constexpr int CPR = kStep / 8, RPI = 64 / CPR;
       const int q = wv * AI + i, pl = q / (2 * AI);
-      const int r = (q % (2 * AI)) * RPI + lane / CPR, c = (lane % CPR) ^ row_swz<CPR>(r);
-      const bf16_t* base = rows + (static_cast<int64_t>(pl) * Tp + t0) * Ep + k0;
-      load_lds16(rsrc(base, (static_cast<int64_t>(kRowsX) * Ep - k0) * 2), dst + q * 1024,
-                 static_cast<uint32_t>((r * Ep + c * 8) * 2));
+      load_lds16(rsrc(rb + pl * Tp * kStep, kRowsX * kStep * 2), dst + q * 1024, aoff[i]);
     }
 #pragma unroll
-    for (int i = 0; i < BI; ++i) {
-      constexpr int RPI = 64 / BCPR;
-      const int q = wv * BI + i;
-      const int r = q * RPI + lane / BCPR, c = ((lane % BCPR) ^ kn_swz(r)) % BCPR;
-      load_lds16(rw, dst + kA + q * 1024, static_cast<uint32_t>(r * d * 2 + c * 16));
-    }
+    for (int i = 0; i < BI; ++i) load_lds16(rw, dst + kA + (wv * BI + i) * 1024, boff[i]);
+    wb += kStep * d;
+    w_bytes -= kStep * d * 2;
+    rb += 2 * Tp * kStep;
   };
   f32x4_t acc[4][4];  // [column block][token block]
 #pragma unroll
@@ -376,13 +402,13 @@ __global__ __launch_bounds__(256) void gate_dx_kernel(const bf16_t* __restrict__
   uint32_t at[8];
   tr_offsets<BCPR>(wn * 64, at);
   pipeline<NST, PER, kStage>((E + kStep - 1) / kStep, lds, issue, [&](const char* cur) {
-    step_products<2, kStep, BCPR>(cur, kPlane, wm * 64, cur + kA, at, acc);
+    step_products<2>(cur, kPlane, wm * 64, cur + kA, at, acc);
   });
   // Accumulator of lane l: columns 4 (l / 16) .. + 3 of token l % 16. Through the
   // stage buffers (a wave's own 16 x 64 block at a time) to eight consecutive
   // columns per lane, so that loads and stores are whole 128-byte lines: with
   // the 8-byte accesses of the accumulator layout reading dx_in and writing dx
-  // took 38 us at 4096 x 7168, this way TIME_EPI.
+  // took 38 us at 4096 x 7168 x 32, this way 25.
   constexpr int kPitch = 64 + 4;
   __syncthreads();  // every wave has read the last stage
   float* ct = reinterpret_cast<float*>(lds) + wv * (16 * kPitch);
@@ -432,13 +458,13 @@ __global__ __launch_bounds__(256) void gate_dx_kernel(const bf16_t* __restrict__
 // with eight.
 constexpr int kColsW = 256;
 int dwg_rows(int E) { return E <= 64 ? 64 : 128; }
-constexpr int kStepW = 64, kStagesW = 2, kStepX = 32, kStagesX = 2;
+constexpr int kStagesW = 3, kStagesX = 2;
 
 struct GateWs {
   int64_t Tp, blocks, steps, ncols;
   int Ep, bm, parts;
-  bf16_t* rows;  // [2][Tp][Ep]
-  bf16_t* cols;  // [3][Ep][Tp]
+  bf16_t* rows;  // [Ep / 32][2][Tp][32]
+  bf16_t* cols;  // [Tp / 32][3][Ep][32]
   float* bpart;
   float* part;  // null when one part: the sums go straight to dwg
 };
@@ -450,7 +476,7 @@ size_t layout(int64_t T, int64_t d, int E, void* ws, GateWs* g) {
   g->Ep = static_cast<int>(up(E, g->bm));
   g->Tp = up(T, kRowsX);
   g->blocks = g->Tp / kBlk;
-  g->steps = (T + kStepW - 1) / kStepW;
+  g->steps = (T + kStep - 1) / kStep;
   g->ncols = (d + kColsW - 1) / kColsW;
   // token parts: as many as one round of 256 workgroups takes, at least 4 steps to each
   const int64_t tiles = g->ncols * (g->Ep / g->bm);
@@ -488,9 +514,9 @@ hipError_t launch_gate_backward(const void* x, const void* wg, const float* dlog
   const int etiles = g.Ep / g.bm;
   const dim3 grid(static_cast<unsigned>(g.ncols * etiles * g.parts));
   if (g.bm == 64) {
-    hipLaunchKernelGGL((dwg_kernel<64, kColsW, kStepW, kStagesW>), grid, dim3(256), 0, s, xb, g.cols, T, d, E, g.Tp, g.Ep, static_cast<int>(g.steps), etiles, g.parts, o);
+    hipLaunchKernelGGL((dwg_kernel<64, kColsW, kStagesW>), grid, dim3(256), 0, s, xb, g.cols, T, d, E, g.Tp, g.Ep, static_cast<int>(g.steps), etiles, g.parts, o);
   } else {
-    hipLaunchKernelGGL((dwg_kernel<128, kColsW, kStepW, kStagesW>), grid, dim3(512), 0, s, xb, g.cols, T, d, E, g.Tp, g.Ep, static_cast<int>(g.steps), etiles, g.parts, o);
+    hipLaunchKernelGGL((dwg_kernel<128, kColsW, kStagesW>), grid, dim3(512), 0, s, xb, g.cols, T, d, E, g.Tp, g.Ep, static_cast<int>(g.steps), etiles, g.parts, o);
   }
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   SumArgs sum{};
@@ -506,7 +532,7 @@ hipError_t launch_gate_backward(const void* x, const void* wg, const float* dlog
   sum.groups = sum.bias_groups + (g.parts > 1 ? static_cast<int>(want < 2048 ? want : 2048) : 0);
   const int ncols = static_cast<int>((d + kColsX - 1) / kColsX);
   const int64_t tiles = ncols * (g.Tp / kRowsX);
-  hipLaunchKernelGGL((gate_dx_kernel<kStepX, kStagesX>), dim3(static_cast<unsigned>(tiles + sum.groups)), dim3(256), 0,
+  hipLaunchKernelGGL(gate_dx_kernel<kStagesX>, dim3(static_cast<unsigned>(tiles + sum.groups)), dim3(256), 0,
                      s, g.rows, static_cast<const bf16_t*>(wg), static_cast<const bf16_t*>(dx_in), T, d, E, g.Tp, g.Ep,
                      static_cast<bf16_t*>(dx), ncols, static_cast<int>(tiles), sum);
   return hipGetLastError();
