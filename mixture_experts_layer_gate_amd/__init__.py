@@ -2,10 +2,12 @@
 
 Route (gate GEMM + top-k softmax), dispatch (histogram, scan, stable
 permutation), grouped SwiGLU expert FFN and weighted combine, and the layer's
-gradients (DGrad, WGrad, routing-weight and gate gradients), each a
-hand-written HIP kernel for gfx950 behind the C-ABI declared in
-``include/moe.h``. The Python functions here only marshal torch tensors into
-that ABI; the library is loaded on first use and a missing build is an error.
+gradients (DGrad, WGrad, routing-weight and gate gradients); a scored router
+(softmax or sigmoid scores, balance bias, groups) with its balance losses and
+gradients; and dropout beside the combine. Each is a hand-written HIP kernel for
+gfx950 behind the C-ABI declared in ``include/moe.h``. The Python functions here
+only marshal torch tensors into that ABI; the library is loaded on first use and
+a missing build is an error.
 """
 from .api import (  # noqa: F401
     MoeError, Dims, workspace_bytes, route, permute, grouped_ffn, combine, layer_forward,
