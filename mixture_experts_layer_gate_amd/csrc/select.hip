@@ -741,7 +741,9 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
         dot += sh[i] * gl[i];
       }
       dot = wave_sum(dot);
-      const float cz = dlosses[1] * 2.0f / static_cast<float>(q.covered) * (m + logf(zs)) * inv_z;
+      // (kept finite, so that an expert of share 0 gets 0 where lse is the largest logit there is)
+      const float cz = fminf(fmaxf(dlosses[1] * 2.0f / static_cast<float>(q.covered) * (m + logf(zs)) * inv_z, -kF32Max),
+                             kF32Max);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         float v = sh[i] * (gl[i] - dot);
@@ -765,9 +767,10 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
 }
 
 // ---------------------------------------------------------------- losses ----
-// Part r of sequence s: its rows' shares p~ summed per expert (fp32 over at
-// most a few dozen rows per wave; the parts are then summed in double), the
-// loads counted (integers, any order gives the same), and sum lse^2 (double).
+// Part r of sequence s: its rows' shares p~ summed per expert in double (a part
+// of a batch of millions of rows has thousands to a wave) and rounded once to
+// fp32, the loads counted (integers, any order gives the same), and sum lse^2 in
+// double. The parts are then summed in double.
 template <int VPL>
 __global__ __launch_bounds__(256) void balance_part_kernel(SelectOpts o, const float* __restrict__ logits,
                                                            const int32_t* __restrict__ idx,
@@ -775,7 +778,7 @@ __global__ __launch_bounds__(256) void balance_part_kernel(SelectOpts o, const f
                                                            float* __restrict__ part_p, int32_t* __restrict__ part_f,
                                                            double* __restrict__ part_z, uint32_t* __restrict__ done) {
   __shared__ int32_t cnt[64 * VPL];
-  __shared__ float psum[4][64 * VPL];
+  __shared__ double psum[4][64 * VPL];
   __shared__ double zsum[4];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int r = blockIdx.x, s = blockIdx.y, parts = gridDim.x;
@@ -785,9 +788,9 @@ __global__ __launch_bounds__(256) void balance_part_kernel(SelectOpts o, const f
   const int lo = a + static_cast<int>(n * r / parts), hi = a + static_cast<int>(n * (r + 1) / parts);
   for (int e = threadIdx.x; e < 64 * VPL; e += 256) cnt[e] = 0;
   __syncthreads();
-  float acc[VPL];
+  double acc[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
+  for (int i = 0; i < VPL; ++i) acc[i] = 0.0;
   double zacc = 0.0;
   // two rows at a time: their loads and their reductions' latencies overlap
   for (int64_t t = lo + wv; t < hi; t += 8) {
@@ -848,7 +851,7 @@ __global__ __launch_bounds__(256) void balance_part_kernel(SelectOpts o, const f
   __syncthreads();
   const int64_t base = (static_cast<int64_t>(s) * parts + r) * E;
   for (int e = threadIdx.x; e < E; e += 256) {
-    part_p[base + e] = ((psum[0][e] + psum[1][e]) + psum[2][e]) + psum[3][e];
+    part_p[base + e] = static_cast<float>(((psum[0][e] + psum[1][e]) + psum[2][e]) + psum[3][e]);
     part_f[base + e] = cnt[e];
   }
   if (threadIdx.x == 0) part_z[static_cast<int64_t>(s) * parts + r] = ((zsum[0] + zsum[1]) + zsum[2]) + zsum[3];

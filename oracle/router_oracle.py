@@ -192,6 +192,7 @@ def philox4x32(counter, key, rounds=10):
 def keep_mask(n, seed, offset, p):
     """Keep decisions of elements 0 .. n-1 (bool)."""
     thr = round(p * 65536)
+    seed, offset = seed % 2 ** 64, offset % 2 ** 64  # the 64 bits of a signed value
     out = np.zeros(n, bool)
     for i in range((n + 7) // 8):
         words = philox4x32([i % 2 ** 32, i >> 32, offset % 2 ** 32, offset >> 32], [seed % 2 ** 32, seed >> 32])

@@ -106,6 +106,10 @@ SELECT = [
     (50, 200, 8, "softmax", 4, 4, "max", True, 1.0, None, "masked"),
     (300, 16, 4, "softmax", 1, 1, "max", False, 1.0, None, "plain"),
     (300, 30, 6, "sigmoid", 3, 2, "top2", True, 1.0, "masked", "plain"),
+    (90, 128, 8, "sigmoid", 8, 3, "max", True, 1.0, "big", "plain"),
+    (90, 200, 5, "softmax", 1, 1, "max", False, 1.0, "big", "plain"),
+    (64, 256, 8, "softmax", 2, 1, "top2", True, 1.0, "small", "plain"),
+    (64, 99, 3, "sigmoid", 33, 20, "max", True, 1.0, "small", "plain"),
 ]
 
 
@@ -118,6 +122,9 @@ def _bias(rng, E, kind):
         b[rng.integers(E)] = NAN
     if kind == "inf":
         b[rng.permutation(E)[:3]] = INF
+    if kind == "big":  # fp32 keys would round to steps of 2^-14 (or 2^-4 above 2^20)
+        b = (1000.0 + 0.01 * rng.standard_normal(E)).astype(np.float32)
+        b[:2] += 2.0 ** 20
     return b
 
 
@@ -318,6 +325,32 @@ def test_backward_repeated_and_foreign_indices(rng):
     assert int(load.sum()) == T * k - 2
 
 
+def test_losses_alone(rng):
+    """The losses' gradient without a selection's: the difference of the other two."""
+    T, E, k = 77, 40, 3
+    l, dims = torch.from_numpy(_logits(rng, T, E, "plain")).cuda(), moe.Dims(77, 64, 64, 40, 3)
+    for opts in (moe.RouteOptions("sigmoid"), moe.RouteOptions(renormalise=False)):
+        idx, w = moe.route_select(dims, opts, l)
+        up = torch.tensor([0.5, 0.25], device="cuda")
+        _, load = moe.balance_loss(dims, opts, l, idx)
+        dw = torch.ones((T, k), device="cuda").cumsum(1)
+        both = moe.route_select_backward(dims, opts, l, idx, w, dw, up, load)
+        sel = moe.route_select_backward(dims, opts, l, idx, w, dw)
+        alone = moe.route_select_backward(dims, opts, l, None, None, None, up, load)
+        torch.testing.assert_close(both - sel, alone, rtol=0, atol=4 * 3 * U)  # elements below 3, two roundings
+
+
+def test_an_expert_of_no_share_gets_no_gradient():
+    """One row whose largest logit is the largest there is: the others' gradients are 0, not NaN."""
+    l = torch.tensor([[INF, 0.0, -INF, 1.0]], device="cuda")
+    dims, opts = moe.Dims(1, 64, 64, 4, 1), moe.RouteOptions()
+    idx, w = moe.route_select(dims, opts, l)
+    _, load = moe.balance_loss(dims, opts, l, idx)
+    dl = moe.route_select_backward(dims, opts, l, idx, w, torch.ones((1, 1), device="cuda"),
+                                   torch.tensor([1.0, 1.0], device="cuda"), load)
+    assert idx.tolist() == [[0]] and dl[0, 1:].tolist() == [0, 0, 0] and float(dl[0, 0]) > 1e38
+
+
 def test_losses_of_an_empty_batch():
     dims = moe.Dims(0, 64, 64, 12, 2)
     lg, ix = torch.empty((0, 12), device="cuda"), torch.empty((0, 2), dtype=torch.int32, device="cuda")
@@ -421,7 +454,7 @@ DROP = [(1, 8, 1, 0.1, True), (1, 6144, 2, 0.1, True), (7, 1048, 4, 0.25, False)
 def test_combine_dropout(case, dtype, rng):
     T, d, k, p, with_res = case
     _say(f"combine_dropout {case} {dtype}")
-    seed, off = int(rng.integers(0, 2 ** 63 - 1)), int(rng.integers(0, 2 ** 63 - 1))
+    seed, off = int(rng.integers(-2 ** 63, 2 ** 63 - 1)), int(rng.integers(-2 ** 63, 2 ** 63 - 1))
     r = torch.tensor([seed, off], dtype=torch.int64, device="cuda")
     mk = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).cuda().to(dtype)  # noqa: E731
     y, res, dout = mk(T * k, d), (mk(T, d) if with_res else None), mk(T, d)
