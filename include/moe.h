@@ -493,7 +493,8 @@ int moe_route_select_backward(const moe_dims_t* dims, const moe_route_opts_t* op
 
 /* Gradients of the gate GEMM for a dense logit gradient:
  *   dx = dx_in + dlogits Wg (bf16, one rounding), dwg = dlogits^T x, dbias = column sums (fp32)
- * x [T][d], wg [E][d], dx_in [T][d] or NULL, dx [T][d] bf16 (may be dx_in);
+ * x [T][d], wg [E][d], dx_in [T][d] or NULL, dx [T][d] bf16 (may be dx_in, and
+ * overlaps nothing else);
  * dlogits [T][E], dwg [E][d], dbias [E] fp32. bf16 only, d % 8 == 0, T <=
  * 4194176, d <= 2^24 and (T/128 + 1)(d/128 + 1) < 2^23 (MOE_ERR_UNSUPPORTED otherwise). T = 0 writes zero dwg and
  * dbias. dwg's products are exact and its sums fp32; fixed summation order.

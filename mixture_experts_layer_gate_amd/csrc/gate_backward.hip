@@ -228,26 +228,42 @@ __global__ __launch_bounds__(256) void split_kernel(const float* __restrict__ dl
   }
 }
 
+struct GateArgs {
+  const bf16_t* x;
+  const bf16_t* wg;
+  const bf16_t* dx_in;
+  bf16_t* dx;
+  const bf16_t* rows;  // split_kernel's outputs
+  const bf16_t* cols;
+  float* out;  // dwg, or its parts [parts][E][d]
+  int64_t T, d, Tp;
+  int E, Ep;
+  int steps, etiles, parts, w_tiles;  // dWg: 32-token steps, expert tiles, token parts, tiles in all
+  int ncols, x_tiles;                 // dx: column tiles, tiles in all
+};
+
 // A BM-expert x BN-column tile of one part of the tokens: out[part][e][n].
 // BM / 64 x BN / 64 waves, each 64 experts x 64 columns.
 template <int BM, int BN, int NST>
-__global__ __launch_bounds__(BM / 64 * (BN / 64) * 64, 1) void dwg_kernel(const bf16_t* __restrict__ x,
-                                                                       const bf16_t* __restrict__ cols, int64_t T,
-                                                                       int64_t d, int E, int64_t Tp, int Ep,
-                                                                       int steps, int etiles, int parts,
-                                                                       float* __restrict__ out) {
+struct DwgTile {
+  static constexpr int kPlane = kStep * BM * 2, kA = 3 * kPlane, kB = kStep * BN * 2, kStage = kA + kB;
+  static constexpr int kLds = NST * kStage;
+  __device__ static __forceinline__ void run(const GateArgs& g, int id, char* lds);
+};
+template <int BM, int BN, int NST>
+__device__ __forceinline__ void DwgTile<BM, BN, NST>::run(const GateArgs& g, int id, char* lds) {
+  const int64_t T = g.T, d = g.d;
+  const int E = g.E, Ep = g.Ep, steps = g.steps, etiles = g.etiles, parts = g.parts;
   constexpr int WN = BN / 64, NW = BM / 64 * WN;
   constexpr int BCPR = BN / 8;  // 16-byte chunks of a stage row of x
-  constexpr int kPlane = kStep * BM * 2, kA = 3 * kPlane, kB = kStep * BN * 2, kStage = kA + kB;
   constexpr int AI = kA / 1024 / NW, BI = kB / 1024 / NW, PER = AI + BI;  // load instructions of a wave
   static_assert(AI * NW * 1024 == kA && BI * NW * 1024 == kB, "every wave loads as much");
-  __shared__ __attribute__((aligned(1024))) char lds[NST * kStage];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv / WN, wn = wv % WN;
   // expert tiles of one column block next to each other (they read the same x),
   // parts outermost (an XCD's tiles then read one or two parts of the planes,
   // which its L2 holds)
-  const int tile = xcd_tile(blockIdx.x, gridDim.x);
+  const int tile = xcd_tile(id, g.w_tiles);
   const int e0 = tile % etiles * BM;
   const int ncols = static_cast<int>((d + BN - 1) / BN);
   const int64_t n0 = static_cast<int64_t>(tile / etiles % ncols) * BN;
@@ -259,9 +275,9 @@ __global__ __launch_bounds__(BM / 64 * (BN / 64) * 64, 1) void dwg_kernel(const 
   // Operand bases of the next step to load, advanced as steps are issued (in
   // order): one 64-bit addition each in front of a step's loads.
   const int64_t t0 = static_cast<int64_t>(s0) * kStep;
-  const bf16_t* xb = x + t0 * d + n0;
+  const bf16_t* xb = g.x + t0 * d + n0;
   int64_t x_bytes = ((T - t0) * d - n0) * 2;  // to x's end: rows past T read as zeros
-  const bf16_t* cb = cols + (static_cast<int64_t>(s0) * 3 * Ep + e0) * kStep;
+  const bf16_t* cb = g.cols + (static_cast<int64_t>(s0) * 3 * Ep + e0) * kStep;
   uint32_t aoff[AI], boff[BI];
 #pragma unroll
   for (int i = 0; i < AI; ++i) {
@@ -299,7 +315,7 @@ __global__ __launch_bounds__(BM / 64 * (BN / 64) * 64, 1) void dwg_kernel(const 
     step_products<3>(cur, kPlane, wm * 64, cur + kA, at, acc);
   });
   // accumulator of lane l: columns 4 (l / 16) .. + 3 of expert l % 16
-  float* o = out + static_cast<int64_t>(part) * E * d;
+  float* o = g.out + static_cast<int64_t>(part) * E * d;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int e = e0 + wm * 64 + j * 16 + lane % 16;
@@ -352,23 +368,27 @@ __device__ __forceinline__ void sum_group(const SumArgs& a, int group, int E, ch
 
 // One 128-token x 128-column tile of dx: K = the experts, planes hi and mid.
 template <int NST>
-__global__ __launch_bounds__(256) void gate_dx_kernel(const bf16_t* __restrict__ rows, const bf16_t* __restrict__ wg,
-                                                      const bf16_t* dx_in, int64_t T, int64_t d, int E, int64_t Tp,
-                                                      int Ep, bf16_t* dx, int ncols, int tiles, SumArgs sum) {
-  constexpr int kPlane = kRowsX * kStep * 2, kA = 2 * kPlane, kB = kStep * kColsX * 2, kStage = kA + kB;
+struct DxTile {
+  static constexpr int kPlane = kRowsX * kStep * 2, kA = 2 * kPlane, kB = kStep * kColsX * 2, kStage = kA + kB;
+  static constexpr int kLds = NST * kStage;
+  __device__ static __forceinline__ void run(const GateArgs& g, int tile, char* lds);
+};
+template <int NST>
+__device__ __forceinline__ void DxTile<NST>::run(const GateArgs& g, int tile, char* lds) {
   constexpr int AI = kA / 1024 / 4, BI = kB / 1024 / 4, PER = AI + BI, BCPR = kColsX / 8;
-  __shared__ __attribute__((aligned(1024))) char lds[NST * kStage];
+  const int64_t T = g.T, d = g.d, Tp = g.Tp;
+  const int E = g.E;
+  const bf16_t* dx_in = g.dx_in;
+  bf16_t* dx = g.dx;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv / 2, wn = wv % 2;
-  const int tile = blockIdx.x;
-  if (tile >= tiles) return sum_group(sum, tile - tiles, E, lds);
-  const int64_t n0 = static_cast<int64_t>(tile % ncols) * kColsX;
-  const int64_t t0 = static_cast<int64_t>(tile / ncols) * kRowsX;
+  const int64_t n0 = static_cast<int64_t>(tile % g.ncols) * kColsX;
+  const int64_t t0 = static_cast<int64_t>(tile / g.ncols) * kRowsX;
 
-  // operand bases of the next step to load, as in dwg_kernel
-  const bf16_t* wb = wg + n0;
+  // operand bases of the next step to load, as for dWg
+  const bf16_t* wb = g.wg + n0;
   int64_t w_bytes = (E * d - n0) * 2;  // rows past E read as zeros
-  const bf16_t* rb = rows + t0 * kStep;
+  const bf16_t* rb = g.rows + t0 * kStep;
   uint32_t aoff[AI], boff[BI];
 #pragma unroll
   for (int i = 0; i < AI; ++i) {
@@ -456,85 +476,127 @@ __global__ __launch_bounds__(256) void gate_dx_kernel(const bf16_t* __restrict__
 // Tile forms of dWg: up to 64 experts, 64 x 256 with four waves (x streamed
 // once, the padding experts' products are cheap beside it); beyond, 128 x 256
 // with eight.
-constexpr int kColsW = 256;
-int dwg_rows(int E) { return E <= 64 ? 64 : 128; }
-constexpr int kStagesW = 3, kStagesX = 2;
+constexpr int kColsW = 256, kStagesW = 3, kStagesX = 2;
+template <int BM>
+__global__ __launch_bounds__(BM * kColsW / 64, 1) void dwg_kernel(GateArgs g) {
+  typedef DwgTile<BM, kColsW, kStagesW> Tile;
+  __shared__ __attribute__((aligned(1024))) char lds[Tile::kLds];
+  Tile::run(g, blockIdx.x, lds);
+}
+__global__ __launch_bounds__(256) void gate_dx_kernel(GateArgs g, SumArgs sum) {
+  typedef DxTile<kStagesX> Tile;
+  __shared__ __attribute__((aligned(1024))) char lds[Tile::kLds];
+  const int id = blockIdx.x;
+  if (id < g.x_tiles)
+    Tile::run(g, id, lds);
+  else
+    sum_group(sum, id - g.x_tiles, g.E, lds);
+}
+// dWg in one part, dx and dbias in one launch (short batches).
+__global__ __launch_bounds__(256) void gate_short_kernel(GateArgs g, SumArgs sum) {
+  typedef DwgTile<64, kColsW, 2> W;
+  typedef DxTile<kStagesX> X;
+  __shared__ __attribute__((aligned(1024))) char lds[W::kLds > X::kLds ? W::kLds : X::kLds];
+  const int id = blockIdx.x;
+  if (id < g.w_tiles)
+    W::run(g, id, lds);
+  else if (id < g.w_tiles + g.x_tiles)
+    X::run(g, id - g.w_tiles, lds);
+  else
+    sum_group(sum, id - g.w_tiles - g.x_tiles, g.E, lds);
+}
+
+// One launch for dWg, dx and dbias, each dWg tile over all the tokens: it saves
+// a launch and lets dx run beside dWg, until the tiles' loops over the tokens
+// are longer than split ones and the sum of the parts together. One launch
+// against two, in us, captured, at d = 7168: 16 experts 7.8 / 10.7 at 32 tokens,
+// 12.0 / 14.5 at 256, 17.2 / 15.1 at 512; 256 experts 12.0 / 19.0 at 32, 15.7 /
+// 31.1 at 256, 23.0 / 31.9 at 512. At d = 1024 and 256 experts 19.6 / 24.8 at
+// 512 and 30.8 / 28.0 at 1024.
+bool one_launch(int64_t T, int E) { return T <= (E <= 64 ? 256 : 512); }
 
 struct GateWs {
-  int64_t Tp, blocks, steps, ncols;
-  int Ep, bm, parts;
-  bf16_t* rows;  // [Ep / 32][2][Tp][32]
-  bf16_t* cols;  // [Tp / 32][3][Ep][32]
+  int64_t blocks;
+  int bm;
   float* bpart;
-  float* part;  // null when one part: the sums go straight to dwg
+  GateArgs g;
 };
 
-size_t layout(int64_t T, int64_t d, int E, void* ws, GateWs* g) {
+size_t layout(int64_t T, int64_t d, int E, void* ws, float* dwg, GateWs* w) {
   auto at = [&](size_t off) { return ws ? static_cast<char*>(ws) + off : nullptr; };
   auto pad = [](size_t v) { return (v + 255) / 256 * 256; };
-  g->bm = dwg_rows(E);
-  g->Ep = static_cast<int>(up(E, g->bm));
-  g->Tp = up(T, kRowsX);
-  g->blocks = g->Tp / kBlk;
-  g->steps = (T + kStep - 1) / kStep;
-  g->ncols = (d + kColsW - 1) / kColsW;
+  GateArgs& g = w->g;
+  const bool small = one_launch(T, E);
+  w->bm = small || E <= 64 ? 64 : 128;
+  g.T = T, g.d = d, g.E = E;
+  g.Ep = static_cast<int>(up(E, w->bm));
+  g.Tp = up(T, kRowsX);
+  w->blocks = g.Tp / kBlk;
+  g.steps = static_cast<int>((T + kStep - 1) / kStep);
+  g.etiles = g.Ep / w->bm;
   // token parts: as many as one round of 256 workgroups takes, at least 4 steps to each
-  const int64_t tiles = g->ncols * (g->Ep / g->bm);
-  int64_t parts = 256 / tiles;
-  if (parts > g->steps / 4) parts = g->steps / 4;
-  g->parts = parts < 1 ? 1 : static_cast<int>(parts);
+  const int64_t tiles = (d + kColsW - 1) / kColsW * g.etiles;
+  int64_t parts = small ? 1 : 256 / tiles;
+  if (parts > g.steps / 4) parts = g.steps / 4;
+  g.parts = parts < 1 ? 1 : static_cast<int>(parts);
+  g.w_tiles = static_cast<int>(tiles * g.parts);
+  g.ncols = static_cast<int>((d + kColsX - 1) / kColsX);
+  g.x_tiles = static_cast<int>(g.ncols * (g.Tp / kRowsX));
   size_t off = 0;
-  g->rows = reinterpret_cast<bf16_t*>(at(off));
-  off += pad(size_t(2) * g->Tp * g->Ep * 2);
-  g->cols = reinterpret_cast<bf16_t*>(at(off));
-  off += pad(size_t(3) * g->Tp * g->Ep * 2);
-  g->bpart = reinterpret_cast<float*>(at(off));
-  off += pad(size_t(g->blocks) * E * 4);
-  g->part = g->parts > 1 ? reinterpret_cast<float*>(at(off)) : nullptr;
-  if (g->parts > 1) off += pad(size_t(g->parts) * E * d * 4);
+  g.rows = reinterpret_cast<bf16_t*>(at(off));  // [Ep / 32][2][Tp][32]
+  off += pad(size_t(2) * g.Tp * g.Ep * 2);
+  g.cols = reinterpret_cast<bf16_t*>(at(off));  // [Tp / 32][3][Ep][32]
+  off += pad(size_t(3) * g.Tp * g.Ep * 2);
+  w->bpart = reinterpret_cast<float*>(at(off));
+  off += pad(size_t(w->blocks) * E * 4);
+  g.out = dwg;
+  if (g.parts > 1) {
+    g.out = reinterpret_cast<float*>(at(off));
+    off += pad(size_t(g.parts) * E * d * 4);
+  }
   return off;
 }
 
 }  // namespace
 
 size_t gate_backward_ws(int64_t T, int64_t d, int E) {
-  GateWs g{};
-  return layout(T, d, E, nullptr, &g);
+  GateWs w{};
+  return layout(T, d, E, nullptr, nullptr, &w);
 }
 
 hipError_t launch_gate_backward(const void* x, const void* wg, const float* dlogits, const void* dx_in, void* dx,
                                 float* dwg, float* dbias, int64_t T, int64_t d, int E, void* ws, hipStream_t s) {
-  GateWs g{};
-  layout(T, d, E, ws, &g);
-  const bf16_t* xb = static_cast<const bf16_t*>(x);
-  hipLaunchKernelGGL(split_kernel, dim3(g.Ep / kBlk, static_cast<unsigned>(g.blocks)), dim3(256), 0, s, dlogits, T, E,
-                     g.Tp, g.Ep, g.rows, g.cols, g.bpart);
-  if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
-  float* o = g.parts > 1 ? g.part : dwg;
-  const int etiles = g.Ep / g.bm;
-  const dim3 grid(static_cast<unsigned>(g.ncols * etiles * g.parts));
-  if (g.bm == 64) {
-    hipLaunchKernelGGL((dwg_kernel<64, kColsW, kStagesW>), grid, dim3(256), 0, s, xb, g.cols, T, d, E, g.Tp, g.Ep, static_cast<int>(g.steps), etiles, g.parts, o);
-  } else {
-    hipLaunchKernelGGL((dwg_kernel<128, kColsW, kStagesW>), grid, dim3(512), 0, s, xb, g.cols, T, d, E, g.Tp, g.Ep, static_cast<int>(g.steps), etiles, g.parts, o);
-  }
+  GateWs w{};
+  layout(T, d, E, ws, dwg, &w);
+  GateArgs& g = w.g;
+  g.x = static_cast<const bf16_t*>(x);
+  g.wg = static_cast<const bf16_t*>(wg);
+  g.dx_in = static_cast<const bf16_t*>(dx_in);
+  g.dx = static_cast<bf16_t*>(dx);
+  hipLaunchKernelGGL(split_kernel, dim3(g.Ep / kBlk, static_cast<unsigned>(w.blocks)), dim3(256), 0, s, dlogits, T, E,
+                     g.Tp, g.Ep, const_cast<bf16_t*>(g.rows), const_cast<bf16_t*>(g.cols), w.bpart);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   SumArgs sum{};
-  sum.part = g.part;
+  sum.part = g.out;
   sum.parts = g.parts;
   sum.n4 = static_cast<int64_t>(E) * d / 4;
   sum.dwg = dwg;
-  sum.bpart = g.bpart;
-  sum.blocks = static_cast<int>(g.blocks);
+  sum.bpart = w.bpart;
+  sum.blocks = static_cast<int>(w.blocks);
   sum.dbias = dbias;
   sum.bias_groups = (E + 15) / 16;
   const int64_t want = (sum.n4 + 255) / 256;
   sum.groups = sum.bias_groups + (g.parts > 1 ? static_cast<int>(want < 2048 ? want : 2048) : 0);
-  const int ncols = static_cast<int>((d + kColsX - 1) / kColsX);
-  const int64_t tiles = ncols * (g.Tp / kRowsX);
-  hipLaunchKernelGGL(gate_dx_kernel<kStagesX>, dim3(static_cast<unsigned>(tiles + sum.groups)), dim3(256), 0,
-                     s, g.rows, static_cast<const bf16_t*>(wg), static_cast<const bf16_t*>(dx_in), T, d, E, g.Tp, g.Ep,
-                     static_cast<bf16_t*>(dx), ncols, static_cast<int>(tiles), sum);
+  if (one_launch(T, E)) {
+    hipLaunchKernelGGL(gate_short_kernel, dim3(g.w_tiles + g.x_tiles + sum.groups), dim3(256), 0, s, g, sum);
+    return hipGetLastError();
+  }
+  if (w.bm == 64)
+    hipLaunchKernelGGL(dwg_kernel<64>, dim3(g.w_tiles), dim3(256), 0, s, g);
+  else
+    hipLaunchKernelGGL(dwg_kernel<128>, dim3(g.w_tiles), dim3(512), 0, s, g);
+  if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
+  hipLaunchKernelGGL(gate_dx_kernel, dim3(g.x_tiles + sum.groups), dim3(256), 0, s, g, sum);
   return hipGetLastError();
 }
 
