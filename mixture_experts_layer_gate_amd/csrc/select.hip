@@ -177,9 +177,9 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, f
 
 // LDS of one wave.
 template <int VPL>
-struct SelectLds {
-  uint64_t key[64 * VPL];  // keys by expert; or the candidates' (key, expert)
-  float val[64 * VPL];     // chosen slots' logits (NaN: out of the choice); or the candidates'
+struct __attribute__((aligned(16))) SelectLds {
+  uint64_t key[64 * VPL];  // keys by expert; or the candidates' logits and experts, then the best of them
+  float val[64 * VPL];     // chosen slots' logits (NaN: out of the choice); or the candidates' keys
 };
 
 // Weights of chosen logits v (NaN or -inf: out of the choice) in fp32; a
@@ -385,14 +385,34 @@ __device__ __forceinline__ uint64_t keep_groups(const SelectOpts& o, const V (&c
   return __ballot(head && rank < o.topk_groups);
 }
 
+// A cut that k to 64 of the wave's keys q reach, by bisection from one that more
+// reach; false where equal keys leave none.
+template <int VPL>
+__device__ __forceinline__ bool nearer_cut(const uint32_t (&q)[VPL], int k, uint32_t& cut) {
+  uint32_t lo = __builtin_amdgcn_readfirstlane(cut), hi = 0xffffffffu;  // too many, too few
+  while (hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) n += __popcll(__ballot(q[i] >= mid));
+    if (n >= k && n <= 64) {
+      cut = mid;
+      return true;
+    }
+    (n < k ? hi : lo) = mid;
+  }
+  return false;
+}
+
 // The same selection for k <= 8 from fp32 keys, one wave per token. Returns
-// false (nothing written) for rows with too few experts in the choice to bound
-// the candidates; the caller then takes select_exact.
+// false (nothing written) for rows with too few experts in the choice, or too
+// many equal ones, to bound the candidates; the caller then takes select_exact.
 //
 // Candidates: the lanes fall into 8 classes (lane mod 8), and the smallest of
 // the classes' largest keys has at least 8 keys at or above it; only the keys
 // down to there (8 H_8 = 22 of them on average) are ranked, one per lane, by
-// counting the larger ones.
+// counting the larger ones. Where they are more than 64 (one row of 256 experts
+// in a thousand: a class whose keys are all small) a nearer cut is looked for.
 //
 // Without bias and groups the key is the logit itself and the order exact. With
 // them it is the fp32 score plus the bias: where a chosen expert's key is within
@@ -489,54 +509,78 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
   top = min_step<1>(top);
   top = min_step<2>(top);
   top = min_step<4>(top);
-  float cut = order32_back(top);
-  if (kKeyed) cut -= margin(cut);
-  // (a cut of -inf stays so; NaN, from a class of no experts or +inf, admits all)
-  int n = 0;
-  wave_lds_sync();
+  int n;
+  uint2* const cand = reinterpret_cast<uint2*>(sh.key);  // logit and expert
+  uint32_t* const cand_key = reinterpret_cast<uint32_t*>(sh.val);
+  for (bool again = false;; again = true) {
+    float cut = order32_back(top);
+    if (kKeyed) cut -= margin(cut);
+    // (a cut of -inf stays so; NaN, from a class of no experts or +inf, admits all)
+    n = 0;
+    wave_lds_sync();
+    cand_key[lane] = 0;
+    wave_lds_sync();
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const bool in = e0 + i < E && !(c[i] < cut);
-    const uint64_t mask = __ballot(in);
-    const int at = n + lanes_below(mask);
-    if (in && at < 64) {
-      sh.key[at] = (static_cast<uint64_t>(q[i]) << 32) | static_cast<uint32_t>(E - 1 - (e0 + i));
-      sh.val[at] = l[i];
+    for (int i = 0; i < VPL; ++i) {
+      const bool in = e0 + i < E && !(c[i] < cut);
+      const uint64_t mask = __ballot(in);
+      const int at = n + lanes_below(mask);
+      if (in && at < 64) {
+        cand[at] = make_uint2(__float_as_uint(l[i]), e0 + i);
+        cand_key[at] = q[i];
+      }
+      n += __popcll(mask);
     }
-    n += __popcll(mask);
+    if (n <= 64) break;
+    if (again || !nearer_cut<VPL>(q, k, top)) return false;
   }
-  if (n > 64) return false;
   wave_lds_sync();
   const bool mine = lane < n;
-  const uint64_t key = mine ? sh.key[lane] : 0;
-  float v = mine ? sh.val[lane] : -INFINITY;
-  const int e = E - 1 - static_cast<int>(static_cast<uint32_t>(key));
-  const float cv = order32_back(static_cast<uint32_t>(key >> 32));
+  const uint2 own = cand[lane];
+  float v = mine ? __uint_as_float(own.x) : -INFINITY;
+  const int e = mine ? static_cast<int>(own.y) : 0;
+  const uint32_t key = cand_key[lane];
+  const float cv = order32_back(key);
   const bool live = mine && cv > -INFINITY;
-  // larger candidates; in keyed form also those not clearly smaller
-  const uint32_t low = order32(cv - margin(cv));
-  int rank = 0, near = 0;
-#pragma unroll 4
-  for (int r = 0; r < n; ++r) {
-    const uint64_t kr = sh.key[r];
-    rank += kr > key;
-    if constexpr (kKeyed) near += static_cast<uint32_t>(kr >> 32) >= low;
+  int rank = 0;  // larger candidates (the slots behind the last hold 0)
+#pragma unroll 2
+  for (int r = 0; r < n; r += 4) {
+    const u32x4_t kr = *reinterpret_cast<const u32x4_t*>(cand_key + r);
+    rank += kr[0] > key;
+    rank += kr[1] > key;
+    rank += kr[2] > key;
+    rank += kr[3] > key;
   }
-  if constexpr (kKeyed) {
-    if (__ballot(live && rank < k && near != rank + 1)) {
+  // The best k + 1 in order: a chosen lane that is not the one at its rank has an
+  // equal beside it; in keyed form the next lower key must be clearly smaller.
+  uint2* const best = cand;  // key and lane
+  wave_lds_sync();
+  if (lane <= k) best[lane] = make_uint2(0, 64);
+  wave_lds_sync();
+  if (mine && rank <= k) best[rank] = make_uint2(key, lane);
+  wave_lds_sync();
+  bool unsure = false;
+  if (mine && rank < k) {
+    unsure = best[rank].y != static_cast<uint32_t>(lane);
+    if (kKeyed) unsure |= live && best[rank + 1].x >= order32(cv - margin(cv));
+  }
+  if (__ballot(unsure)) {
+    // by exact keys, then by the logits, then by the experts' order
+    uint64_t hi = key, lo = static_cast<uint32_t>(E - 1 - e);
+    if constexpr (kKeyed) {
       const double zs = exact_inv_z();
-      uint64_t hi = kKeyTaken, lo = static_cast<uint32_t>(E - 1 - e);
+      hi = kKeyTaken;
       if (mine) hi = live ? order_bits(exact_key(v, bias ? bias[e] : 0.0f, zs)) : kKeyDead;
       if (live) lo |= static_cast<uint64_t>(order32(v)) << 32;
-      const auto of_lane = [](uint64_t x, int at) {
-        return (static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(x >> 32), at)) << 32) |
-               static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(x), at));
-      };
-      rank = 0;
-      for (int r = 0; r < n; ++r) {
-        const uint64_t h = of_lane(hi, r), x = of_lane(lo, r);
-        rank += h > hi || (h == hi && x > lo);
-      }
+    }
+    const auto of_lane = [](uint64_t x, int at) {
+      return (static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(x >> 32), at)) << 32) |
+             static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(x), at));
+    };
+    rank = 0;
+    for (int r = 0; r < n; ++r) {
+      const uint64_t h = of_lane(hi, r), x = of_lane(lo, r);
+      rank += h > hi || (h == hi && x > lo);
     }
   }
   const bool chosen = mine && rank < k;
