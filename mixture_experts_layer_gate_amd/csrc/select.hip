@@ -34,7 +34,9 @@ constexpr uint64_t kKeyDead = 1;   // out of the choice: chosen last, in ascendi
 // (row swaps). After each step the lanes it joined hold the same value.
 template <int kCtrl>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return __builtin_amdgcn_update_dpp(v, v, kCtrl, 0xf, 0xf, false);
+  // every lane has a source, so the old value and bound_ctrl do not matter; this
+  // form folds into the instruction that takes the result
+  return __builtin_amdgcn_update_dpp(0, v, kCtrl, 0xf, 0xf, true);
 }
 template <int kDist>
 __device__ __forceinline__ void partner(uint32_t v, uint32_t& a, uint32_t& b) {
@@ -173,6 +175,13 @@ template <int VPL>
 __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, float (&l)[VPL]) {
   load_raw<VPL>(row, E, -INFINITY, l);
   clean_row<VPL>(l);
+}
+
+template <int VPL>
+__device__ __forceinline__ void load_bias(const float* __restrict__ bias, int E, float (&b)[VPL]) {
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) b[i] = 0.0f;
+  if (bias) load_raw<VPL>(bias, E, 0.0f, b);
 }
 
 // LDS of one wave.
@@ -371,10 +380,14 @@ __device__ __forceinline__ uint64_t keep_groups(const SelectOpts& o, const V (&c
       return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(gk), at),
                               __builtin_amdgcn_readlane(__double2loint(gk), at));
   };
+  // A group's rank: its lanes compare it with lpg groups at a time, and the bits
+  // of the ballot that are theirs count.
   int rank = 0;
-  for (int q = 0; q < o.groups; ++q) {
-    const V v = of_lane(q * lpg);
-    rank += v > gk || (v == gk && q < g);
+  const uint64_t own = (~uint64_t(0) >> (64 - lpg)) << (lane - j);
+  for (int q0 = 0; q0 < o.groups; q0 += lpg) {
+    const int q = q0 + j;
+    const V v = __shfl(gk, (q << o.lpg_log2) & 63);
+    rank += __popcll(__ballot(q < o.groups && (v > gk || (v == gk && q < g))) & own);
   }
   const bool head = j == 0 && g < o.groups;
   if constexpr (sizeof(V) == 4) {
@@ -420,8 +433,8 @@ __device__ __forceinline__ bool nearer_cut(const uint32_t (&q)[VPL], int k, uint
 // are formed again in doubles and ranked by those; likewise the groups' keys
 // where the last kept and the next are that close.
 template <int VPL, bool kKeyed>
-__device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&raw)[VPL], const float* __restrict__ bias,
-                                            int E, int k, int32_t* __restrict__ idx, float* __restrict__ w,
+__device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&raw)[VPL], const float (&bv)[VPL],
+                                            const float* __restrict__ bias, int E, int k, int32_t* __restrict__ idx, float* __restrict__ w,
                                             SelectLds<VPL>& sh) {
   const int lane = threadIdx.x & 63;
   const int e0 = lane * VPL;
@@ -462,16 +475,15 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
   };
   // keys; -inf: out of the choice
   if constexpr (kKeyed) {
-    float bv[VPL];
+    if (o.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) bv[i] = 0.0f;
-    if (bias) load_raw<VPL>(bias, E, 0.0f, bv);
+      for (int i = 0; i < VPL; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
+    } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const float b = bv[i];
-      const float s = o.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-l[i])) : c[i] * inv_z;
-      c[i] = live_value(fminf(l[i], b)) && b == b ? s + b : -INFINITY;
+      for (int i = 0; i < VPL; ++i) c[i] *= inv_z;
     }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c[i] = live_value(l[i]) & live_value(bv[i]) ? c[i] + bv[i] : -INFINITY;
   } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) c[i] = l[i];
@@ -607,16 +619,17 @@ __global__ __launch_bounds__(256) void select_kernel(SelectOpts o, const float* 
                                                      const float* __restrict__ bias, int T, int E, int k,
                                                      int32_t* __restrict__ idx, float* __restrict__ w) {
   __shared__ SelectLds<VPL> lds[4];
-  const int wv = threadIdx.x >> 6;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wv;
   if (t >= T) return;
   const float* row = logits + t * E;
   int32_t* ti = idx + t * k;
   float* tw = w + t * k;
   if constexpr (kFast) {
-    float raw[VPL];
+    float raw[VPL], bv[VPL];
     load_raw<VPL>(row, E, -INFINITY, raw);
-    if (select_fast<VPL, kKeyed>(o, raw, bias, E, k, ti, tw, lds[wv])) return;
+    if (kKeyed) load_bias<VPL>(bias, E, bv);
+    if (select_fast<VPL, kKeyed>(o, raw, bv, bias, E, k, ti, tw, lds[wv])) return;
   }
   select_exact<VPL>(o, row, bias, E, k, ti, tw, lds[wv]);
 }
