@@ -148,23 +148,21 @@ __device__ __forceinline__ Sig sigmoid2(float l) {
 // where all of a row's scores are tiny, since only ratios of them are used.
 __device__ __forceinline__ float sigmoid_scaled(const Sig& g, float u, float m) { return m >= 0.0f ? g.s : u * g.n; }
 
-// lane's experts: lane * VPL + i, i < VPL (so lower lanes hold lower experts)
+// A lane's experts: lane + 64 i, i < VPL, so that a wave's loads and stores are
+// whole lines wherever the row starts. Those of i < VPL / 2 exist (by_width).
+__device__ __forceinline__ int expert_of(int i) { return (threadIdx.x & 63) + 64 * i; }
+template <int VPL>
+__device__ __forceinline__ bool has_expert(int i, int E) {
+  return (VPL > 1 && i < VPL / 2) || expert_of(i) < E;
+}
 template <int VPL>
 __device__ __forceinline__ void load_raw(const float* __restrict__ row, int E, float pad, float (&v)[VPL]) {
-  const int e0 = (threadIdx.x & 63) * VPL;
-  if constexpr (VPL >= 4) {
-    // whole 16-byte loads where every row starts on such a boundary
-    if (E % 4 == 0 && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
 #pragma unroll
-      for (int i = 0; i < VPL; i += 4) {
-        const f32x4_t u = e0 + i < E ? *reinterpret_cast<const f32x4_t*>(row + e0 + i) : f32x4_t{pad, pad, pad, pad};
-        v[i] = u[0]; v[i + 1] = u[1]; v[i + 2] = u[2]; v[i + 3] = u[3];
-      }
-      return;
-    }
+  for (int i = 0; i < VPL; ++i) {
+    const bool has = has_expert<VPL>(i, E);
+    const float u = row[VPL > 1 && i < VPL / 2 ? expert_of(i) : min(expert_of(i), E - 1)];
+    v[i] = has ? u : pad;
   }
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) v[i] = e0 + i < E ? row[e0 + i] : pad;
 }
 template <int VPL>
 __device__ __forceinline__ void clean_row(float (&l)[VPL]) {
@@ -213,7 +211,6 @@ __device__ __forceinline__ void select_exact(const SelectOpts& o, const float* _
                                              const float* __restrict__ bias, int E, int k,
                                              int32_t* __restrict__ idx, float* __restrict__ w, SelectLds<VPL>& sh) {
   const int lane = threadIdx.x & 63;
-  const int e0 = lane * VPL;
   float l[VPL];
   load_row<VPL>(row, E, l);
   uint64_t key[VPL];
@@ -232,17 +229,17 @@ __device__ __forceinline__ void select_exact(const SelectOpts& o, const float* _
   }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const float b = bias && e0 + i < E ? bias[e0 + i] : 0.0f;
+    const float b = bias && has_expert<VPL>(i, E) ? bias[expert_of(i)] : 0.0f;
     const bool live = live_value(l[i]) && live_value(b);
     double s = 0.0;
     if (live) s = o.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l[i]))) : z[i] / zs;
-    key[i] = e0 + i >= E ? kKeyTaken : (live ? order_bits(s + b) : kKeyDead);
+    key[i] = !has_expert<VPL>(i, E) ? kKeyTaken : (live ? order_bits(s + b) : kKeyDead);
   }
 
   if (o.groups > 1) {
     wave_lds_sync();
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) sh.key[e0 + i] = key[i];
+    for (int i = 0; i < VPL; ++i) sh.key[expert_of(i)] = key[i];
     wave_lds_sync();
     const int per = o.per;
     // lane g: group g's key, again as ordered bits (0: no live expert)
@@ -273,7 +270,7 @@ __device__ __forceinline__ void select_exact(const SelectOpts& o, const float* _
     const uint64_t kept = __ballot(lane < o.groups && rank < o.topk_groups);
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (e0 + i < E && !((kept >> ((e0 + i) / per)) & 1)) key[i] = kKeyDead;
+      if (has_expert<VPL>(i, E) && !((kept >> (expert_of(i) / per)) & 1)) key[i] = kKeyDead;
   }
 
   wave_lds_sync();
@@ -283,7 +280,7 @@ __device__ __forceinline__ void select_exact(const SelectOpts& o, const float* _
     int be = E;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (key[i] > bk || (key[i] == bk && key[i] > kKeyDead && l[i] > bl)) { bk = key[i]; bl = l[i]; be = e0 + i; }
+      if (key[i] > bk || (key[i] == bk && key[i] > kKeyDead && l[i] > bl)) { bk = key[i]; bl = l[i]; be = expert_of(i); }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) {
       const uint64_t ok = shfl_xor64(bk, off);
@@ -296,7 +293,7 @@ __device__ __forceinline__ void select_exact(const SelectOpts& o, const float* _
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (e0 + i == be) key[i] = kKeyTaken;
+      if (expert_of(i) == be) key[i] = kKeyTaken;
     if (lane == 0) {
       idx[j] = be;
       sh.val[j] = bk > kKeyDead ? bl : NAN;
@@ -343,7 +340,7 @@ __device__ __forceinline__ uint64_t keep_groups(const SelectOpts& o, const V (&c
   const int lane = threadIdx.x & 63;
   wave_lds_sync();
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) sh[lane * VPL + i] = c[i];
+  for (int i = 0; i < VPL; ++i) sh[expert_of(i)] = c[i];
   wave_lds_sync();
   const auto most = [](V x, V y) { return x > y ? x : y; };
   const auto least = [](V x, V y) { return x > y ? y : x; };
@@ -437,7 +434,6 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
                                             const float* __restrict__ bias, int E, int k, int32_t* __restrict__ idx, float* __restrict__ w,
                                             SelectLds<VPL>& sh) {
   const int lane = threadIdx.x & 63;
-  const int e0 = lane * VPL;
   float l[VPL], c[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) l[i] = raw[i];
@@ -498,12 +494,12 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
       double cd[VPL];
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        cd[i] = c[i] > -INFINITY ? exact_key(l[i], bias ? bias[e0 + i] : 0.0f, zs) : -INFINITY;
+        cd[i] = c[i] > -INFINITY ? exact_key(l[i], bias ? bias[expert_of(i)] : 0.0f, zs) : -INFINITY;
       kept = keep_groups<double, VPL>(o, cd, per, lpg, reinterpret_cast<double*>(sh.key), sure);
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int ge = static_cast<int>((static_cast<float>(e0 + i) + 0.5f) * o.inv_per);  // (e0 + i) / per, below 2^11
+      const int ge = static_cast<int>((static_cast<float>(expert_of(i)) + 0.5f) * o.inv_per);  // expert / per, below 2^11
       if (!((kept >> ((ge << o.lpg_log2) & 63)) & 1)) c[i] = -INFINITY;
     }
   }
@@ -512,7 +508,7 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
   uint32_t q[VPL], top = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    q[i] = e0 + i < E ? order32(c[i]) : 0;
+    q[i] = has_expert<VPL>(i, E) ? order32(c[i]) : 0;
     top = q[i] > top ? q[i] : top;
   }
   top = max_step<8>(top);
@@ -534,11 +530,11 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
     wave_lds_sync();
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const bool in = e0 + i < E && !(c[i] < cut);
+      const bool in = has_expert<VPL>(i, E) && !(c[i] < cut);
       const uint64_t mask = __ballot(in);
       const int at = n + lanes_below(mask);
       if (in && at < 64) {
-        cand[at] = make_uint2(__float_as_uint(l[i]), e0 + i);
+        cand[at] = make_uint2(__float_as_uint(l[i]), expert_of(i));
         cand_key[at] = q[i];
       }
       n += __popcll(mask);
@@ -677,10 +673,10 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
                                                               float* __restrict__ dlogits) {
   __shared__ float slots[4][64 * VPL];  // the chosen experts' part, by expert
   const int lane = threadIdx.x & 63;
-  const int e0 = lane * VPL;
-  float* slot = slots[threadIdx.x >> 6];
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float* slot = slots[wv];
   const bool need_p = dlosses || !(o.sigmoid || o.renorm);  // softmax over the row
-  const int64_t t = t0 + static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t t = t0 + static_cast<int64_t>(blockIdx.x) * 4 + wv;
   if (t >= T) return;
   const int64_t row = t * E, a0 = t * k;
   float l[VPL], dl[VPL], u[VPL];
@@ -719,7 +715,7 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
   // the selection
   if (dw) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) slot[e0 + i] = 0.0f;
+    for (int i = 0; i < VPL; ++i) slot[expert_of(i)] = 0.0f;
     wave_lds_sync();
     const float unit = o.renorm && o.scale != 0.0f ? 1.0f / o.scale : 0.0f;
     float dsum = 0.0f;
@@ -757,7 +753,7 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
     }
     wave_lds_sync();
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) dl[i] = slot[e0 + i];
+    for (int i = 0; i < VPL; ++i) dl[i] = slot[expert_of(i)];
     if (o.sigmoid) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) dl[i] *= g[i].n;
@@ -809,18 +805,9 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
       }
     }
   }
-  if constexpr (VPL >= 4) {
-    if (E % 4 == 0 && (reinterpret_cast<uintptr_t>(dlogits) & 15) == 0) {
-#pragma unroll
-      for (int i = 0; i < VPL; i += 4)
-        if (e0 + i < E)
-          *reinterpret_cast<f32x4_t*>(dlogits + row + e0 + i) = f32x4_t{dl[i], dl[i + 1], dl[i + 2], dl[i + 3]};
-      return;
-    }
-  }
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
-    if (e0 + i < E) dlogits[row + e0 + i] = dl[i];
+    if (has_expert<VPL>(i, E)) dlogits[row + expert_of(i)] = dl[i];
 }
 
 // ---------------------------------------------------------------- losses ----
@@ -837,7 +824,7 @@ __global__ __launch_bounds__(256) void balance_part_kernel(SelectOpts o, const f
   __shared__ int32_t cnt[64 * VPL];
   __shared__ double psum[4][64 * VPL];
   __shared__ double zsum[4];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = blockIdx.x, s = blockIdx.y, parts = gridDim.x;
   if (r == 0 && s == 0 && threadIdx.x == 0) *done = 0;
   const int a = seq_offsets ? clamp_off(seq_offsets[s], T) : 0, b = seq_offsets ? clamp_off(seq_offsets[s + 1], T) : T;
@@ -903,7 +890,7 @@ __global__ __launch_bounds__(256) void balance_part_kernel(SelectOpts o, const f
     }
   }
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) psum[wv][lane * VPL + i] = acc[i];
+  for (int i = 0; i < VPL; ++i) psum[wv][expert_of(i)] = acc[i];
   if (lane == 0) zsum[wv] = zacc;
   __syncthreads();
   const int64_t base = (static_cast<int64_t>(s) * parts + r) * E;
