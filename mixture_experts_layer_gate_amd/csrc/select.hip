@@ -325,18 +325,25 @@ __device__ __forceinline__ float order32_back(uint32_t q) {
 }
 
 constexpr int kFastK = 8;
-// Error of an fp32 key c: less than kErr (1 + |c| / 8). A score is at most 1 and
-// comes out of an exponential, a reciprocal and (softmax) a sum over at most 16 +
-// 6 additions, each within 2^-23 or less of it; adding the bias rounds by 2^-24 |c|.
-constexpr float kErr = 0x1p-19f;
-__device__ __forceinline__ float margin(float c) { return 2.0f * kErr * (1.0f + 0.125f * fabsf(c)); }
+// Error of an fp32 key c = s + bias: at most es + 2^-23 |c|. Sigmoid: s comes out
+// of an exponential whose argument is rounded (|l| 2^-24 of it, times s (1 - s):
+// below 2^-25), of the exponential, an addition and a reciprocal, 2^-23 or less of
+// s or of s (1 - s) each: below 2^-21. Softmax: no score is above inv_z = 1 / sum
+// exp(l - m), and a score's error is below 2^-18 of that: argument, exponential,
+// reciprocal and product together 2^-20, the sum over at most 16 + 6 additions
+// and its terms' own errors 33 2^-24. The sum s + bias rounds by 2^-24 |c|.
+__device__ __forceinline__ float score_error(const SelectOpts& o, float inv_z) {
+  return o.sigmoid ? 0x1p-21f : 0x1p-18f * inv_z;
+}
+// two keys near c this far apart are in their exact order
+__device__ __forceinline__ float margin(float es, float c) { return 2.0f * (es + 0x1p-23f * fabsf(c)); }
 
 // Groups kept, as a mask with bit g * lpg set: 64 / groups lanes (lpg, a power of
 // two) scan a group's keys (c: this lane's, -inf out of the choice) and join.
 // `sure` turns false when fp32 keys cannot tell the last kept from the next.
 template <typename V, int VPL>
-__device__ __forceinline__ uint64_t keep_groups(const SelectOpts& o, const V (&c)[VPL], int per, int lpg, V* sh,
-                                                bool& sure) {
+__device__ __forceinline__ uint64_t keep_groups(const SelectOpts& o, const V (&c)[VPL], int per, int lpg, float es,
+                                                V* sh, bool& sure) {
   const int lane = threadIdx.x & 63;
   wave_lds_sync();
 #pragma unroll
@@ -368,15 +375,8 @@ __device__ __forceinline__ uint64_t keep_groups(const SelectOpts& o, const V (&c
   join(std::integral_constant<int, 8>{});
   join(std::integral_constant<int, 16>{});
   join(std::integral_constant<int, 32>{});
-  V gk = a;
-  if (o.top2 && b > -INFINITY) gk = a + b;
-  const auto of_lane = [&](int at) -> V {
-    if constexpr (sizeof(V) == 4)
-      return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(gk), at));
-    else
-      return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(gk), at),
-                              __builtin_amdgcn_readlane(__double2loint(gk), at));
-  };
+  const bool both = o.top2 && b > -INFINITY;
+  const V gk = both ? a + b : a;
   // A group's rank: its lanes compare it with lpg groups at a time, and the bits
   // of the ballot that are theirs count.
   int rank = 0;
@@ -388,9 +388,13 @@ __device__ __forceinline__ uint64_t keep_groups(const SelectOpts& o, const V (&c
   }
   const bool head = j == 0 && g < o.groups;
   if constexpr (sizeof(V) == 4) {
-    const float gl = of_lane(__ffsll(__ballot(head && rank == o.topk_groups - 1)) - 1);
-    const float gn = of_lane(__ffsll(__ballot(head && rank == o.topk_groups)) - 1);
-    sure = gl - gn > 2.0f * margin(gl);
+    // the lower end of the last kept group's key, the upper end of the next one's
+    const float err = both ? 2.0f * es + 0x1p-22f * (fabsf(a) + fabsf(b)) : es + 0x1p-23f * fabsf(a);
+    const uint64_t kept_last = __ballot(head && rank == o.topk_groups - 1), next = __ballot(head && rank == o.topk_groups);
+    const auto of_lane = [](float x, uint64_t mask) {
+      return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), __ffsll(static_cast<unsigned long long>(mask)) - 1));
+    };
+    sure = of_lane(gk - err, kept_last) > of_lane(a > -INFINITY ? gk + err : -INFINITY, next);
   }
   return __ballot(head && rank < o.topk_groups);
 }
@@ -455,8 +459,9 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
     zs = wave_sum(zs);
     inv_z = zs > 0.0f ? recip(zs) : 0.0f;  // the largest term is 1
   }
-  // 1 / sum exp(l - m) in doubles, and a double key (for a live expert)
-  auto exact_inv_z = [&]() -> double {
+  const float es = score_error(o, inv_z);
+  // sum exp(l - m) in doubles, and a double key (for a live expert)
+  auto exact_sum = [&]() -> double {
     double zs = 0.0;
     if (!o.sigmoid) {
 #pragma unroll
@@ -488,14 +493,14 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
   if (kKeyed && o.groups > 1) {
     const int per = o.per, lpg = 1 << o.lpg_log2;
     bool sure = true;
-    uint64_t kept = keep_groups<float, VPL>(o, c, per, lpg, sh.val, sure);
+    uint64_t kept = keep_groups<float, VPL>(o, c, per, lpg, es, sh.val, sure);
     if (!sure) {
-      const double zs = exact_inv_z();
+      const double zs = exact_sum();
       double cd[VPL];
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
         cd[i] = c[i] > -INFINITY ? exact_key(l[i], bias ? bias[expert_of(i)] : 0.0f, zs) : -INFINITY;
-      kept = keep_groups<double, VPL>(o, cd, per, lpg, reinterpret_cast<double*>(sh.key), sure);
+      kept = keep_groups<double, VPL>(o, cd, per, lpg, es, reinterpret_cast<double*>(sh.key), sure);
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -522,7 +527,7 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
   uint32_t* const cand_key = reinterpret_cast<uint32_t*>(sh.val);
   for (bool again = false;; again = true) {
     float cut = order32_back(top);
-    if (kKeyed) cut -= margin(cut);
+    if (kKeyed) cut -= margin(es, cut);
     // (a cut of -inf stays so; NaN, from a class of no experts or +inf, admits all)
     n = 0;
     wave_lds_sync();
@@ -570,16 +575,20 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
   bool unsure = false;
   if (mine && rank < k) {
     unsure = best[rank].y != static_cast<uint32_t>(lane);
-    if (kKeyed) unsure |= live && best[rank + 1].x >= order32(cv - margin(cv));
+    if (kKeyed) unsure |= live && best[rank + 1].x >= order32(cv - margin(es, cv));
   }
   if (__ballot(unsure)) {
     // by exact keys, then by the logits, then by the experts' order
     uint64_t hi = key, lo = static_cast<uint32_t>(E - 1 - e);
     if constexpr (kKeyed) {
-      const double zs = exact_inv_z();
-      hi = kKeyTaken;
-      if (mine) hi = live ? order_bits(exact_key(v, bias ? bias[e] : 0.0f, zs)) : kKeyDead;
-      if (live) lo |= static_cast<uint64_t>(order32(v)) << 32;
+      hi = mine ? kKeyDead : kKeyTaken;
+      if (bias) {
+        const double zs = exact_sum();
+        if (live) hi = order_bits(exact_key(v, bias[e], zs));
+        if (live) lo |= static_cast<uint64_t>(order32(v)) << 32;
+      } else if (live) {
+        hi = order32(v);  // scores without a bias have the logits' order
+      }
     }
     const auto of_lane = [](uint64_t x, int at) {
       return (static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(x >> 32), at)) << 32) |
