@@ -172,6 +172,36 @@ def test_select_many_near_ties(rng):
         np.testing.assert_array_equal(idx.cpu().numpy(), np.repeat(want, T, axis=0))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 8])
+@pytest.mark.parametrize("E", [64, 120, 256, 1024])
+@pytest.mark.parametrize("kind", ["one small class", "few values", "one value", "opposite biases"])
+def test_select_rows_with_many_candidates(kind, E, groups, score, rng):
+    """Rows whose largest keys do not stand out by residues of the expert, are equal, or come from biases that cancel."""
+    T, k = 24, 8
+    l, b = rng.standard_normal((T, E)).astype(np.float32), None
+    if kind == "one small class":
+        for t in range(T):
+            l[t, t % 8::8] = -30.0 - t
+        l[::3, :] += 25.0 * (np.arange(E) < 3)  # fewer far above than are chosen
+    elif kind == "few values":
+        l = np.round(2.0 * l) / 2.0
+    elif kind == "one value":
+        l[:] = 0.25
+        l[1::2, E // 2] = 0.5
+    else:
+        b = np.where(np.arange(E) % 2 == 0, 300.0, -300.0).astype(np.float32)
+        b += (1e-3 * rng.integers(0, 2, E)).astype(np.float32)
+        l *= 1e-3
+    for bias in (b, np.zeros(E, np.float32) if b is None else -b):
+        spec = ro.RouteSpec(score, groups, max(1, groups // 2), "top2" if groups > 1 else "max", True, 1.0)
+        idx, w = moe.route_select(moe.Dims(T, 64, 64, E, k), _opts(spec), torch.from_numpy(l).cuda(),
+                                  None if bias is None else torch.from_numpy(bias).cuda())
+        want_i, want_w = ro.select(l, bias, k, spec)
+        np.testing.assert_array_equal(idx.cpu().numpy(), want_i)
+        np.testing.assert_allclose(w.cpu().numpy(), want_w, rtol=_rel(l), atol=2.0 ** -126)
+
+
 def test_select_large_batch_against_torch():
     """A batch of many workgroups: the choice and weights of every row against float64 sorts."""
     T, E, k = 20011, 250, 6
