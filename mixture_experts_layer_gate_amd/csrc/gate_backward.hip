@@ -19,7 +19,7 @@
 //
 // Measured at 4096 x 7168 x 256: dWg 46 us (45 GFLOP in bf16, 980 TFLOP/s; its
 // matrix products alone take 20 us of matrix-core time, the loads alone about 26
-// us, and they overlap in part), dx with dWg's parts 39 us (118 MB, 3.0 TB/s; 30
+// us, and they overlap in part), dx with dWg's parts 38 us (118 MB, 3.1 TB/s; 30
 // GFLOP), the split 6 us.
 #include "common.h"
 #include "router.h"
@@ -385,6 +385,26 @@ __device__ __forceinline__ void DxTile<NST>::run(const GateArgs& g, int tile, ch
   const int64_t n0 = static_cast<int64_t>(tile % g.ncols) * kColsX;
   const int64_t t0 = static_cast<int64_t>(tile / g.ncols) * kRowsX;
 
+  // dx_in's rows as the epilogue takes them, those of the first two of its four
+  // blocks read beside the first stage, the others two blocks ahead: read behind
+  // the K loop they kept each tile waiting (the whole call 91.5 against 89.8 us at
+  // 4096 x 7168 x 256, 53.4 against 51.4 at 8192 x 4096 x 64; all four ahead take
+  // the registers of a third wave per SIMD).
+  const int tr = lane / 8;
+  const int64_t n = n0 + wn * 64 + (lane % 8) * 8;
+  const bool col = n < d;
+  u32x4_t in[2][2];
+  auto read_in = [&](int j) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int64_t t = t0 + wm * 64 + j * 16 + p * 8 + tr;
+      in[j % 2][p] = u32x4_t{0, 0, 0, 0};
+      if (dx_in && col && t < T) in[j % 2][p] = *reinterpret_cast<const u32x4_t*>(dx_in + t * d + n);
+    }
+  };
+  read_in(0);
+  read_in(1);
+
   // operand bases of the next step to load, as for dWg
   const bf16_t* wb = g.wg + n0;
   int64_t w_bytes = (E * d - n0) * 2;  // rows past E read as zeros
@@ -432,20 +452,10 @@ __device__ __forceinline__ void DxTile<NST>::run(const GateArgs& g, int tile, ch
   constexpr int kPitch = 64 + 4;
   __syncthreads();  // every wave has read the last stage
   float* ct = reinterpret_cast<float*>(lds) + wv * (16 * kPitch);
-  const int tr = lane / 8;
-  const int64_t n = n0 + wn * 64 + (lane % 8) * 8;
-  const bool col = n < d;
-  u32x4_t in[4][2];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int64_t t = t0 + wm * 64 + j * 16 + p * 8 + tr;
-      in[j][p] = u32x4_t{0, 0, 0, 0};
-      if (dx_in && col && t < T) in[j][p] = *reinterpret_cast<const u32x4_t*>(dx_in + t * d + n);
-    }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
+    const u32x4_t own[2] = {in[j % 2][0], in[j % 2][1]};
+    if (j < 2) read_in(j + 2);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<f32x4_t*>(ct + (lane % 16) * kPitch + i * 16 + 4 * (lane / 16)) = acc[i][j];
@@ -460,8 +470,8 @@ __device__ __forceinline__ void DxTile<NST>::run(const GateArgs& g, int tile, ch
       bf16x8_t r;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        r[2 * q] = static_cast<__bf16>((q < 2 ? lo[2 * q] : hi[2 * q - 4]) + bf16_lo(in[j][p][q]));
-        r[2 * q + 1] = static_cast<__bf16>((q < 2 ? lo[2 * q + 1] : hi[2 * q - 3]) + bf16_hi(in[j][p][q]));
+        r[2 * q] = static_cast<__bf16>((q < 2 ? lo[2 * q] : hi[2 * q - 4]) + bf16_lo(own[p][q]));
+        r[2 * q + 1] = static_cast<__bf16>((q < 2 ? lo[2 * q + 1] : hi[2 * q - 3]) + bf16_hi(own[p][q]));
       }
       // dx is not read again here: stored past the caches' replacement order (45 -> 43 us)
       if (col && t < T)
