@@ -361,6 +361,7 @@ __device__ __forceinline__ void sum_group(const SumArgs& a, int group, int E, ch
   const int64_t stride = static_cast<int64_t>(a.groups - a.bias_groups) * 256;
   for (int64_t i = static_cast<int64_t>(group - a.bias_groups) * 256 + threadIdx.x; i < a.n4; i += stride) {
     f32x4_t v = reinterpret_cast<const f32x4_t*>(a.part)[i];
+#pragma unroll 4  // loads in flight together (2047 x 6144 x 16, ten parts: the call 24.7 -> 23.2 us)
     for (int p = 1; p < a.parts; ++p) v += reinterpret_cast<const f32x4_t*>(a.part)[p * a.n4 + i];
     reinterpret_cast<f32x4_t*>(a.dwg)[i] = v;
   }
