@@ -4,11 +4,12 @@
 //   dWg[e]  = sum_t dl[t][e] x[t],   dbias[e] = sum_t dl[t][e]
 //
 // dl is fp32 and the matrix cores take bf16, so dl is written once as three bf16
-// planes whose sum it is exactly (8 significant bits each: hi, then what hi
-// leaves, then what both leave; the last rounds only denormals). dWg is an fp32
-// result and takes all three planes: its products are then exact and its sums
-// fp32. dx is a bf16 result and takes the first two: what it drops is below
-// 2^-16 of each term, where its final rounding is up to 2^-8 of the sum.
+// planes whose sum it is exactly (8 significant bits each: hi, truncated, then
+// what hi leaves, to nearest, then what both leave; the last rounds only
+// denormals). dWg is an fp32 result and takes all three planes: its products are
+// then exact and its sums fp32. dx is a bf16 result and takes the first two: what
+// it drops is at most 2^-16 of each term (mid's last bit is 2^-15 of dl's first,
+// at most), where its final rounding is up to 2^-8 of the sum.
 //
 // dWg sums over tokens, and both its operands come with the token as the slow
 // index: the planes are written transposed as well, and x's fragments (eight
@@ -192,7 +193,8 @@ __global__ __launch_bounds__(256) void split_kernel(const float* __restrict__ dl
       const uint32_t hb = __float_as_uint(v[r][c]) & 0xffff0000u;
       const bool fin = (hb & 0x7f800000u) != 0x7f800000u;
       const float r1 = fin ? v[r][c] - __uint_as_float(hb) : 0.0f;
-      const uint32_t mb = __float_as_uint(r1) & 0xffff0000u;
+      // mid to nearest: what dx drops is then at most 2^-16 of dl
+      const uint32_t mb = static_cast<uint32_t>(f32_to_bf16_bits(r1)) << 16;
       p[0][r][c] = (hb >> 16) | (v[r][c] != v[r][c] ? 0x40u : 0u);  // a NaN keeps a set mantissa bit
       p[1][r][c] = mb >> 16;
       p[2][r][c] = f32_to_bf16_bits(r1 - __uint_as_float(mb));
