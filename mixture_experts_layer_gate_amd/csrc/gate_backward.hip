@@ -528,6 +528,26 @@ __global__ __launch_bounds__(256) void gate_short_kernel(GateArgs g, SumArgs sum
 // 512 and 30.8 / 28.0 at 1024.
 bool one_launch(int64_t T, int E) { return T <= (E <= 64 ? 256 : 512); }
 
+// Token parts of dWg, at least four steps to each: those of the least estimated
+// time, rounds of 256 workgroups (one to a CU) times a part's steps, plus each
+// part's way through memory (bytes written and read again). A step takes 1.4 us in
+// tiles of 128 experts, 0.8 of 64, a tile's start and end 3. As many parts as one
+// round takes are mostly the best (4 for the 56 tiles of 7168 x 256); 4096 x 8448 x
+// 512 with its 132 tiles took 229 us in one part and takes 198 in three.
+int token_parts(int64_t tiles, int steps, int bm, double bytes) {
+  const int64_t most = steps / 4, round = 256 / tiles;
+  if (round >= 64) return static_cast<int>(most < 1 ? 1 : most < round ? most : round);
+  const double step = bm == 128 ? 1.4 : 0.8, through = bytes / 5.3e6;
+  int best = 1;
+  double least = 0.0;
+  for (int p = 1; p <= 64 && (p == 1 || p <= most); ++p) {
+    const double rounds = static_cast<double>((tiles * p + 255) / 256);
+    const double us = rounds * ((steps + p - 1) / p * step + 3.0) + (p > 1 ? p * through : 0.0);
+    if (p == 1 || us < least) best = p, least = us;
+  }
+  return best;
+}
+
 struct GateWs {
   int64_t blocks;
   int bm;
@@ -547,11 +567,8 @@ size_t layout(int64_t T, int64_t d, int E, void* ws, float* dwg, GateWs* w) {
   w->blocks = g.Tp / kBlk;
   g.steps = static_cast<int>((T + kStep - 1) / kStep);
   g.etiles = g.Ep / w->bm;
-  // token parts: as many as one round of 256 workgroups takes, at least 4 steps to each
   const int64_t tiles = (d + kColsW - 1) / kColsW * g.etiles;
-  int64_t parts = small ? 1 : 256 / tiles;
-  if (parts > g.steps / 4) parts = g.steps / 4;
-  g.parts = parts < 1 ? 1 : static_cast<int>(parts);
+  g.parts = small ? 1 : token_parts(tiles, g.steps, w->bm, 8.0 * E * d);
   g.w_tiles = static_cast<int>(tiles * g.parts);
   g.ncols = static_cast<int>((d + kColsX - 1) / kColsX);
   g.x_tiles = static_cast<int>(g.ncols * (g.Tp / kRowsX));

@@ -415,7 +415,7 @@ def test_many_sequences(rng):
 GATE = [(1, 8, 1), (1, 256, 8), (3, 72, 5), (31, 128, 16), (33, 136, 33), (128, 256, 64), (129, 264, 65), (200, 1000, 96),
         (257, 392, 130), (520, 256, 256), (70, 128, 1024), (2049, 512, 24), (900, 2048, 200),
         (256, 512, 40), (257, 512, 40), (255, 1000, 64), (512, 264, 256), (513, 264, 256), (511, 136, 65),
-        (8300, 136, 3)]
+        (1100, 8448, 520), (8300, 136, 3)]
 
 
 @pytest.mark.parametrize("with_in", [True, False])
