@@ -334,6 +334,31 @@ def test_losses_and_gradient(case, rng):
     assert (err <= (2 * _rel(l) + (k + 16) * U) * mag + 1e-37).all(), float((err / (mag + 1e-37)).max() / U)
 
 
+def test_gradient_of_shares_below_the_normal_range(rng):
+    """Logits some hundreds apart: shares below 2^-126 may be off by up to that, times what multiplies them."""
+    T, E, k = 30, 300, 3
+    spec, offs = ro.RouteSpec("softmax"), [0, 4, 30]
+    l = (50.0 * rng.standard_normal((T, E))).astype(np.float32)
+    idx, w = ro.select(l, None, k, spec)
+    up = np.array([0.8, 0.05], np.float32)
+    dims = moe.Dims(T, 64, 64, E, k)
+    tl, ti, tup = (torch.from_numpy(np.ascontiguousarray(v)).cuda() for v in (l, idx, up))
+    seq = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    _, load = moe.balance_loss(dims, _opts(spec), tl, ti, seq)
+    got = moe.route_select_backward(dims, _opts(spec), tl, None, None, None, tup, load, seq).cpu().numpy()
+    _, f = ro.balance_losses(l, idx, offs, spec)
+    want = ro.select_backward(l, idx, w, None, spec, up, f, offs)
+    for t in range(T):
+        s = 0 if t < offs[1] else 1
+        n = offs[s + 1] - offs[s]
+        p = np.array(ro.scores(ro._clean(l[t]), "softmax"))
+        g = float(up[0]) * E / (k * n * n * 2) * f[s]
+        z = 2 * float(up[1]) * (abs(ro._lse(ro._clean(l[t]))) + float(np.abs(l[t]).max())) / T
+        factor = g + (p * g).sum() + z  # of a share
+        tol = (2 * _rel(l) + (k + 16) * U) * p * factor + 2.0 ** -126 * (factor + 1)
+        assert (np.abs(got[t] - want[t]) <= tol).all()
+
+
 def test_backward_repeated_and_foreign_indices(rng):
     """Repeated entries add up, entries outside [0, E) are skipped; both stay in bounds."""
     T, E, k = 6, 40, 4
