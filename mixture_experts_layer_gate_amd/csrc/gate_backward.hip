@@ -330,8 +330,8 @@ __device__ __forceinline__ void DwgTile<BM, BN, NST>::run(const GateArgs& g, int
   }
 }
 
-// What the dx launch does besides dx: the parts of dWg summed in order, and
-// dbias from the 64-token blocks' sums.
+// What else there is to do: dbias from the 64-token blocks' sums, and, behind dWg,
+// its parts summed in order.
 struct SumArgs {
   const float* part;
   int parts;  // 1: dwg is whole already
@@ -486,13 +486,13 @@ __device__ __forceinline__ void DxTile<NST>::run(const GateArgs& g, int tile, ch
   }
 }
 
-// Tile forms of dWg: up to 64 experts, 64 x 256 with four waves (x streamed
-// once, the padding experts' products are cheap beside it); beyond, 128 x 256
-// with eight.
+// Two forms. Up to 64 experts, and for short batches: dWg in 64 x 256 tiles of four
+// waves (x streamed once up to 64 experts, the padding experts' products are cheap
+// beside it) in one launch with dx and dbias, whose loads and products fill each
+// other's waits. Else dWg in 128 x 256 tiles of eight waves, and dx behind it.
 constexpr int kColsW = 256, kStagesW = 3, kStagesX = 2;
-template <int BM>
-__global__ __launch_bounds__(BM * kColsW / 64, 1) void dwg_kernel(GateArgs g) {
-  typedef DwgTile<BM, kColsW, kStagesW> Tile;
+__global__ __launch_bounds__(512, 1) void dwg_kernel(GateArgs g) {
+  typedef DwgTile<128, kColsW, kStagesW> Tile;
   __shared__ __attribute__((aligned(1024))) char lds[Tile::kLds];
   Tile::run(g, blockIdx.x, lds);
 }
@@ -505,8 +505,8 @@ __global__ __launch_bounds__(256) void gate_dx_kernel(GateArgs g, SumArgs sum) {
   else
     sum_group(sum, id - g.x_tiles, g.E, lds);
 }
-// dWg in one part, dx and dbias in one launch (short batches).
-__global__ __launch_bounds__(256) void gate_short_kernel(GateArgs g, SumArgs sum) {
+// dWg, dx and dbias (two stages of both tiles leave room for two workgroups on a CU).
+__global__ __launch_bounds__(256) void gate_both_kernel(GateArgs g, SumArgs sum) {
   typedef DwgTile<64, kColsW, 2> W;
   typedef DxTile<kStagesX> X;
   __shared__ __attribute__((aligned(1024))) char lds[W::kLds > X::kLds ? W::kLds : X::kLds];
@@ -519,33 +519,37 @@ __global__ __launch_bounds__(256) void gate_short_kernel(GateArgs g, SumArgs sum
     sum_group(sum, id - g.w_tiles - g.x_tiles, g.E, lds);
 }
 
-// One launch for dWg, dx and dbias, each dWg tile over all the tokens: it saves
-// a launch and lets dx run beside dWg, until the tiles' loops over the tokens
-// are longer than split ones and the sum of the parts together. One launch
-// against two, in us, captured, at d = 7168: 16 experts 7.8 / 10.7 at 32 tokens,
-// 12.0 / 14.5 at 256, 17.2 / 15.1 at 512; 256 experts 12.0 / 19.0 at 32, 15.7 /
-// 31.1 at 256, 23.0 / 31.9 at 512. At d = 1024 and 256 experts 19.6 / 24.8 at
-// 512 and 30.8 / 28.0 at 1024.
-bool one_launch(int64_t T, int E) { return T <= (E <= 64 ? 256 : 512); }
+// Batches that take the 64-expert tiles whatever E is: one launch against dWg's
+// and dx's, in us, captured, 256 experts at d = 7168: 12.0 / 19.0 at 32 tokens,
+// 15.7 / 31.1 at 256, 23.0 / 31.9 at 512; at d = 1024 19.6 / 24.8 at 512 and 30.8 /
+// 28.0 at 1024. Up to 64 experts one launch was always the shorter: 2047 x 6144 x
+// 16 21.7 / 23.5, 8192 x 4096 x 64 47.9 / 50.5, 300 x 7168 x 64 14.9 / 18.0.
+bool one_launch(int64_t T, int E) { return E <= 64 || T <= 512; }
 
 // Token parts of dWg, at least four steps to each: those of the least estimated
 // time, rounds of 256 workgroups (one to a CU) times a part's steps, plus each
 // part's way through memory (bytes written and read again). A step takes 1.4 us in
-// tiles of 128 experts, 0.8 of 64, a tile's start and end 3. As many parts as one
-// round takes are mostly the best (4 for the 56 tiles of 7168 x 256); 4096 x 8448 x
-// 512 with its 132 tiles took 229 us in one part and takes 198 in three.
+// tiles of 128 experts, 0.8 of 64, a tile's start and end 3; beside the 64-expert
+// tiles the parts' sum is a launch of its own, 4. As many parts as one round takes
+// are mostly the best (4 for the 56 tiles of 7168 x 256); 4096 x 8448 x 512 with its
+// 132 tiles took 229 us in one part and takes 198 in three.
 int token_parts(int64_t tiles, int steps, int bm, double bytes) {
   const int64_t most = steps / 4, round = 256 / tiles;
   if (round >= 64) return static_cast<int>(most < 1 ? 1 : most < round ? most : round);
-  const double step = bm == 128 ? 1.4 : 0.8, through = bytes / 5.3e6;
+  const double step = bm == 128 ? 1.4 : 0.8, through = bytes / 5.3e6, launch = bm == 128 ? 0.0 : 4.0;
   int best = 1;
   double least = 0.0;
   for (int p = 1; p <= 64 && (p == 1 || p <= most); ++p) {
     const double rounds = static_cast<double>((tiles * p + 255) / 256);
-    const double us = rounds * ((steps + p - 1) / p * step + 3.0) + (p > 1 ? p * through : 0.0);
+    const double us = rounds * ((steps + p - 1) / p * step + 3.0) + (p > 1 ? launch + p * through : 0.0);
     if (p == 1 || us < least) best = p, least = us;
   }
   return best;
+}
+
+__global__ __launch_bounds__(256) void gate_sum_kernel(SumArgs sum, int E) {
+  __shared__ __attribute__((aligned(16))) char lds[256 * 8];
+  sum_group(sum, sum.bias_groups + blockIdx.x, E, lds);
 }
 
 struct GateWs {
@@ -559,8 +563,7 @@ size_t layout(int64_t T, int64_t d, int E, void* ws, float* dwg, GateWs* w) {
   auto at = [&](size_t off) { return ws ? static_cast<char*>(ws) + off : nullptr; };
   auto pad = [](size_t v) { return (v + 255) / 256 * 256; };
   GateArgs& g = w->g;
-  const bool small = one_launch(T, E);
-  w->bm = small || E <= 64 ? 64 : 128;
+  w->bm = one_launch(T, E) ? 64 : 128;
   g.T = T, g.d = d, g.E = E;
   g.Ep = static_cast<int>(up(E, w->bm));
   g.Tp = up(T, kRowsX);
@@ -568,7 +571,7 @@ size_t layout(int64_t T, int64_t d, int E, void* ws, float* dwg, GateWs* w) {
   g.steps = static_cast<int>((T + kStep - 1) / kStep);
   g.etiles = g.Ep / w->bm;
   const int64_t tiles = (d + kColsW - 1) / kColsW * g.etiles;
-  g.parts = small ? 1 : token_parts(tiles, g.steps, w->bm, 8.0 * E * d);
+  g.parts = token_parts(tiles, g.steps, w->bm, 8.0 * E * d);
   g.w_tiles = static_cast<int>(tiles * g.parts);
   g.ncols = static_cast<int>((d + kColsX - 1) / kColsX);
   g.x_tiles = static_cast<int>(g.ncols * (g.Tp / kRowsX));
@@ -617,14 +620,14 @@ hipError_t launch_gate_backward(const void* x, const void* wg, const float* dlog
   sum.bias_groups = (E + 15) / 16;
   const int64_t want = (sum.n4 + 255) / 256;
   sum.groups = sum.bias_groups + (g.parts > 1 ? static_cast<int>(want < 2048 ? want : 2048) : 0);
-  if (one_launch(T, E)) {
-    hipLaunchKernelGGL(gate_short_kernel, dim3(g.w_tiles + g.x_tiles + sum.groups), dim3(256), 0, s, g, sum);
+  if (w.bm == 64) {
+    hipLaunchKernelGGL(gate_both_kernel, dim3(g.w_tiles + g.x_tiles + sum.bias_groups), dim3(256), 0, s, g, sum);
+    if (g.parts == 1) return hipGetLastError();
+    if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
+    hipLaunchKernelGGL(gate_sum_kernel, dim3(sum.groups - sum.bias_groups), dim3(256), 0, s, sum, E);
     return hipGetLastError();
   }
-  if (w.bm == 64)
-    hipLaunchKernelGGL(dwg_kernel<64>, dim3(g.w_tiles), dim3(256), 0, s, g);
-  else
-    hipLaunchKernelGGL(dwg_kernel<128>, dim3(g.w_tiles), dim3(512), 0, s, g);
+  hipLaunchKernelGGL(dwg_kernel, dim3(g.w_tiles), dim3(512), 0, s, g);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   hipLaunchKernelGGL(gate_dx_kernel, dim3(g.x_tiles + sum.groups), dim3(256), 0, s, g, sum);
   return hipGetLastError();
