@@ -388,13 +388,18 @@ __device__ __forceinline__ uint64_t keep_groups(const SelectOpts& o, const V (&c
   }
   const bool head = j == 0 && g < o.groups;
   if constexpr (sizeof(V) == 4) {
-    // the lower end of the last kept group's key, the upper end of the next one's
+    // A key is sure of its side when its error does not reach the middle between the
+    // last kept key and the next. Every group is asked, not those two alone: biases
+    // that cancel give an ordinary key an error of their own size, at any rank. (Groups
+    // with nothing live come last in any case, and among each other by their number.)
     const float err = both ? 2.0f * es + 0x1p-22f * (fabsf(a) + fabsf(b)) : es + 0x1p-23f * fabsf(a);
-    const uint64_t kept_last = __ballot(head && rank == o.topk_groups - 1), next = __ballot(head && rank == o.topk_groups);
-    const auto of_lane = [](float x, uint64_t mask) {
-      return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), __ffsll(static_cast<unsigned long long>(mask)) - 1));
+    const auto of_rank = [&](int r) {
+      const uint64_t mask = __ballot(head && rank == r);
+      return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(gk), __ffsll(static_cast<unsigned long long>(mask)) - 1));
     };
-    sure = of_lane(gk - err, kept_last) > of_lane(a > -INFINITY ? gk + err : -INFINITY, next);
+    const float middle = 0.5f * of_rank(o.topk_groups - 1) + 0.5f * of_rank(o.topk_groups);
+    const bool clear = !(a > -INFINITY) || (rank < o.topk_groups ? gk - err > middle : gk + err < middle);
+    sure = !__ballot(head && !clear);
   }
   return __ballot(head && rank < o.topk_groups);
 }

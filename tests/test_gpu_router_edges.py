@@ -1,0 +1,56 @@
+"""Inputs at the edge of what the scored router's calls accept: keys made of biases
+that cancel, against the float64 oracle (oracle/router_oracle.py). Index arrays
+must be equal.
+"""
+import math
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_gate_amd as moe
+from oracle import router_oracle as ro
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+INF, NAN = math.inf, math.nan
+
+
+def _say(msg):
+    print(msg, flush=True)
+    sys.stdout.flush()
+
+
+def _opts(spec):
+    return moe.RouteOptions(spec.score, spec.groups, spec.topk_groups, spec.group_rule, spec.renormalise, spec.scale)
+
+
+def _gpu(*arrays):
+    return [None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in arrays]
+
+
+# ---------------------------------------------------------------- selection ----
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("groups,per,kept", [(4, 2, 2), (4, 2, 1), (4, 2, 3), (8, 4, 4), (16, 2, 6), (64, 2, 20), (8, 32, 4)])
+def test_group_keys_of_biases_that_cancel(groups, per, kept, score, rng):
+    """Top-2 group keys 1e-5 to 1e-3 apart, those of one group in four made of biases of +-1000 (or +-2^20) that
+    cancel: such a key is inexact in fp32 by far more than its neighbours', wherever it ranks."""
+    T, E, k = 512, groups * per, min(4, kept * per)
+    _say(f"cancelling biases: {groups} groups of {per}, {kept} kept, {score}")
+    for rep in range(6):
+        l = (10.0 ** (-5 + rep // 2) * rng.standard_normal((T, E))).astype(np.float32)
+        b = np.zeros(E, np.float32)
+        for g in rng.permutation(groups)[:max(1, groups // 4)]:
+            at = g * per + rng.permutation(per)[:2]
+            big = 1000.0 if rep % 2 == 0 else 2.0 ** 20
+            b[g * per:(g + 1) * per] = -2.0 * big
+            b[at] = big, -big
+        spec = ro.RouteSpec(score, groups, kept, "top2", True, 1.0)
+        tl, tb = _gpu(l, b)
+        idx, w = moe.route_select(moe.Dims(T, 64, 64, E, k), _opts(spec), tl, tb)
+        want_i, want_w = ro.select(l, b, k, spec)
+        np.testing.assert_array_equal(idx.cpu().numpy(), want_i)
+        # each weight a ratio of exponentials of differences below 1: (1 + 32) u
+        np.testing.assert_allclose(w.cpu().numpy(), want_w, rtol=33 * U)
