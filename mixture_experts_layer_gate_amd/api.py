@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 from typing import Optional
 
 import torch
@@ -51,8 +51,24 @@ class _Dims(ctypes.Structure):
                 ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+class _Frozen:
+    """Base of the frozen dataclasses that the calls take."""
+
+    def ref(self):
+        """A reference to the C struct, made once (the fields are frozen and the library only reads it)."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = ctypes.byref(self.c())
+            object.__setattr__(self, "_ref", r)
+        return r
+
+    def __getstate__(self):
+        """Copies and pickles take the fields: a ctypes reference can be neither copied nor pickled."""
+        return {f.name: getattr(self, f.name) for f in fields(self)}
+
+
 @dataclass(frozen=True)
-class Dims:
+class Dims(_Frozen):
     T: int
     d: int
     f: int
@@ -63,14 +79,6 @@ class Dims:
     def c(self) -> _Dims:
         return _Dims(self.T, self.d, self.f, self.E, self.k, MOE_DTYPE.get(self.dtype, -1))
 
-    def ref(self):
-        """A reference to the C struct, made once (the fields are frozen and the library only reads it)."""
-        r = self.__dict__.get("_ref")
-        if r is None:
-            r = ctypes.byref(self.c())
-            object.__setattr__(self, "_ref", r)
-        return r
-
 
 class _RouteOpts(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
@@ -78,7 +86,7 @@ class _RouteOpts(ctypes.Structure):
 
 
 @dataclass(frozen=True)
-class RouteOptions:
+class RouteOptions(_Frozen):
     """How route_select chooses experts from gate logits: scores by "softmax" (over
     all experts) or "sigmoid"; with groups > 1, only the topk_groups groups of
     consecutive experts with the largest group key are chosen from, the key being
@@ -100,14 +108,6 @@ class RouteOptions:
     def c(self) -> _RouteOpts:
         return _RouteOpts(int(self.score == "sigmoid"), self.groups, self.topk_groups, int(self.group_rule == "top2"),
                           int(bool(self.renormalise)), self.scale)
-
-    def ref(self):
-        """A reference to the C struct, made once (the fields are frozen and the library only reads it)."""
-        r = self.__dict__.get("_ref")
-        if r is None:
-            r = ctypes.byref(self.c())
-            object.__setattr__(self, "_ref", r)
-        return r
 
 
 def library_path() -> str:

@@ -1,10 +1,12 @@
 """The scored router's oracle against independent statements of it (brute force,
 closed forms, automatic and finite differences, published generator outputs),
 and the refusals of the new entry points. Host-only: no call reaches a launch."""
+import copy
 import ctypes
 import itertools
 import math
 import os
+import pickle
 
 import numpy as np
 import pytest
@@ -227,3 +229,16 @@ def test_binding_refusals():
         moe.balance_loss(dims, moe.RouteOptions(), cpu, cpu)
     with pytest.raises(ValueError, match="GPU tensor"):
         moe.dropout_backward(dims, 0.1, cpu, cpu)
+
+
+@pytest.mark.parametrize("value", [moe.Dims(4, 64, 64, 8, 2), moe.RouteOptions("sigmoid", 4, 2, "top2", True, 2.5)])
+def test_dims_and_options_are_copied_and_pickled_after_use(value):
+    """Whatever a call keeps beside the fields stays behind, and the copy serves calls of its own."""
+    fresh = pickle.dumps(value)
+    value.ref()
+    if isinstance(value, moe.Dims) and os.path.exists(moe.library_path()):
+        assert moe.balance_workspace_bytes(value) > 0 and moe.gate_backward_workspace_bytes(value) > 0
+    assert pickle.dumps(value) == fresh
+    for other in (copy.copy(value), copy.deepcopy(value), pickle.loads(pickle.dumps(value))):
+        assert other == value and hash(other) == hash(value)
+        assert bytes(other.ref()._obj) == bytes(value.ref()._obj) and other.ref()._obj is not value.ref()._obj
