@@ -485,7 +485,10 @@ int moe_balance_loss(const moe_dims_t* dims, const moe_route_opts_t* opts, const
  * [n_seq][E] as moe_balance_loss returned it for the same seq_offsets.
  * topk_idx and topk_w as moe_route_select returned them for these logits and
  * options: a slot of weight 0 passes no gradient, an entry outside [0, E) is
- * skipped, repeated entries add up. Experts whose logit is -inf or NaN get 0;
+ * skipped, repeated entries add up. Values of dtopk_w and dlosses that are not
+ * finite go where the formula sends them; a finite dlosses[1] whose product with
+ * a row's log-sum-exp passes fp32's range counts as the largest value there is.
+ * Experts whose logit is -inf or NaN get 0;
  * shares below 2^-126 have that absolute precision. */
 int moe_route_select_backward(const moe_dims_t* dims, const moe_route_opts_t* opts, const float* logits,
                               const int32_t* topk_idx, const float* topk_w, const float* dtopk_w,

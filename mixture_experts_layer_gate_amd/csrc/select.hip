@@ -813,9 +813,11 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
         dot += sh[i] * gl[i];
       }
       dot = wave_sum(dot);
-      // (kept finite, so that an expert of share 0 gets 0 where lse is the largest logit there is)
-      const float cz = fminf(fmaxf(dlosses[1] * 2.0f / static_cast<float>(q.covered) * (m + logf(zs)) * inv_z, -kF32Max),
-                             kF32Max);
+      // kept finite, so that an expert of share 0 gets 0 where lse is the largest logit
+      // there is; but not where the gradient that comes in is no finite number itself
+      const float dz = dlosses[1];
+      float cz = dz * 2.0f / static_cast<float>(q.covered) * (m + logf(zs)) * inv_z;
+      if (fabsf(dz) <= kF32Max) cz = fminf(fmaxf(cz, -kF32Max), kF32Max);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         float v = sh[i] * (gl[i] - dot);

@@ -54,3 +54,29 @@ def test_group_keys_of_biases_that_cancel(groups, per, kept, score, rng):
         np.testing.assert_array_equal(idx.cpu().numpy(), want_i)
         # each weight a ratio of exponentials of differences below 1: (1 + 32) u
         np.testing.assert_allclose(w.cpu().numpy(), want_w, rtol=33 * U)
+
+
+# ---------------------------------------------------------------- gradients ----
+@pytest.mark.parametrize("E", [6, 70, 300])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+def test_non_finite_gradients_of_the_losses_show(value, score, renorm, E, rng):
+    """A z loss whose gradient is NaN or infinite gives that to every expert of the rows it covers, so that an
+    overflow is seen; the rows outside every sequence keep the selection's gradient alone."""
+    T, k = 9, 2
+    l = (1.0 + 0.1 * rng.standard_normal((T, E))).astype(np.float32)  # log-sum-exp above 0, no share below 1e-3
+    spec = ro.RouteSpec(score, renormalise=renorm)
+    tl, tseq = _gpu(l, np.array([0, 4, 7], np.int32))
+    dims, opts = moe.Dims(T, 64, 64, E, k), _opts(spec)
+    idx, w = moe.route_select(dims, opts, tl)
+    _, load = moe.balance_loss(dims, opts, tl, idx, tseq)
+    dw = torch.ones((T, k), device="cuda").cumsum(1)
+    up = torch.tensor([0.5, value], device="cuda")
+    got = moe.route_select_backward(dims, opts, tl, idx, w, dw, up, load, tseq).cpu()
+    alone = moe.route_select_backward(dims, opts, tl, idx, w, dw).cpu()
+    assert torch.equal(got[7:], alone[7:])
+    assert bool(torch.isnan(got[:7]).all() if value != value else (got[:7] == value).all())
+    # the balance loss's: NaN, by the formula (inf - inf)
+    up = torch.tensor([value, 0.5], device="cuda")
+    got = moe.route_select_backward(dims, opts, tl, idx, w, dw, up, load, tseq).cpu()
+    assert bool(torch.isnan(got[:7]).all()) and torch.equal(got[7:], alone[7:])
