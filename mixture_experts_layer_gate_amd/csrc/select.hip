@@ -826,9 +826,10 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
       }
     }
   }
+  // (out of the choice: 0 times a gradient that is no finite number would be NaN)
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
-    if (has_expert<VPL>(i, E)) dlogits[row + expert_of(i)] = dl[i];
+    if (has_expert<VPL>(i, E)) dlogits[row + expert_of(i)] = live_value(l[i]) ? dl[i] : 0.0f;
 }
 
 // ---------------------------------------------------------------- losses ----

@@ -80,3 +80,28 @@ def test_non_finite_gradients_of_the_losses_show(value, score, renorm, E, rng):
     up = torch.tensor([value, 0.5], device="cuda")
     got = moe.route_select_backward(dims, opts, tl, idx, w, dw, up, load, tseq).cpu()
     assert bool(torch.isnan(got[:7]).all()) and torch.equal(got[7:], alone[7:])
+
+
+@pytest.mark.parametrize("E", [8, 90, 600])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_masked_experts_get_no_gradient_whatever_comes_in(value, score, renorm, E, rng):
+    """Logits of -inf or NaN: gradient 0 there, also where dtopk_w or dlosses are not finite."""
+    T, k = 6, 3
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    dead = rng.random((T, E)) < 0.4
+    dead[:, :k] = False  # three experts of every row are in the choice
+    l[dead] = np.where(rng.random((T, E)) < 0.5, -INF, NAN)[dead]
+    tl, = _gpu(l)
+    dims, opts = moe.Dims(T, 64, 64, E, k), moe.RouteOptions(score, renormalise=renorm)
+    idx, w = moe.route_select(dims, opts, tl)
+    _, load = moe.balance_loss(dims, opts, tl, idx)
+    dw = torch.ones((T, k), device="cuda")
+    for up in ([value, 0.0], [0.0, value], [value, value]):
+        up = torch.tensor(up, device="cuda")
+        got = moe.route_select_backward(dims, opts, tl, idx, w, dw, up, load).cpu().numpy()
+        assert not got[dead].any()
+        got = moe.route_select_backward(dims, opts, tl, None, None, None, up, load).cpu().numpy()
+        assert not got[dead].any()
+    got = moe.route_select_backward(dims, opts, tl, idx, w, value * dw).cpu().numpy()
+    assert not got[dead].any() and not np.isfinite(got).all()
