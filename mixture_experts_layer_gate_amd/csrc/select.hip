@@ -736,7 +736,6 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
 #pragma unroll
     for (int i = 0; i < VPL; ++i) slot[expert_of(i)] = 0.0f;
     wave_lds_sync();
-    const float unit = o.renorm && o.scale != 0.0f ? 1.0f / o.scale : 0.0f;
     float dsum = 0.0f;
     for (int j0 = 0; j0 < k; j0 += 64) {
       if (j0 > 0) {
@@ -749,7 +748,8 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
       float v = sw != 0.0f ? sw * sd : 0.0f;
       dsum += v;
       if (o.renorm) {
-        // dw_j - sum_i v_i dw_i as sum_i v_i (dw_j - dw_i), v = w / scale summing to 1: nothing cancels
+        // dw_j - sum_i v_i dw_i as sum_i v_i (dw_j - dw_i), v = w / scale summing to 1: nothing
+        // cancels (divided one by one: 1 / scale is past fp32's range for scales below 2^-128)
         float acc = 0.0f;
         for (int i0 = 0; i0 < k; i0 += 64) {
           const bool in = i0 + lane < k;
@@ -759,6 +759,7 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
             di = in ? dw[a0 + i0 + lane] : 0.0f;
           }
           if (wi == 0.0f) di = 0.0f;
+          else wi /= o.scale;
           const int n = min(64, k - i0);
           for (int q = 0; q < n; ++q) {
             const float wq = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wi), q));
@@ -766,7 +767,7 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
             acc += wq * (sd - dq);
           }
         }
-        v = sw != 0.0f ? sw * (acc * unit) : 0.0f;
+        v = sw != 0.0f ? sw * acc : 0.0f;
       }
       if (se >= 0 && se < E) atomicAdd(&slot[se], v);
     }

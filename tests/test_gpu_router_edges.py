@@ -105,3 +105,35 @@ def test_masked_experts_get_no_gradient_whatever_comes_in(value, score, renorm, 
         assert not got[dead].any()
     got = moe.route_select_backward(dims, opts, tl, idx, w, value * dw).cpu().numpy()
     assert not got[dead].any() and not np.isfinite(got).all()
+
+
+@pytest.mark.parametrize("k", [4, 128])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("scale", [2.0 ** -140, 2.0 ** -147, -(2.0 ** -130), 2.0 ** 100, 2.0 ** 127])
+def test_gradient_of_weights_of_any_scale(scale, score, k):
+    """k equal experts share the scale exactly; dw is scaled so that the gradients w_j (dw_j - mean dw) are
+    ordinary numbers, while 1 / scale is not one where the scale is below 2^-128."""
+    T, E = 5, 300
+    w_one, unit = scale / k, 2.0 ** -math.frexp(scale / k)[1]
+    if k == 128 and abs(scale) < 2.0 ** -142:
+        pytest.skip("the weights would be below fp32's smallest number")
+    unit = min(max(unit, 2.0 ** -100), 2.0 ** 100)
+    l = np.full((T, E), -3.0, np.float32)
+    l[:, :k] = 0.5
+    tl, = _gpu(l)
+    dims, opts = moe.Dims(T, 64, 64, E, k), moe.RouteOptions(score, renormalise=True, scale=scale)
+    idx, w = moe.route_select(dims, opts, tl)
+    # softmax: the scale over k, exactly. Sigmoid: s (scale / (k s)), where k s is exact and the quotient and the
+    # product round once each: 2 u of the weight, or half a step of 2^-149 each below the normal range
+    off = 0.0 if score == "softmax" else 2 * U * (1 + U) * abs(w_one) + 2.0 ** -149
+    w64 = w.cpu().double().numpy()
+    assert idx.tolist() == [list(range(k))] * T and (np.abs(w64 - w_one) <= off).all()
+    dw = unit * (np.arange(T)[:, None] + np.arange(k)[None, :] % 5).astype(np.float32)
+    got = moe.route_select_backward(dims, opts, tl, idx, w, _gpu(dw)[0]).cpu().double().numpy()
+    d64 = dw.astype(np.float64)
+    want = w64 * ((w64 / scale)[:, None, :] * (d64[:, :, None] - d64[:, None, :])).sum(axis=2)
+    if score == "sigmoid":
+        want = want / (1.0 + math.exp(0.5))
+    # k terms, each a difference below 5 unit, times the weight and 1 - s: (k + 16) u of the largest
+    assert (np.abs(got[:, :k] - want) <= (k + 16) * U * 5 * unit * abs(w_one) + 2.0 ** -149).all()
+    assert not got[:, k:].any()
