@@ -789,7 +789,9 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
     const Seq q = find_seq(seq_offsets, n_seq, static_cast<int>(t), T);
     if (q.id >= 0 && m > -INFINITY) {
       const float n = static_cast<float>(q.len);
-      const float cb = dlosses[0] * static_cast<float>(E) / (static_cast<float>(k) * static_cast<float>(q.filled)) / n / n;
+      // (dlosses[0] comes in last: its product with E alone could leave fp32's range)
+      const float db = dlosses[0];
+      const float cb = static_cast<float>(E) / (static_cast<float>(k) * static_cast<float>(q.filled)) / n / n;
       float f[VPL];  // the loads' bits
       load_raw<VPL>(reinterpret_cast<const float*>(load + static_cast<int64_t>(q.id) * E), E, 0.0f, f);
       // shares p~, up to the factor r
@@ -810,7 +812,7 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         sh[i] *= r;
-        gl[i] = cb * static_cast<float>(__float_as_int(f[i]));
+        gl[i] = db * (cb * static_cast<float>(__float_as_int(f[i])));
         dot += sh[i] * gl[i];
       }
       dot = wave_sum(dot);

@@ -137,3 +137,24 @@ def test_gradient_of_weights_of_any_scale(scale, score, k):
     # k terms, each a difference below 5 unit, times the weight and 1 - s: (k + 16) u of the largest
     assert (np.abs(got[:, :k] - want) <= (k + 16) * U * 5 * unit * abs(w_one) + 2.0 ** -149).all()
     assert not got[:, k:].any()
+
+
+@pytest.mark.parametrize("E", [60, 600])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("power", [120, -110])
+def test_gradient_of_the_balance_loss_is_linear_in_its_own(power, score, E, rng):
+    """A dlosses[0] of 2^120 or 2^-110, whose product with E leaves fp32's range or whose quotient by the rows'
+    square loses bits below 2^-126: the gradient of dlosses[0] = 1 times that, bit for bit but for denormals."""
+    T, k = 5000, 1
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    tl, = _gpu(l)
+    dims, opts = moe.Dims(T, 64, 64, E, k), moe.RouteOptions(score)
+    idx, w = moe.route_select(dims, opts, tl)
+    _, load = moe.balance_loss(dims, opts, tl, idx)
+
+    def grad(up):
+        up = torch.tensor([up, 0.0], device="cuda")
+        return moe.route_select_backward(dims, opts, tl, None, None, None, up, load).double()
+    one, far = grad(1.0), grad(2.0 ** power) * 2.0 ** -power
+    # powers of two commute with rounding; a sum of E terms and two products below 2^-126 are off by 2^-149 each
+    assert bool(((far - one).abs() <= (E + 8) * 2.0 ** (-149 - power)).all() if power < 0 else torch.equal(far, one))
