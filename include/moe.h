@@ -502,6 +502,7 @@ int moe_route_select_backward(const moe_dims_t* dims, const moe_route_opts_t* op
  * dlogits [T][E], dwg [E][d], dbias [E] fp32. bf16 only, d % 8 == 0, T <=
  * 4194176, d <= 2^24 and (T/128 + 1)(d/128 + 1) < 2^23 (MOE_ERR_UNSUPPORTED otherwise). T = 0 writes zero dwg and
  * dbias. dwg's products are exact and its sums fp32; fixed summation order.
+ * Infinities and NaN, of x and wg as of dlogits, go where the formula sends them.
  * ws: at least moe_gate_backward_workspace_bytes(dims), 256-byte aligned. */
 size_t moe_gate_backward_workspace_bytes(const moe_dims_t* dims);
 int moe_gate_backward(const moe_dims_t* dims, const void* x, const void* wg, const float* dlogits, const void* dx_in,

@@ -11,6 +11,13 @@
 // it drops is at most 2^-16 of each term (mid's last bit is 2^-15 of dl's first,
 // at most), where its final rounding is up to 2^-8 of the sum.
 //
+// An infinity in x or Wg meets planes that are zero or of the other sign, which
+// would make a NaN of the formula's infinity (and so may products past fp32's
+// range). Each non-finite result is therefore formed again from dl itself, term by
+// term: no finite result can come of such products, so nothing else is looked at.
+// (Asking every accumulator costs 0.2 to 0.9 us a call: 2047 x 6144 x 16 21.6 -> 21.8,
+// 8192 x 4096 x 64 47.0 -> 47.9, 32 x 7168 x 256 11.2 -> 11.7, 4096 x 7168 x 256 the same.)
+//
 // dWg sums over tokens, and both its operands come with the token as the slow
 // index: the planes are written transposed as well, and x's fragments (eight
 // consecutive tokens per lane) come from transposing LDS reads
@@ -235,6 +242,7 @@ struct GateArgs {
   const bf16_t* wg;
   const bf16_t* dx_in;
   bf16_t* dx;
+  const float* dl;
   const bf16_t* rows;  // split_kernel's outputs
   const bf16_t* cols;
   float* out;  // dwg, or its parts [parts][E][d]
@@ -243,6 +251,8 @@ struct GateArgs {
   int steps, etiles, parts, w_tiles;  // dWg: 32-token steps, expert tiles, token parts, tiles in all
   int ncols, x_tiles;                 // dx: column tiles, tiles in all
 };
+
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.402823466e38f; }
 
 // A BM-expert x BN-column tile of one part of the tokens: out[part][e][n].
 // BM / 64 x BN / 64 waves, each 64 experts x 64 columns.
@@ -318,6 +328,7 @@ __device__ __forceinline__ void DwgTile<BM, BN, NST>::run(const GateArgs& g, int
   });
   // accumulator of lane l: columns 4 (l / 16) .. + 3 of expert l % 16
   float* o = g.out + static_cast<int64_t>(part) * E * d;
+  f32x4_t odd = {0.0f, 0.0f, 0.0f, 0.0f};  // NaN once an accumulator is not finite (four chains)
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int e = e0 + wm * 64 + j * 16 + lane % 16;
@@ -325,8 +336,33 @@ __device__ __forceinline__ void DwgTile<BM, BN, NST>::run(const GateArgs& g, int
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t n = n0 + wn * 64 + i * 16 + 4 * (lane / 16);
-      if (n < d) *reinterpret_cast<f32x4_t*>(o + e * d + n) = acc[i][j];
+      if (n >= d) continue;
+      *reinterpret_cast<f32x4_t*>(o + e * d + n) = acc[i][j];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) odd[q] = __builtin_fmaf(acc[i][j][q], 0.0f, odd[q]);
     }
+  }
+  if (!__ballot((odd[0] + odd[1]) + (odd[2] + odd[3]) != 0.0f)) return;
+  // each of them again, in token order (a lane reads what it has just written)
+  const int64_t t1 = min(T, t0 + static_cast<int64_t>(n_steps) * kStep);
+  for (int b = 0; b < 16; ++b) {
+    const int e = e0 + wm * 64 + b / 4 * 16 + lane % 16;
+    const int64_t n = n0 + wn * 64 + b % 4 * 16 + 4 * (lane / 16);
+    if (e >= E || n >= d) continue;
+    f32x4_t v = *reinterpret_cast<const f32x4_t*>(o + e * d + n);
+    if (finite(v[0]) && finite(v[1]) && finite(v[2]) && finite(v[3])) continue;
+    f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t t = t0; t < t1; ++t) {
+      const float a = g.dl[t * E + e];
+      const uint2 u = *reinterpret_cast<const uint2*>(g.x + t * d + n);
+      sum[0] = __builtin_fmaf(a, bf16_lo(u.x), sum[0]);
+      sum[1] = __builtin_fmaf(a, bf16_hi(u.x), sum[1]);
+      sum[2] = __builtin_fmaf(a, bf16_lo(u.y), sum[2]);
+      sum[3] = __builtin_fmaf(a, bf16_hi(u.y), sum[3]);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = finite(v[q]) ? v[q] : sum[q];
+    *reinterpret_cast<f32x4_t*>(o + e * d + n) = v;
   }
 }
 
@@ -455,6 +491,7 @@ __device__ __forceinline__ void DxTile<NST>::run(const GateArgs& g, int tile, ch
   constexpr int kPitch = 64 + 4;
   __syncthreads();  // every wave has read the last stage
   float* ct = reinterpret_cast<float*>(lds) + wv * (16 * kPitch);
+  uint32_t again = 0;  // rows of this lane left out, one bit to each
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const u32x4_t own[2] = {in[j % 2][0], in[j % 2][1]};
@@ -470,19 +507,51 @@ __device__ __forceinline__ void DxTile<NST>::run(const GateArgs& g, int tile, ch
       const int64_t t = t0 + wm * 64 + j * 16 + p * 8 + tr;
       const float* src = ct + (p * 8 + tr) * kPitch + (lane % 8) * 8;
       const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(src), hi = *reinterpret_cast<const f32x4_t*>(src + 4);
+      float odd[2] = {0.0f, 0.0f};  // NaN where a sum is not finite
       bf16x8_t r;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        r[2 * q] = static_cast<__bf16>((q < 2 ? lo[2 * q] : hi[2 * q - 4]) + bf16_lo(own[p][q]));
-        r[2 * q + 1] = static_cast<__bf16>((q < 2 ? lo[2 * q + 1] : hi[2 * q - 3]) + bf16_hi(own[p][q]));
+        const float v0 = q < 2 ? lo[2 * q] : hi[2 * q - 4], v1 = q < 2 ? lo[2 * q + 1] : hi[2 * q - 3];
+        odd[0] = __builtin_fmaf(v0, 0.0f, odd[0]);
+        odd[1] = __builtin_fmaf(v1, 0.0f, odd[1]);
+        r[2 * q] = static_cast<__bf16>(v0 + bf16_lo(own[p][q]));
+        r[2 * q + 1] = static_cast<__bf16>(v1 + bf16_hi(own[p][q]));
       }
+      const bool on = col && t < T, whole = odd[0] + odd[1] == 0.0f;
+      if (on && !whole) again |= 1u << (2 * j + p);
       // dx is not read again here: stored past the caches' replacement order (45 -> 43 us)
-      if (col && t < T)
+      if (on && whole)
         __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, r), reinterpret_cast<u32x4_t*>(dx + t * d + n));
     }
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+  // those, in the experts' order (dx_in, which dx may be, still holds what it held)
+  for (; again; again &= again - 1) {
+    const int b = __builtin_ctz(again);
+    const int64_t t = t0 + wm * 64 + b / 2 * 16 + b % 2 * 8 + tr;
+    float sum[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum[q] = 0.0f;
+    for (int e = 0; e < E; ++e) {
+      const float a = g.dl[t * E + e];
+      const u32x4_t u = *reinterpret_cast<const u32x4_t*>(g.wg + e * d + n);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        sum[2 * q] = __builtin_fmaf(a, bf16_lo(u[q]), sum[2 * q]);
+        sum[2 * q + 1] = __builtin_fmaf(a, bf16_hi(u[q]), sum[2 * q + 1]);
+      }
+    }
+    u32x4_t old = {0, 0, 0, 0};
+    if (dx_in) old = *reinterpret_cast<const u32x4_t*>(dx_in + t * d + n);
+    bf16x8_t r;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      r[2 * q] = static_cast<__bf16>(sum[2 * q] + bf16_lo(old[q]));
+      r[2 * q + 1] = static_cast<__bf16>(sum[2 * q + 1] + bf16_hi(old[q]));
+    }
+    *reinterpret_cast<u32x4_t*>(dx + t * d + n) = __builtin_bit_cast(u32x4_t, r);
   }
 }
 
@@ -605,6 +674,7 @@ hipError_t launch_gate_backward(const void* x, const void* wg, const float* dlog
   g.x = static_cast<const bf16_t*>(x);
   g.wg = static_cast<const bf16_t*>(wg);
   g.dx_in = static_cast<const bf16_t*>(dx_in);
+  g.dl = dlogits;
   g.dx = static_cast<bf16_t*>(dx);
   hipLaunchKernelGGL(split_kernel, dim3(g.Ep / kBlk, static_cast<unsigned>(w.blocks)), dim3(256), 0, s, dlogits, T, E,
                      g.Tp, g.Ep, const_cast<bf16_t*>(g.rows), const_cast<bf16_t*>(g.cols), w.bpart);

@@ -158,3 +158,59 @@ def test_gradient_of_the_balance_loss_is_linear_in_its_own(power, score, E, rng)
     one, far = grad(1.0), grad(2.0 ** power) * 2.0 ** -power
     # powers of two commute with rounding; a sum of E terms and two products below 2^-126 are off by 2^-149 each
     assert bool(((far - one).abs() <= (E + 8) * 2.0 ** (-149 - power)).all() if power < 0 else torch.equal(far, one))
+
+
+BF = 2.0 ** -8
+
+
+def _agree(got, want, tol):
+    """NaN and infinities (of the same sign) in the same places, the finite rest within tol. A value past the
+    output type's range is an infinity of it: bf16's ends at 3.396e38, where its largest number 3.3895e38 (255 steps
+    of 2^120) and half a step more round up, fp32's at 3.403e38."""
+    got, near = got.double().cpu(), want.to(got.dtype).double()
+    assert torch.equal(torch.isnan(got), torch.isnan(near))
+    inf = torch.isinf(near)
+    assert torch.equal(got[inf], near[inf])
+    fin = torch.isfinite(near)
+    assert bool(((got - want).abs()[fin] <= tol[fin]).all())
+
+
+@pytest.mark.parametrize("with_in", [True, False])
+@pytest.mark.parametrize("shape", [(40, 64, 6), (700, 264, 20), (33, 136, 65), (900, 520, 130), (1300, 2056, 70)],
+                         ids=lambda s: "T{}_d{}_E{}".format(*s))
+def test_gate_backward_of_infinities_in_x_and_wg(shape, with_in, rng):
+    """x and Wg holding infinities, NaN and values whose products overflow go where the formula sends them,
+    whatever bits of dlogits meet them (1, -1, 0, all 24 bits, denormals); everything else keeps its bounds."""
+    T, d, E = shape
+    _say(f"gate_backward, infinities in x and wg: {shape} dx_in={with_in}")
+    bf = torch.bfloat16
+    x = rng.standard_normal((T, d)).astype(np.float32)
+    wg = rng.standard_normal((E, d)).astype(np.float32)
+    dl = (rng.standard_normal((T, E)) * 10.0 ** rng.uniform(-6, 2, (T, E))).astype(np.float32)
+    values = [INF, -INF, NAN, 3.0e38, -3.0e38]
+    # one special value to a column, so that no two of them cancel
+    for c, v in zip(rng.permutation(d)[:20], values * 4):
+        t = int(rng.integers(T))
+        x[t, c] = v
+        dl[t, :4] = 1.0, -1.0, 0.0, 2.0 ** -140
+        dl[t, 4:6] = 16777215.0, -16777215.0 * 2.0 ** -40
+    for c, v in zip(rng.permutation(d)[:20], values * 4):
+        e = int(rng.integers(E))
+        wg[e, c] = v
+        dl[rng.permutation(T)[:4], e] = 1.0, -1.0, 0.0, 2.0 ** -140
+    x, wg, dl = (torch.from_numpy(v).cuda() for v in (x, wg, dl))
+    x, wg = x.to(bf), wg.to(bf)
+    dx_in = torch.from_numpy(rng.standard_normal((T, d)).astype(np.float32)).cuda().to(bf) if with_in else None
+    if with_in:
+        dx_in[T // 2, 3] = INF
+    X, W, D = (v.double().cpu() for v in (x, wg, dl))
+    I = torch.zeros((T, d), dtype=torch.float64) if dx_in is None else dx_in.double().cpu()
+    dx, dwg, _ = moe.gate_backward(moe.Dims(T, d, 64, E, 1), x, wg, dl, dx_in, dx=dx_in)
+    # fp32 sums of exact products; dx from dlogits within 2^-16 of each term (test_gate_backward's bounds). The
+    # planes of dlogits are bf16, whose smallest step is 2^-133: a dlogits of fewer bits than that (2^-140, a
+    # denormal) is off by half of it at most, 2^-134 times the x or Wg beside it
+    step = 2.0 ** -134
+    _agree(dwg, D.t() @ X, (T + 8) * U * (D.abs().t() @ X.abs()) + step * X.abs().sum(0))
+    want = I + D @ W
+    _agree(dx, want, BF * want.abs() + (2.0 ** -16 * (1 + BF) + (E + 8) * U) * (D.abs() @ W.abs()) + 4 * U * I.abs()
+           + (1 + BF) * step * W.abs().sum(0))
