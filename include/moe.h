@@ -501,7 +501,10 @@ int moe_route_select_backward(const moe_dims_t* dims, const moe_route_opts_t* op
  * overlaps nothing else);
  * dlogits [T][E], dwg [E][d], dbias [E] fp32. bf16 only, d % 8 == 0, T <=
  * 4194176, d <= 2^24 and (T/128 + 1)(d/128 + 1) < 2^23 (MOE_ERR_UNSUPPORTED otherwise). T = 0 writes zero dwg and
- * dbias. dwg's products are exact and its sums fp32; fixed summation order.
+ * dbias. dwg's sums are fp32, of exact products; fixed summation order. dx's sum
+ * is fp32 too, but takes dlogits to 16 bits: up to 2^-16 of each term is lost
+ * before it, which shows behind the bf16 rounding where terms cancel by more than
+ * some 2^8. In both, bits of dlogits below 2^-133 are rounded to that.
  * Infinities and NaN, of x and wg as of dlogits, go where the formula sends them.
  * ws: at least moe_gate_backward_workspace_bytes(dims), 256-byte aligned. */
 size_t moe_gate_backward_workspace_bytes(const moe_dims_t* dims);

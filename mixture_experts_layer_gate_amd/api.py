@@ -792,7 +792,8 @@ def gate_backward_workspace_bytes(dims: Dims) -> int:
 
 def gate_backward(dims: Dims, x, wg, dlogits, dx_in=None, dx=None, dwg=None, dbias=None, ws=None, stream=None):
     """Gradients of the gate GEMM for a dense dlogits [T][E] (fp32): dx [T][d] = dx_in +
-    dlogits wg (bf16; dx may be dx_in), dwg [E][d] and dbias [E] (fp32). bf16 layers.
+    dlogits wg (bf16, dlogits taken to 16 bits; dx may be dx_in), dwg [E][d] and dbias [E]
+    (fp32, from all of dlogits). bf16 layers.
     Returns (dx, dwg, dbias)."""
     lib = _lib or load_library()
     dev = x.device

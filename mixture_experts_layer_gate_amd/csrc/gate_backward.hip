@@ -9,7 +9,9 @@
 // denormals). dWg is an fp32 result and takes all three planes: its products are
 // then exact and its sums fp32. dx is a bf16 result and takes the first two: what
 // it drops is at most 2^-16 of each term (mid's last bit is 2^-15 of dl's first,
-// at most), where its final rounding is up to 2^-8 of the sum.
+// at most), where its final rounding is up to 2^-8 of the sum: it shows where the
+// terms cancel by more than some 2^8. The third plane was measured: 4096 x 7168 x 256
+// 84 -> 96 us, 32 x 7168 x 256 11.7 -> 13.1, 2047 x 6144 x 16 21.7 -> 22.1.
 //
 // An infinity in x or Wg meets planes that are zero or of the other sign, which
 // would make a NaN of the formula's infinity (and so may products past fp32's

@@ -214,3 +214,31 @@ def test_gate_backward_of_infinities_in_x_and_wg(shape, with_in, rng):
     want = I + D @ W
     _agree(dx, want, BF * want.abs() + (2.0 ** -16 * (1 + BF) + (E + 8) * U) * (D.abs() @ W.abs()) + 4 * U * I.abs()
            + (1 + BF) * step * W.abs().sum(0))
+
+
+@pytest.mark.parametrize("shape", [(40, 64, 8), (200, 264, 70), (700, 520, 130)], ids=lambda s: "T{}_d{}_E{}".format(*s))
+def test_gate_backward_of_terms_that_cancel(shape, rng):
+    """Experts in pairs of the same Wg whose logit gradients nearly cancel: dx within 2^-16 of each term, as the
+    header has it (in the mean far less), and exact where dlogits has 16 bits; dWg's sums from all 24 bits."""
+    T, d, E = shape
+    _say(f"gate_backward, cancelling terms: {shape}")
+    bf = torch.bfloat16
+    x = torch.from_numpy(rng.standard_normal((T, d)).astype(np.float32)).cuda().to(bf)
+    wg = rng.standard_normal((E // 2, d)).astype(np.float32).repeat(2, axis=0)
+    wg = torch.from_numpy(wg).cuda().to(bf)
+    a = rng.standard_normal((T, E // 2)).astype(np.float32)
+    for part in (2.0 ** -12, 2.0 ** -20):
+        b = (-a * (1.0 + part * rng.standard_normal(a.shape))).astype(np.float32)
+        dl = torch.from_numpy(np.stack([a, b], axis=2).reshape(T, E)).cuda()
+        dx, dwg, _ = moe.gate_backward(moe.Dims(T, d, 64, E, 1), x, wg, dl)
+        X, W, D = (v.double().cpu() for v in (x, wg, dl))
+        want, mag = D @ W, D.abs() @ W.abs()
+        _agree(dx, want, BF * want.abs() + (2.0 ** -16 * (1 + BF) + (E + 8) * U) * mag)
+        _agree(dwg, D.t() @ X, (T + 8) * U * (D.abs().t() @ X.abs()))
+    # dlogits of 16 bits, and every pair equal and opposite: nothing is left
+    b = torch.from_numpy(a).cuda()
+    b = (b.view(torch.int32) & ~0xFF).view(torch.float32)
+    dl = torch.stack([b, -b], dim=2).reshape(T, E).contiguous()
+    dx, _, _ = moe.gate_backward(moe.Dims(T, d, 64, E, 1), x, wg, dl)
+    want, mag = torch.zeros((T, d), dtype=torch.float64), dl.double().cpu().abs() @ W.abs()
+    _agree(dx, want, (E + 8) * U * mag)
