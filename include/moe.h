@@ -424,6 +424,9 @@ int moe_layer_backward_ex(const moe_dims_t* dims, const void* x, const void* wg,
  *   the k experts with the largest c are chosen, slot by slot (ties: larger
  *   logit, then lower expert). Keys are compared as doubles;
  *   topk_w[j] = scale * s_j, with renormalise divided by the sum of the chosen s.
+ *   Scores (with renormalise, their quotients by the largest chosen one) below
+ *   2^-126 have that absolute precision and may come as 0; a weight of 0 passes
+ *   no gradient.
  * Where fewer than k experts are in the choice, the slots left take the
  * experts out of it in ascending order with weight 0 (so every index is valid
  * for moe_permute); a row with none gets experts 0 .. k-1 and weights 0.

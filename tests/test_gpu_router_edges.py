@@ -56,6 +56,31 @@ def test_group_keys_of_biases_that_cancel(groups, per, kept, score, rng):
         np.testing.assert_allclose(w.cpu().numpy(), want_w, rtol=33 * U)
 
 
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 20])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_weights_below_the_normal_range(score, renorm, scale, rng):
+    """Scores from 2^-110 down to nothing: within 2^-126 of a score (its weight within that times the scale), and
+    where such a weight has become 0 its gradient is 0 too."""
+    T, E, k = 40, 16, 4
+    l = -(76.0 + rng.random((T, E)) * 40.0).astype(np.float32)
+    if score == "softmax" or renorm:
+        l[:, 0] = 0.0  # the scores, or their quotients by the largest, are as small as before
+    spec = ro.RouteSpec(score, renormalise=renorm, scale=scale)
+    tl, = _gpu(l)
+    dims = moe.Dims(T, 64, 64, E, k)
+    idx, w = moe.route_select(dims, _opts(spec), tl)
+    want_i, want_w = ro.select(l, None, k, spec)
+    np.testing.assert_array_equal(idx.cpu().numpy(), want_i)
+    w32 = w.cpu().numpy()
+    # (spread + 32) u, the spread of the logits up to 116; a quotient is by a sum of at least 0.5
+    np.testing.assert_allclose(w32, want_w, rtol=148 * U, atol=2.0 * scale * 2.0 ** -126)
+    dl = moe.route_select_backward(dims, _opts(spec), tl, idx, w, torch.ones_like(w).cumsum(1)).cpu().numpy()
+    assert np.isfinite(dl).all()
+    if not (score == "softmax" and not renorm):  # (whose every logit takes part in the sum)
+        assert not np.take_along_axis(dl, want_i, axis=1)[w32 == 0].any()
+
+
 # ---------------------------------------------------------------- gradients ----
 @pytest.mark.parametrize("E", [6, 70, 300])
 @pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
