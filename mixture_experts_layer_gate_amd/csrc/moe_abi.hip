@@ -734,7 +734,8 @@ static int run_backward(const moe_dims_t* dm, const void* x, const void* wg, con
                         void* stream, bool gate = true) {
   if (int st = check_dims(dm)) return st;
   if (gate && (!ok16(wg) || !ok16(dwg) || !ok4(dbias))) return MOE_ERR_INVALID;
-  if (!ok16(w1) || !ok16(w3) || !ok16(w2) || !ok16(dw1) || !ok16(dw3) || !ok16(dw2) || !ok4(counts) || !ok4(offsets) || !ok4_or_null(dlogits) || !ok4_or_null(dtopk_w))
+  if (!ok16(w1) || !ok16(w3) || !ok16(w2) || !ok16(dw1) || !ok16(dw3) || !ok16(dw2) || !ok4(counts) ||
+      !ok4(offsets) || !ok4_or_null(dlogits) || !ok4_or_null(dtopk_w))
     return MOE_ERR_INVALID;
   if (dm->T > 0 && (!ok16(x) || !ok4(topk_idx) || !ok4(topk_w) || !ok4(perm) || !ok4(inv_perm) || !ok16(dout) ||
                     !ok16(dx)))

@@ -489,7 +489,10 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
       for (int i = 0; i < VPL; ++i) c[i] *= inv_z;
     }
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) c[i] = live_value(l[i]) & live_value(bv[i]) ? c[i] + bv[i] : -INFINITY;
+    for (int i = 0; i < VPL; ++i) {
+      const int live = static_cast<int>(live_value(l[i])) & static_cast<int>(live_value(bv[i]));
+      c[i] = live ? c[i] + bv[i] : -INFINITY;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) c[i] = l[i];
@@ -1023,7 +1026,6 @@ __global__ __launch_bounds__(256) void balance_reduce_kernel(const float* __rest
   }
 }
 
-// VPL: experts per lane, the least power of two that covers E with 64 lanes.
 // Tokens of one launch (it holds fewer than 2^32 threads, 64 to a token); a
 // larger batch takes several.
 constexpr int64_t kLaunchTokens = int64_t(1) << 25;

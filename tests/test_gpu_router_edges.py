@@ -1,6 +1,9 @@
-"""Inputs at the edge of what the scored router's calls accept: keys made of biases
-that cancel, against the float64 oracle (oracle/router_oracle.py). Index arrays
-must be equal.
+"""Inputs at the edge of what the scored router's calls accept, against the float64
+oracle (oracle/router_oracle.py) and the formulas: keys made of biases that cancel,
+weights below fp32's normal range, gradients that are not finite or of extreme
+size, infinities in the gate's operands, terms that cancel. Index arrays must be
+equal; u = 2^-24 is fp32's half step, 2^-8 bf16's, and each test derives its bound
+from them.
 """
 import math
 import sys
@@ -132,16 +135,14 @@ def test_masked_experts_get_no_gradient_whatever_comes_in(value, score, renorm, 
     assert not got[dead].any() and not np.isfinite(got).all()
 
 
-@pytest.mark.parametrize("k", [4, 128])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("scale", [2.0 ** -140, 2.0 ** -147, -(2.0 ** -130), 2.0 ** 100, 2.0 ** 127])
+@pytest.mark.parametrize("scale,k", [(2.0 ** -147, 4)] + [
+    (scale, k) for scale in (2.0 ** -140, -(2.0 ** -130), 2.0 ** 100, 2.0 ** 127) for k in (4, 128)])
 def test_gradient_of_weights_of_any_scale(scale, score, k):
     """k equal experts share the scale exactly; dw is scaled so that the gradients w_j (dw_j - mean dw) are
     ordinary numbers, while 1 / scale is not one where the scale is below 2^-128."""
     T, E = 5, 300
     w_one, unit = scale / k, 2.0 ** -math.frexp(scale / k)[1]
-    if k == 128 and abs(scale) < 2.0 ** -142:
-        pytest.skip("the weights would be below fp32's smallest number")
     unit = min(max(unit, 2.0 ** -100), 2.0 ** 100)
     l = np.full((T, E), -3.0, np.float32)
     l[:, :k] = 0.5
