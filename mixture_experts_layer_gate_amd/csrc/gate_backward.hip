@@ -595,6 +595,9 @@ __global__ __launch_bounds__(256) void gate_both_kernel(GateArgs g, SumArgs sum)
 // 15.7 / 31.1 at 256, 23.0 / 31.9 at 512; at d = 1024 19.6 / 24.8 at 512 and 30.8 /
 // 28.0 at 1024. Up to 64 experts one launch was always the shorter: 2047 x 6144 x
 // 16 21.7 / 23.5, 8192 x 4096 x 64 47.9 / 50.5, 300 x 7168 x 64 14.9 / 18.0.
+// 65 to 128 experts at more than 512 tokens take the two, and would be shorter in one
+// as well: 513 x 7168 x 96 20.2 / 25.6, 1024 x 2048 x 128 18.7 / 25.4, 8192 x 2048 x 65
+// 36.5 / 40.1, 4096 x 7168 x 128 54.2 / 62.7.
 bool one_launch(int64_t T, int E) { return E <= 64 || T <= 512; }
 
 // Token parts of dWg, at least four steps to each: those of the least estimated

@@ -324,6 +324,9 @@ __device__ __forceinline__ float order32_back(uint32_t q) {
   return __uint_as_float(q ^ ((q >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
+// The eight lane classes of select_fast bound eight keys. Larger k take select_exact,
+// k rounds over the whole row: 4096 x 512 5.8 us with k = 8, 24.3 with 9, 26.1 with 10;
+// 4096 x 256 29.3 with k = 16, 4096 x 1024 128 with k = 32.
 constexpr int kFastK = 8;
 // Error of an fp32 key c = s + bias: at most es + 2^-23 |c|. Sigmoid: s comes out
 // of an exponential whose argument is rounded (|l| 2^-24 of it, times s (1 - s):
@@ -627,9 +630,11 @@ __device__ __forceinline__ bool select_fast(const SelectOpts& o, const float (&r
 
 // One wave per token (a loop over tokens would put the rare paths' constants and
 // divisions in front of every wave: 400 instructions, as many as a row takes).
-// Measured: 1 x 256 with groups and bias 3.4 us, 4096 x 256 the same 6.3, 16383 x
+// Measured: 1 x 256 with groups and bias 3.3 us, 4096 x 256 the same 6.5, 16383 x
 // 250 with bias 11.7 (1.4 TB/s of logits). Bound by vector instructions: 475 a row
 // with groups, 311 without (11.7 us are 1.4 times their issue at four cycles each).
+// A wave takes one row whatever E is: 16384 x 8 5.3 us, 65536 x 8 15.6. Where a bias
+// masks whole groups: 4096 x 256 with 5 of 8 groups masked and 4 kept 6.9, 3 kept 5.5.
 template <int VPL, bool kKeyed, bool kFast>
 __global__ __launch_bounds__(256) void select_kernel(SelectOpts o, const float* __restrict__ logits,
                                                      const float* __restrict__ bias, int T, int E, int k,
@@ -681,8 +686,9 @@ __device__ __forceinline__ Seq find_seq(const int32_t* __restrict__ off, int n_s
 // and, with shares p~ (softmax: p; sigmoid: s over its row sum) and the balance
 // loss's g_e = dB E f_e / (k n^2 filled), the z loss's lse = log sum exp l:
 //   dl[e] += p~_e (g_e - sum p~ g) (1 - s_e if sigmoid) + dZ 2 lse p_e / covered.
-// Measured: 4096 x 256 7.0 us, 8192 x 16 5.9, 333 x 60 4.2 (a launch by itself takes
+// Measured: 4096 x 256 7.2 us, 8192 x 16 6.0, 333 x 60 4.2 (a launch by itself takes
 // about 2): bound by the latency of loads, reductions and stores behind each other.
+// Each row looks its sequence up among all: 65536 x 256 46 us in one sequence, 84 in 1024.
 template <int VPL>
 __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, const float* __restrict__ logits,
                                                               const int32_t* __restrict__ idx,
@@ -842,8 +848,12 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectOpts o, cons
 // Part r of sequence s: its rows' shares p~ summed per expert in double (a part
 // of a batch of millions of rows has thousands to a wave) and rounded once to
 // fp32, the loads counted (integers, any order gives the same), and sum lse^2 in
-// double. The parts are then summed in double. Measured: 4096 x 256 8.2 us and 6.0
-// for the reduction, 8192 x 16 4.8 and 7.0: latency, as above.
+// double. The parts are then summed in double. Measured: 4096 x 256 8.2 us and 6 to 7
+// for the reduction, 8192 x 16 4.8 and 6.5: latency, as above. Every sequence has the
+// same number of parts, so the longest of many takes the time: 8126 x 256 in 64 even
+// sequences 35 us (both kernels), with one of 8000 rows 129; 65536 x 256 as one
+// sequence 39, in 1024 of 64 rows 388, with one of 60000 rows among 1024 short ones
+// 13200.
 template <int VPL>
 __global__ __launch_bounds__(256) void balance_part_kernel(SelectOpts o, const float* __restrict__ logits,
                                                            const int32_t* __restrict__ idx,
