@@ -18,7 +18,8 @@
 // range). Each non-finite result is therefore formed again from dl itself, term by
 // term: no finite result can come of such products, so nothing else is looked at.
 // (Asking every accumulator costs 0.2 to 0.9 us a call: 2047 x 6144 x 16 21.6 -> 21.8,
-// 8192 x 4096 x 64 47.0 -> 47.9, 32 x 7168 x 256 11.2 -> 11.7, 4096 x 7168 x 256 the same.)
+// 8192 x 4096 x 64 47.0 -> 47.9, 32 x 7168 x 256 11.2 -> 11.7, 4096 x 7168 x 256 the
+// same. With one infinite row of x the last takes 1.4 ms, with nothing else in x and Wg 1.9.)
 //
 // dWg sums over tokens, and both its operands come with the token as the slow
 // index: the planes are written transposed as well, and x's fragments (eight
@@ -354,6 +355,7 @@ __device__ __forceinline__ void DwgTile<BM, BN, NST>::run(const GateArgs& g, int
     f32x4_t v = *reinterpret_cast<const f32x4_t*>(o + e * d + n);
     if (finite(v[0]) && finite(v[1]) && finite(v[2]) && finite(v[3])) continue;
     f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8  // loads in flight together
     for (int64_t t = t0; t < t1; ++t) {
       const float a = g.dl[t * E + e];
       const uint2 u = *reinterpret_cast<const uint2*>(g.x + t * d + n);
@@ -536,6 +538,7 @@ __device__ __forceinline__ void DxTile<NST>::run(const GateArgs& g, int tile, ch
     float sum[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) sum[q] = 0.0f;
+#pragma unroll 8
     for (int e = 0; e < E; ++e) {
       const float a = g.dl[t * E + e];
       const u32x4_t u = *reinterpret_cast<const u32x4_t*>(g.wg + e * d + n);
