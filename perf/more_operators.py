@@ -1,0 +1,470 @@
+"""The measured cases of what a training step needs around the layer: the norm in
+front of it (with the residual added), its gradients, the 2-norm of all
+gradients with the clipping factor, and the AdamW update of many tensors with
+states in 32 or in 8 bits. ``run`` computes them in their plain form, or through
+the library where ``own`` is true.
+
+Shapes follow the workloads this repository is benchmarked on (widths 6144 and
+7168, experts of 6144 x 16384 and 7168 x 2048, 8 to 256 experts), from one token
+to prefill batches and from single tensors to whole lists of them.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+BLOCK = 128  # elements that share a scale of the 8-bit states; every tensor of a list begins at a multiple of it
+
+
+# ------------------------------------------------------------------ cases ----
+def _norm(name, op, T, d, kind, dtype, wdtype, bias, residual):
+    return {"name": name, "op": op, "T": T, "d": d, "kind": kind, "dtype": dtype, "wdtype": wdtype, "bias": bias,
+            "residual": residual, "eps": 1e-6 if kind == "rms" else 1e-5}
+
+
+def _gnorm(name, sizes, repeat, dtype, scale, max_norm):
+    return {"name": name, "op": "grad_norm", "sizes": sizes, "repeat": repeat, "dtype": dtype, "scale": scale,
+            "max_norm": max_norm}
+
+
+def _adam(name, bits, sizes, repeat, param, grad, master, stochastic, step, lr, wd, beta2):
+    return {"name": name, "op": "adam", "bits": bits, "sizes": sizes, "repeat": repeat, "param": param, "grad": grad,
+            "master": master, "stochastic": stochastic, "step": step, "lr": lr, "wd": wd, "beta1": 0.9,
+            "beta2": beta2, "eps": 1e-8}
+
+
+def listed():
+    return [
+        # one decode step's norm in front of the 256-expert layer, the residual added
+        _norm("norm_t1_d7168", "norm", 1, 7168, "rms", "bf16", "bf16", False, True),
+        # a prefill batch in front of the 8-expert layer, the residual added
+        _norm("norm_t16384_d6144", "norm", 16384, 6144, "rms", "bf16", "f32", False, True),
+        # a narrow fp32 model's layer norm with weight and bias, an odd number of tokens
+        _norm("norm_t1500_d1048_f32", "norm", 1500, 1048, "layer", "f32", "f32", True, False),
+        # gradients of the norm in front of the 256-expert layer's training batch, the residual's gradient added
+        _norm("norm_grad_t4096_d7168", "norm_grad", 4096, 7168, "rms", "bf16", "f32", False, True),
+        # a layer norm with bias in front of the 16-expert layer, one token short of even
+        _norm("norm_grad_t2047_d6144", "norm_grad", 2047, 6144, "layer", "bf16", "bf16", True, False),
+        # a short fp32 microbatch of an odd length
+        _norm("norm_grad_t333_d1048_f32", "norm_grad", 333, 1048, "layer", "f32", "f32", True, True),
+        # the fp32 weight gradients of one 6144 x 16384 expert
+        _gnorm("grad_norm_expert", "100663296,100663296,100663296", 1, "f32", 1.0, 1.0),
+        # the small tensors of a stack of layers: gate weights and biases, norm weights, in bf16 under a loss scale
+        _gnorm("grad_norm_small", "98304,16,6144,6144", 40, "bf16", 2.0 ** -10, 1.0),
+        # the fp32 gates, biases and norms of a stack of 16-expert layers
+        _adam("adam_small", 32, "98304,16,6144,6144", 10, "f32", "f32", False, False, 1, 3e-4, 0.0, 0.999),
+        # one 6144 x 16384 expert in bf16 with fp32 master weights and fp32 states
+        _adam("adam_expert", 32, "100663296,100663296,100663296", 1, "bf16", "f32", True, False, 1000, 3e-4, 0.1, 0.95),
+        # two 7168 x 2048 experts in bf16 without master weights, 8-bit states, bf16 weight gradients
+        _adam("adam8_experts", 8, "14680064,14680064,14680064", 2, "bf16", "bf16", False, True, 1000, 3e-4, 0.1, 0.95),
+        # the gate, its bias and two norms of a 256-expert layer, tensors of odd lengths among them
+        _adam("adam8_small", 8, "1835008,256,7168,7165", 2, "f32", "f32", False, False, 7, 1e-3, 0.01, 0.999),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["norm", "norm_grad", "grad_norm", "adam", "adam"])
+    if op in ("norm", "norm_grad"):
+        kind, dtype = rng.choice(["rms", "layer"]), rng.choice(["bf16", "bf16", "f32"])
+        return _norm("", op, _log_int(rng, 1, 4096 if dtype == "bf16" else 2048), 8 * _log_int(rng, 8, 1024), kind, dtype,
+                     rng.choice(["bf16", "f32"]), kind == "layer" and rng.random() < 0.7, rng.random() < 0.6)
+    sizes = [_log_int(rng, 1, 4 << 20) for _ in range(rng.randint(1, 6))]
+    repeat = min(_log_int(rng, 1, 16), max(1, (48 << 20) // sum(sizes)))
+    sizes = ",".join(map(str, sizes))
+    dtype = rng.choice(["bf16", "f32"])
+    if op == "grad_norm":
+        return _gnorm("", sizes, repeat, dtype, rng.choice([1.0, 2.0 ** -12, 0.25]), rng.choice([0.5, 1.0, 1e9]))
+    bits, param = rng.choice([8, 32]), rng.choice(["bf16", "f32"])
+    master = param == "bf16" and rng.random() < 0.5
+    return _adam("", bits, sizes, repeat, param, dtype, master, param == "bf16" and not master and rng.random() < 0.7,
+                 _log_int(rng, 1, 100000), rng.choice([1e-4, 3e-4, 1e-3]), rng.choice([0.0, 0.01, 0.1]),
+                 rng.choice([0.95, 0.99, 0.999]))
+
+
+# ----------------------------------------------------------------- inputs ----
+def _type(text):
+    return torch.float32 if text == "f32" else torch.bfloat16
+
+
+def _sizes(case):
+    return [int(v) for v in case["sizes"].split(",")] * case["repeat"]
+
+
+def _starts(sizes):
+    """First element of each tensor of a list in its flat buffer, and the buffer's length."""
+    at, starts = 0, []
+    for n in sizes:
+        starts.append(at)
+        at += -(-n // BLOCK) * BLOCK
+    return starts, at
+
+
+def _views(flat, sizes, starts):
+    return [flat[a:a + n] for a, n in zip(starts, sizes)]
+
+
+def _gaps(flat, sizes, starts):
+    """The elements between the tensors of a flat buffer set to 0."""
+    ends = starts[1:] + [flat.numel()]
+    for a, n, e in zip(starts, sizes, ends):
+        if e > a + n:
+            flat[a + n:e] = 0
+    return flat
+
+
+def _gradients(gen, sizes, starts, total, dtype, spread):
+    """Weight gradients as a backward gives them: one size per tensor, rows of 64 of their own size, some of them
+    zero (experts that received no tokens)."""
+    g = torch.randn(total, generator=gen, device="cuda")
+    rows = total // 64
+    size = torch.exp(torch.randn(rows, generator=gen, device="cuda") * spread) * 1e-3
+    size = torch.where(torch.rand(rows, generator=gen, device="cuda") < 0.05, torch.zeros_like(size), size)
+    g.view(rows, 64).mul_(size[:, None])
+    return _gaps(g.to(dtype), sizes, starts)
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    op = case["op"]
+    st = {"case": case}
+    if own:
+        import mixture_experts_layer_gate_amd as moe
+        st["moe"] = moe
+    if op in ("norm", "norm_grad"):
+        T, d, dt, wt = case["T"], case["d"], _type(case["dtype"]), _type(case["wdtype"])
+
+        def rows(scale):
+            return (torch.randn((T, d), generator=gen, device="cuda") * scale).to(dt)
+        # a residual stream: a mean of its own per row, a few columns far larger than the others
+        x = torch.randn((T, d), generator=gen, device="cuda") + 0.5 * torch.randn((T, 1), generator=gen, device="cuda")
+        x[:, :: max(1, d // 7)] *= 20.0
+        st["x"] = x.to(dt)
+        st["w"] = (1.0 + 0.2 * torch.randn(d, generator=gen, device="cuda")).to(wt)
+        st["b"] = (0.2 * torch.randn(d, generator=gen, device="cuda")).to(wt) if case["bias"] else None
+        if op == "norm":
+            st["res"] = rows(1.0) if case["residual"] else None
+        else:
+            st["dy"] = rows(0.01)
+            st["dx_in"] = rows(0.01) if case["residual"] else None
+            # the statistics that the forward handed on
+            s = st["x"].double()
+            mu = s.mean(dim=1) if case["kind"] == "layer" else torch.zeros(T, dtype=torch.float64, device="cuda")
+            var = ((s - mu[:, None]) ** 2).mean(dim=1)
+            st["mean"] = mu.float() if case["kind"] == "layer" else None
+            st["rstd"] = (1.0 / torch.sqrt(var + case["eps"])).float()
+        if own:
+            st["dims"] = moe.Dims(T, d, 64, 8, 2, dt)
+            st["opts"] = moe.NormOptions(kind=case["kind"], eps=case["eps"], param_dtype=wt)
+        return st
+    sizes = _sizes(case)
+    starts, total = _starts(sizes)
+    if op == "grad_norm":
+        st["g"] = _gradients(gen, sizes, starts, total, _type(case["dtype"]), 1.0)
+        st["g"] = st["g"] / case["scale"] if case["scale"] < 1 else st["g"]  # gradients of a scaled loss
+        st["grads"] = _views(st["g"], sizes, starts)
+        return st
+    st["p"] = _gaps((torch.randn(total, generator=gen, device="cuda") * 0.0125).to(_type(case["param"])), sizes, starts)
+    st["master"] = None
+    if case["master"]:  # the weights before their rounding to bf16
+        st["master"] = st["p"].float() * (1.0 + (torch.rand(total, generator=gen, device="cuda") - 0.5) * 2.0 ** -9)
+    st["g"] = _gradients(gen, sizes, starts, total, _type(case["grad"]), 1.0)
+    st["gscale"] = 0.25 + 0.75 * torch.rand(1, generator=gen, device="cuda")
+    st["rng"] = torch.randint(0, 2 ** 62, (2,), generator=gen, device="cuda", dtype=torch.int64)
+    # states after some steps on gradients of this kind
+    m = _gradients(gen, sizes, starts, total, torch.float32, 1.0) * 0.3
+    r = _gaps(m.abs() * (1.0 + torch.rand(total, generator=gen, device="cuda")) + 1e-5, sizes, starts)
+    if case["bits"] == 32:
+        st["m"], st["v"] = m, r * r
+        st["ms"] = st["rs"] = None
+    else:
+        u = torch.full((total,), 32768, dtype=torch.int32, device="cuda")
+        (st["m"], st["ms"]), (st["v"], st["rs"]) = _plain_encode(m, u, 20), _plain_encode(r, u, 19)
+    del m, r
+    if own:
+        def split(flat, unit=1):
+            if flat is None:
+                return None
+            return [flat[a // unit:-(-(a + n) // unit)] for a, n in zip(starts, sizes)]
+        st["state"] = moe.AdamState(split(st["p"]), split(st["m"]), split(st["v"]), m_scale=split(st["ms"], BLOCK),
+                                    v_scale=split(st["rs"], BLOCK), master=split(st["master"]))
+        st["opts"] = moe.AdamOptions(beta1=case["beta1"], beta2=case["beta2"], eps=case["eps"],
+                                     weight_decay=case["wd"], stochastic=case["stochastic"])
+        st["grads"] = _views(st["g"], sizes, starts)
+        if case["bits"] == 8:
+            st["vals"] = [torch.zeros(total, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            st["val_views"] = [_views(v, sizes, starts) for v in st["vals"]]
+    return st
+
+
+# ------------------------------------------------------------ plain forms ----
+def _plain_norm(c, x, res, w, b):
+    s = x if res is None else (x.float() + res.float()).to(x.dtype)
+    f = s.float()
+    mean = None
+    if c["kind"] == "layer":
+        mean = f.mean(dim=1)
+        f = f - mean[:, None]
+    rstd = 1.0 / torch.sqrt((f * f).mean(dim=1) + c["eps"])
+    y = f * rstd[:, None] * w.float()
+    if b is not None:
+        y = y + b.float()
+    return y.to(x.dtype), s if res is not None else None, mean, rstd
+
+
+def _plain_norm_grad(c, dy, s, w, mean, rstd, dx_in):
+    h = s.float()
+    if mean is not None:
+        h = h - mean[:, None]
+    h = h * rstd[:, None]
+    up = dy.float()
+    g = up * w.float()
+    dx = g - h * (g * h).mean(dim=1, keepdim=True)
+    if mean is not None:
+        dx = dx - g.mean(dim=1, keepdim=True)
+    dx = dx * rstd[:, None]
+    if dx_in is not None:
+        dx = dx + dx_in.float()
+    return dx.to(dy.dtype), (up * h).sum(dim=0), up.sum(dim=0) if c["bias"] else None
+
+
+def _plain_grad_norm(c, g):
+    norm = torch.sqrt((g.float() * c["scale"]).square().sum(dtype=torch.float64))
+    coef = c["scale"] * torch.clamp(c["max_norm"] / (norm + 1e-6), max=1.0)
+    return torch.stack([norm, coef]).float()
+
+
+def _mulhi(a, m):
+    """High 32 bits of the 64-bit product of a (below 2^32, int64) and the constant m."""
+    return ((a >> 16) * m + (((a & 0xFFFF) * m) >> 16)) >> 16
+
+
+def _plain_numbers(n, rng):
+    """One 16-bit number per element: ten rounds of Philox4x32 give the eight of a counter."""
+    dev, lo = rng.device, 0xFFFFFFFF
+    i = torch.arange(n // 8, device=dev, dtype=torch.int64)
+    seed, off = rng[0], rng[1]
+    c0, c1 = i & lo, i >> 32
+    c2, c3 = (off & lo).expand(n // 8), ((off >> 32) & lo).expand(n // 8)
+    k0, k1 = seed & lo, (seed >> 32) & lo
+    for _ in range(10):
+        h0, l0 = _mulhi(c0, 0xD2511F53), (c0 * 0xD2511F53) & lo
+        h1, l1 = _mulhi(c2, 0xCD9E8D57), (c2 * 0xCD9E8D57) & lo
+        c0, c1, c2, c3 = h1 ^ c1 ^ k0, l1, h0 ^ c3 ^ k1, l0
+        k0, k1 = (k0 + 0x9E3779B9) & lo, (k1 + 0xBB67AE85) & lo
+    words = torch.stack([c0, c1, c2, c3], dim=1)
+    return torch.stack([words & 0xFFFF, words >> 16], dim=2).reshape(-1).to(torch.int32)
+
+
+def _plain_encode(x, u, shift):
+    """Codes and scale bytes of x: per block the exponent whose top code holds the largest value (255: not finite),
+    then the value's fp32 bits, brought down to exponents 0..15, rounded at `shift` bits by the numbers u. With 20 the
+    code has a sign and three fraction bits, with 19 (no sign) four, and what is above 0 stays above 0."""
+    top = x.abs().view(torch.int32).view(-1, BLOCK).amax(dim=1)
+    e = (top + ((1 << shift) - 1)) >> 23
+    a = x.abs().view(-1, BLOCK).double() * torch.exp2(15.0 - e.clamp(max=254).double())[:, None]
+    bits = a.float().view(torch.int32).view(-1)
+    code = (bits + (u << (shift - 16))) >> shift
+    if shift == 19:
+        code = torch.where(x > 0, code.clamp(min=1), code)
+    else:
+        code = code | torch.where(torch.signbit(x), 128, 0)
+    code = torch.where((e > 254).repeat_interleave(BLOCK), torch.zeros_like(code), code)
+    return code.to(torch.uint8), e.clamp(max=255).to(torch.uint8)
+
+
+def _plain_decode(code, scale, shift):
+    c, e = code.to(torch.int32), scale.to(torch.int32)
+    mag = (c if shift == 19 else c & 127) << shift
+    x = mag.view(torch.float32).view(-1, BLOCK).double() * torch.exp2(e.double() - 15.0)[:, None]
+    x = torch.where((e == 255)[:, None], torch.full_like(x, math.nan), x).float().view(-1)
+    return x if shift == 19 else torch.where(c >= 128, -x, x)
+
+
+def _plain_adam(c, st):
+    b1, b2, t = c["beta1"], c["beta2"], c["step"]
+    p, g = st["p"], st["g"].float() * st["gscale"]
+    if c["bits"] == 8:
+        m, r = _plain_decode(st["m"], st["ms"], 20), _plain_decode(st["v"], st["rs"], 19)
+        v = r * r
+    else:
+        m, v = st["m"], st["v"]
+    m = m * b1 + g * (1.0 - b1)
+    v = v * b2 + (g * g) * (1.0 - b2)
+    r = torch.sqrt(v)
+    w = st["master"] if c["master"] else p.float()
+    c1, c2 = 1.0 - b1 ** t, math.sqrt(1.0 - b2 ** t)
+    w = w - ((c["lr"] / c1) * (m / (r / c2 + c["eps"])) + (c["lr"] * c["wd"]) * w)
+    u = _plain_numbers(p.numel(), st["rng"]) if c["bits"] == 8 or c["stochastic"] else None
+    if c["master"]:
+        st["master"].copy_(w)
+    if c["stochastic"]:
+        bits = (w.view(torch.int32) + u) & -65536
+        p.copy_(bits.view(torch.float32))
+    else:
+        p.copy_(w)
+    if c["bits"] == 32:
+        st["m"].copy_(m)
+        st["v"].copy_(v)
+        return p, st["master"], st["m"], st["v"]
+    for x, shift, code, scale in ((m, 20, "m", "ms"), (r, 19, "v", "rs")):
+        q, e = _plain_encode(x, u, shift)
+        st[code].copy_(q)
+        st[scale].copy_(e)
+    # a code has at most five significant bits: bf16 holds its value
+    return (p, st["master"], _plain_decode(st["m"], st["ms"], 20).to(torch.bfloat16),
+            _plain_decode(st["v"], st["rs"], 19).to(torch.bfloat16))
+
+
+# -------------------------------------------------------------------- run ----
+def run(st):
+    c = st["case"]
+    op = c["op"]
+    if own:
+        moe = st["moe"]
+        if op == "norm":
+            y, s, mean, rstd = moe.norm_forward(st["dims"], st["opts"], st["x"], st["w"], st["b"], residual=st["res"],
+                                                keep=True)
+            return y, s if st["res"] is not None else None, mean, rstd
+        if op == "norm_grad":
+            return moe.norm_backward(st["dims"], st["opts"], st["dy"], st["x"], st["w"], st["rstd"], mean=st["mean"],
+                                     dx_in=st["dx_in"], want_dbias=c["bias"])
+        if op == "grad_norm":
+            return moe.grad_norm(st["grads"], grad_scale=c["scale"], max_norm=c["max_norm"])
+        moe.adam_step(st["opts"], st["state"], st["grads"], lr=c["lr"], step=c["step"], gscale=st["gscale"],
+                      rng=st["rng"])
+        if c["bits"] == 32:
+            return st["p"], st["master"], st["m"], st["v"]
+        moe.adam_state_values(st["state"], m=st["val_views"][0], r=st["val_views"][1])
+        return st["p"], st["master"], st["vals"][0], st["vals"][1]
+    if op == "norm":
+        return _plain_norm(c, st["x"], st["res"], st["w"], st["b"])
+    if op == "norm_grad":
+        return _plain_norm_grad(c, st["dy"], st["x"], st["w"], st["mean"], st["rstd"], st["dx_in"])
+    if op == "grad_norm":
+        return _plain_grad_norm(c, st["g"])
+    return _plain_adam(c, st)
+
+
+def work(case):
+    op = case["op"]
+    if op in ("norm", "norm_grad"):
+        T, d, b, wb = case["T"], case["d"], 4 if case["dtype"] == "f32" else 2, 4 if case["wdtype"] == "f32" else 2
+        stats = (8 if case["kind"] == "layer" else 4) * T
+        if op == "norm":
+            return {"bytes": T * d * b * (4 if case["residual"] else 2) + stats + d * wb * (2 if case["bias"] else 1),
+                    "flops": 6 * T * d}
+        return {"bytes": T * d * b * (4 if case["residual"] else 3) + stats + d * wb + 4 * d * (2 if case["bias"] else 1),
+                "flops": 12 * T * d}
+    n = sum(_sizes(case))
+    if op == "grad_norm":
+        return {"bytes": n * (4 if case["dtype"] == "f32" else 2) + 8, "flops": 2 * n}
+    pb, gb = (4 if case["param"] == "f32" else 2), (4 if case["grad"] == "f32" else 2)
+    # 8 bits: codes and scales read and written, and the values they stand for written once (2 x 2 bytes)
+    state = 16.0 if case["bits"] == 32 else 4.0 + 4.0 / BLOCK + 4.0
+    return {"bytes": int(n * (2 * pb + gb + state + (8 if case["master"] else 0))), "flops": 18 * n}
+
+
+# ------------------------------------------------------------------ exact ----
+def _exact_norm(c, st):
+    """The norm written down in float64; its gradients by differentiation."""
+    x = st["x"]
+    if c["op"] == "norm" and st["res"] is not None:
+        x = (x.double() + st["res"].double()).float().to(x.dtype)  # the residual stream is held in its type
+    s = x.double().requires_grad_(True)
+    w = st["w"].double().requires_grad_(True)
+    b = torch.zeros_like(w) if st["b"] is None else st["b"].double()
+    b = b.detach().requires_grad_(True)
+    mean = s.mean(dim=1)
+    if c["kind"] == "layer":
+        spread = torch.sqrt(s.var(dim=1, unbiased=False) + c["eps"])
+        y = (s - mean[:, None]) / spread[:, None] * w + b
+    else:
+        spread = torch.sqrt(s.pow(2).mean(dim=1) + c["eps"])
+        y = s / spread[:, None] * w + b
+    if c["op"] == "norm":
+        return (y.detach(), x.double() if st["res"] is not None else None,
+                mean.detach() if c["kind"] == "layer" else None, (1.0 / spread).detach())
+    ds, dw, db = torch.autograd.grad((y * st["dy"].double()).sum(), [s, w, b])
+    if st["dx_in"] is not None:
+        ds = ds + st["dx_in"].double()
+    return ds, dw, db if c["bias"] else None
+
+
+def _exact_numbers(n, rng):
+    seed, off = (int(v) & 0xFFFFFFFFFFFFFFFF for v in rng.tolist())
+    mask, sh = np.uint64(0xFFFFFFFF), np.uint64(32)
+    i = np.arange(n // 8, dtype=np.uint64)
+    x = [i & mask, i >> sh, np.full_like(i, off & 0xFFFFFFFF), np.full_like(i, off >> 32)]
+    key = [seed & 0xFFFFFFFF, seed >> 32]
+    for _ in range(10):
+        a, b = x[0] * np.uint64(0xD2511F53), x[2] * np.uint64(0xCD9E8D57)
+        x = [(b >> sh) ^ x[1] ^ np.uint64(key[0]), b & mask, (a >> sh) ^ x[3] ^ np.uint64(key[1]), a & mask]
+        key = [(key[0] + 0x9E3779B9) % 2 ** 32, (key[1] + 0xBB67AE85) % 2 ** 32]
+    half = np.empty((n // 8, 8), np.uint16)
+    for j in range(4):
+        half[:, 2 * j] = (x[j] & np.uint64(0xFFFF)).astype(np.uint16)
+        half[:, 2 * j + 1] = (x[j] >> np.uint64(16)).astype(np.uint16)
+    return torch.from_numpy(half.reshape(-1).astype(np.float64)).cuda()
+
+
+def _exact_values(code, scale, fraction):
+    """What codes stand for: sign (three fraction bits only), four exponent bits, fraction, gradual underflow."""
+    c, top = code.double(), torch.exp2(scale.double() - 127.0).repeat_interleave(BLOCK)
+    sign = torch.ones_like(c)
+    if fraction == 3:
+        sign = torch.where(c >= 128, -sign, sign)
+        c = torch.where(c >= 128, c - 128, c)
+    e = torch.floor(c / 2 ** fraction)
+    f = c / 2 ** fraction - e
+    return sign * torch.where(e > 0, (1 + f) * torch.exp2(e - 15), f * torch.exp2(torch.full_like(e, -14.0))) * top
+
+
+def _exact_round(x, number, fraction):
+    """x rounded to such a code's value: up where the part of a step below it and number / 2^16 reach a step."""
+    a = x.abs().view(-1, BLOCK)
+    most = a.amax(dim=1)
+    e = torch.floor(torch.log2(most.clamp(min=2.0 ** -126)))
+    e = torch.where(most > (2.0 - 2.0 ** -fraction) * torch.exp2(e), e + 1, e)[:, None]
+    own_e = torch.floor(torch.log2(a.clamp(min=1e-300))).clamp(min=e - 14)
+    step = torch.exp2(own_e - fraction)
+    q = torch.floor(a / step + number.view(-1, BLOCK) / 65536.0) * step
+    if fraction == 4:
+        q = torch.where((a > 0) & (q == 0), torch.exp2(e - 14 - fraction).expand_as(q), q)
+    return torch.sign(x) * q.view(-1)
+
+
+def _exact_adam(c, st):
+    p = (st["master"] if c["master"] else st["p"]).double()
+    g = st["g"].double() * st["gscale"].double()
+    if c["bits"] == 8:
+        m = _exact_values(st["m"], st["ms"], 3)
+        v = _exact_values(st["v"], st["rs"], 4) ** 2
+    else:
+        m, v = st["m"].double(), st["v"].double()
+    m = c["beta1"] * m + (1 - c["beta1"]) * g
+    v = c["beta2"] * v + (1 - c["beta2"]) * g ** 2
+    del g
+    mhat, vhat = m / (1 - c["beta1"] ** c["step"]), v / (1 - c["beta2"] ** c["step"])
+    new = p - c["lr"] * c["wd"] * p - c["lr"] * mhat / (vhat.sqrt() + c["eps"])
+    del mhat, vhat
+    if c["bits"] == 8:
+        number = _exact_numbers(p.numel(), st["rng"])
+        m, v = _exact_round(m, number, 3), _exact_round(v.sqrt(), number, 4)
+    return new, new if c["master"] else None, m, v
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    if case["op"] in ("norm", "norm_grad"):
+        return _exact_norm(case, st)
+    if case["op"] == "grad_norm":
+        norm = (st["g"].double().pow(2).sum()).sqrt() * case["scale"]
+        return torch.stack([norm, case["scale"] * (case["max_norm"] / (norm + 1e-6)).clamp(max=1.0)])
+    return _exact_adam(case, st)
