@@ -168,7 +168,8 @@ def prepare(case, seed):
     if op == "grad_norm":
         st["g"] = _gradients(gen, sizes, starts, total, _type(case["dtype"]), 1.0)
         st["g"] = st["g"] / case["scale"] if case["scale"] < 1 else st["g"]  # gradients of a scaled loss
-        st["grads"] = _views(st["g"], sizes, starts)
+        if own:
+            st["grads"] = moe.GradList(_views(st["g"], sizes, starts))
         return st
     st["p"] = _gaps((torch.randn(total, generator=gen, device="cuda") * 0.0125).to(_type(case["param"])), sizes, starts)
     st["master"] = None
@@ -196,7 +197,7 @@ def prepare(case, seed):
                                     v_scale=split(st["rs"], BLOCK), master=split(st["master"]))
         st["opts"] = moe.AdamOptions(beta1=case["beta1"], beta2=case["beta2"], eps=case["eps"],
                                      weight_decay=case["wd"], stochastic=case["stochastic"])
-        st["grads"] = _views(st["g"], sizes, starts)
+        st["grads"] = moe.GradList(_views(st["g"], sizes, starts))
         if case["bits"] == 8:
             st["vals"] = [torch.zeros(total, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
             st["val_views"] = [_views(v, sizes, starts) for v in st["vals"]]
