@@ -551,6 +551,134 @@ int moe_combine_dropout(const moe_dims_t* dims, double p, const uint64_t* rng, c
 int moe_dropout_backward(const moe_dims_t* dims, double p, const uint64_t* rng, const void* dout, void* dy,
                          void* stream);
 
+/* ---- around the layer: the norm in front of it ----
+ * y = norm(s), s = x + residual: the row s is summed in fp32 and rounded to the
+ * dtype, and what is normalised is that rounded row. With d columns:
+ *   MOE_NORM_RMS:    rstd = (mean s^2 + eps)^(-1/2),            y = s rstd weight
+ *   MOE_NORM_LAYER:  rstd = (mean (s - mean s)^2 + eps)^(-1/2), y = (s - mean s) rstd weight + bias
+ * Statistics in fp32, from the differences to the mean; a row whose sums pass
+ * fp32's range is summed at a smaller scale. y is rounded once. Infinities and
+ * NaN in a row go where the formula sends them.
+ *   x, residual (NULL = 0), sum (NULL: not written; may be x or residual), y [T][d]
+ *   dtype; y may be x or residual (and is not sum);
+ *   weight, bias [d] of opts->param_dtype, or NULL (1 and 0); bias NULL for RMS;
+ *   mean, rstd [T] fp32 outputs, or NULL (mean NULL for RMS).
+ * d % 8 == 0 and d <= 16384 (MOE_ERR_UNSUPPORTED otherwise); eps in [2^-100, 2^100],
+ * else MOE_ERR_INVALID. Only T, d and dtype of dims are used. `opts` is a HOST
+ * pointer. Tensors of x's shape, weight and bias 16-byte aligned. */
+typedef enum {
+  MOE_NORM_RMS = 0,
+  MOE_NORM_LAYER = 1
+} moe_norm_kind_t;
+typedef struct {
+  int32_t kind;        /* moe_norm_kind_t */
+  int32_t param_dtype; /* moe_dtype_t of weight and bias */
+  float eps;
+} moe_norm_opts_t;
+int moe_norm_forward(const moe_dims_t* dims, const moe_norm_opts_t* opts, const void* x, const void* residual,
+                     const void* weight, const void* bias, void* sum, void* y, float* mean, float* rstd,
+                     void* stream);
+
+/* Its gradients. With h = (s - mean) rstd (RMS: s rstd) and g = dy weight:
+ *   dx = rstd (g - mean g - h mean(g h)) + dx_in   (RMS: without mean g)
+ *   dweight = sum_t dy h,  dbias = sum_t dy
+ * dx is the gradient of s, hence of x and of residual alike.
+ *   dy, s [T][d] (s: the row that was normalised: x, or the forward's sum);
+ *   weight as in the forward; mean (layer norm), rstd [T] as the forward gave them;
+ *   dx_in [T][d] (the gradient that reaches s by other ways) or NULL;
+ *   dx [T][d] (may be dy, s or dx_in); dweight, dbias [d] fp32, each NULL to leave
+ *   it out (dbias NULL for RMS).
+ * fp32 throughout, dx rounded once; sums over rows in a fixed order. T = 0 writes
+ * zero dweight and dbias. Limits as the forward's; dweight and dbias 16-byte
+ * aligned. ws: at least moe_norm_backward_workspace_bytes (0 for invalid dims),
+ * 256-byte aligned; not looked at where neither dweight nor dbias is asked for. */
+size_t moe_norm_backward_workspace_bytes(const moe_dims_t* dims, const moe_norm_opts_t* opts);
+int moe_norm_backward(const moe_dims_t* dims, const moe_norm_opts_t* opts, const void* dy, const void* s,
+                      const void* weight, const float* mean, const float* rstd, const void* dx_in, void* dx,
+                      float* dweight, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- behind the backward: the gradients' norm and the update ----
+ * Both take a list of tensors, a HOST array that is read during the call only (a
+ * captured graph holds its contents). At most 2^36 elements to a tensor and 2^20
+ * tensors (MOE_ERR_UNSUPPORTED beyond); tensors of 0 elements are passed over.
+ * Buffers need their element's alignment; where all of a tensor's are 16-byte
+ * aligned (8-bit codes: 8-byte) the loads are wide. */
+typedef struct {
+  const void* grad; /* DEVICE [n] */
+  int64_t n;
+  int64_t dtype;    /* moe_dtype_t */
+} moe_grad_t;
+
+/* out[0] = N = |grad_scale| (sum over all elements g^2)^(1/2), and the factor
+ * that unscales and clips: out[1] = grad_scale min(1, max_norm / (N + 1e-6)), or
+ * NaN where N is not finite. Squares are summed in double in a fixed order.
+ * out [2] fp32 (DEVICE). grad_scale finite, max_norm >= 0 (infinity: no clipping),
+ * else MOE_ERR_INVALID. ws: at least moe_grad_norm_workspace_bytes (0 for an
+ * invalid list), 256-byte aligned. An empty list gives N = 0. */
+size_t moe_grad_norm_workspace_bytes(const moe_grad_t* grads, int32_t count);
+int moe_grad_norm(const moe_grad_t* grads, int32_t count, double grad_scale, double max_norm, float* out, void* ws,
+                  size_t ws_bytes, void* stream);
+
+/* AdamW (decoupled weight decay) over a list of tensors, in place. With step t:
+ *   x  = gscale g
+ *   m' = beta1 m + (1 - beta1) x,   v' = beta2 v + (1 - beta2) x^2
+ *   w' = w - lr / (1 - beta1^t) m' / (sqrt(v' / (1 - beta2^t)) + eps) - lr weight_decay w
+ * in fp32; w is master where there is one, else param. param bf16 is rounded to
+ * nearest even, or with `stochastic` (without master) up or down at random so that
+ * its mean is w'. A gscale that is not finite leaves everything as it was.
+ *
+ * state_bits 32: m, v [n] fp32. state_bits 8: m, v [n] uint8 and m_scale, v_scale
+ * [ceil(n / 128)] uint8, one for each 128 elements of the tensor. A scale byte E is
+ * a biased fp32 exponent; code c of m stands for (-1)^(c >> 7) a 2^(E - 15), a the
+ * fp32 value whose bits are (c & 127) << 20, and code c of v for the ROOT of the
+ * second moment, a 2^(E - 15) with bits c << 19: four exponent bits, three (m, with
+ * a sign) or four fraction bits, gradual underflow. E = 255: NaN. All zero bytes
+ * are the state before the first step. m' and sqrt(v') are formed in fp32 and then
+ * rounded at random: E is the least exponent whose top code holds the 128 largest
+ * (255 where one is not finite), and a value is rounded away from zero where the
+ * part of a code step that it drops and u / 2^16 reach 1, u the element's 16-bit
+ * number; a root above 0 stays above 0.
+ *
+ * Numbers: elements are counted through the list, each tensor beginning at a
+ * multiple of 128; element i takes number i % 8 (low half of word 0, its high half,
+ * low half of word 1, ..) of Philox4x32 with ten rounds, key = seed, counter =
+ * {i / 8, offset} (as moe_combine_dropout's). rng: DEVICE {seed, offset}, 8-byte
+ * aligned, needed with state_bits 8 and with stochastic; states and weights of an
+ * element share its number.
+ *
+ * lr_step: DEVICE {lr, step} (two doubles, step a whole number from 1), read when
+ * the kernels run, so that a captured graph follows its owner's schedule; NULL:
+ * opts->lr and opts->step. gscale: DEVICE fp32 [1] or NULL (1).
+ * grads[i] belongs to tensors[i] and has its n. No buffer may overlap another
+ * (one that is written and appears twice: MOE_ERR_INVALID). beta1, beta2 in
+ * [0, 1), eps in [2^-100, 2^100], lr and weight_decay finite, step >= 1 (unless
+ * lr_step), else MOE_ERR_INVALID. `opts`, `tensors` and `grads` are HOST pointers. */
+typedef struct {
+  void* param;      /* [n] */
+  float* master;    /* [n] fp32, or NULL; bf16 parameters only */
+  void* m;          /* [n] */
+  void* v;          /* [n] */
+  uint8_t* m_scale; /* 8-bit states; else not looked at */
+  uint8_t* v_scale;
+  int64_t n;
+  int64_t dtype;    /* moe_dtype_t of param */
+} moe_adam_tensor_t;
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  int32_t state_bits; /* 32 or 8 */
+  int32_t stochastic; /* 0 or 1 */
+} moe_adam_opts_t;
+int moe_adam_step(const moe_adam_opts_t* opts, const moe_adam_tensor_t* tensors, const moe_grad_t* grads,
+                  int32_t count, const double* lr_step, const float* gscale, const uint64_t* rng, void* stream);
+
+/* What 8-bit states stand for: m_out[i] [n] = m and r_out[i] [n] = sqrt(v) of
+ * tensors[i] (HOST arrays of DEVICE pointers), of out_dtype (bf16 holds every
+ * code's value from 2^-126 on; smaller ones are rounded). param, master are not
+ * looked at. */
+int moe_adam_state_values(const moe_adam_tensor_t* tensors, int32_t count, void* const* m_out, void* const* r_out,
+                          int out_dtype, void* stream);
+
 /* ---- stage timing (instrumentation; process-wide, not thread-safe) ----
  * While enabled, every kernel the library launches is bracketed by HIP events
  * recorded on the stream it is launched on. Stages: */
@@ -583,7 +711,11 @@ enum {
   MOE_STAGE_GATE_BWD = 25,     /* dense gate gradients */
   MOE_STAGE_COMBINE_DROP = 26, /* combine with dropout */
   MOE_STAGE_DROP_BWD = 27,     /* dropout backward */
-  MOE_NUM_STAGES = 28
+  MOE_STAGE_NORM = 28,         /* norm */
+  MOE_STAGE_NORM_BWD = 29,     /* norm backward */
+  MOE_STAGE_GRAD_NORM = 30,    /* 2-norm of the gradients */
+  MOE_STAGE_ADAM = 31,         /* AdamW update; values of its states */
+  MOE_NUM_STAGES = 32
 };
 /* Start recording; `capacity` = launches per stage to keep (host memory only);
  * `stage_mask` = bit s set records stage s (0 = every stage). Discards

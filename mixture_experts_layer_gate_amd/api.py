@@ -7,6 +7,7 @@ is loaded on first use; if it is missing, calls raise -- there is no fallback.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from dataclasses import dataclass, fields
@@ -20,7 +21,7 @@ _LIB_NAME = "libmoe_amd.so"
 STAGES = ["gate", "topk", "hist", "scan", "scatter", "plan", "fc1", "fc2", "combine", "dispatch",
           "bwd_wt", "bwd_fc1", "bwd_dh", "bwd_swiglu", "bwd_route", "bwd_dx", "bwd_dxsum", "bwd_act_t",
           "bwd_wg2", "bwd_wg13", "bwd_gate", "ffn_fused", "select", "balance", "select_grad", "gate_grad",
-          "combine_drop", "drop_grad"]
+          "combine_drop", "drop_grad", "norm", "norm_grad", "grad_norm", "adam"]
 MOE_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 # Every symbol include/moe.h declares.
@@ -34,7 +35,8 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_workspace_bytes", "moe_route
            "moe_layer_backward_saved", "moe_layer_backward_ex", "moe_route_select", "moe_route_scored",
            "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_select_backward",
            "moe_gate_backward_workspace_bytes", "moe_gate_backward", "moe_experts_backward", "moe_combine_dropout",
-           "moe_dropout_backward"]
+           "moe_dropout_backward", "moe_norm_forward", "moe_norm_backward_workspace_bytes", "moe_norm_backward",
+           "moe_grad_norm_workspace_bytes", "moe_grad_norm", "moe_adam_step", "moe_adam_state_values"]
 
 # Bytes of the static scratch moe_layer_forward_noalloc uses (MOE_NOALLOC_SCRATCH_BYTES in include/moe.h).
 NOALLOC_SCRATCH_BYTES = 128 << 20
@@ -110,6 +112,46 @@ class RouteOptions(_Frozen):
                           int(bool(self.renormalise)), self.scale)
 
 
+class _NormOpts(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("param_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+@dataclass(frozen=True)
+class NormOptions(_Frozen):
+    """The norm in front of the layer: kind "rms" (no mean, no bias) or "layer", eps
+    under the root, and the type of its weight and bias (fp32 or bf16)."""
+    kind: str = "rms"
+    eps: float = 1e-6
+    param_dtype: torch.dtype = torch.float32
+
+    def __post_init__(self):
+        if self.kind not in ("rms", "layer"):
+            raise ValueError(f"kind must be 'rms' or 'layer', not {self.kind!r}")
+        if self.param_dtype not in MOE_DTYPE:
+            raise ValueError("param_dtype must be torch.float32 or torch.bfloat16")
+
+    def c(self) -> _NormOpts:
+        return _NormOpts(int(self.kind == "layer"), MOE_DTYPE[self.param_dtype], self.eps)
+
+
+class _AdamOpts(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("state_bits", ctypes.c_int32), ("stochastic", ctypes.c_int32)]
+
+
+@dataclass(frozen=True)
+class AdamOptions:
+    """What adam_step keeps from step to step: the moments' decay rates, eps beside the
+    root of the second moment, the decoupled weight decay, and whether bf16 parameters
+    without master weights are rounded stochastically."""
+    beta1: float = 0.9
+    beta2: float = 0.999
+    eps: float = 1e-8
+    weight_decay: float = 0.0
+    stochastic: bool = False
+
+
 def library_path() -> str:
     return os.environ.get("MOE_AMD_LIB", os.path.join(_PKG, _LIB_NAME))
 
@@ -174,6 +216,16 @@ def load_library():
     lib.moe_experts_backward.argtypes = [_DP] + [_P] * 12 + [ctypes.c_int] + [_P] * 6 + [_S, _P]
     lib.moe_combine_dropout.argtypes = [_DP, ctypes.c_double] + [_P] * 7
     lib.moe_dropout_backward.argtypes = [_DP, ctypes.c_double] + [_P] * 4
+    np_ = ctypes.POINTER(_NormOpts)
+    lib.moe_norm_forward.argtypes = [_DP, np_] + [_P] * 9
+    lib.moe_norm_backward_workspace_bytes.restype = _S
+    lib.moe_norm_backward_workspace_bytes.argtypes = [_DP, np_]
+    lib.moe_norm_backward.argtypes = [_DP, np_] + [_P] * 10 + [_S, _P]
+    lib.moe_grad_norm_workspace_bytes.restype = _S
+    lib.moe_grad_norm_workspace_bytes.argtypes = [_P, ctypes.c_int32]
+    lib.moe_grad_norm.argtypes = [_P, ctypes.c_int32, ctypes.c_double, ctypes.c_double, _P, _P, _S, _P]
+    lib.moe_adam_step.argtypes = [ctypes.POINTER(_AdamOpts), _P, _P, ctypes.c_int32] + [_P] * 4
+    lib.moe_adam_state_values.argtypes = [_P, ctypes.c_int32, _P, _P, ctypes.c_int, _P]
     lib.moe_timing_enable.argtypes = [ctypes.c_int, ctypes.c_uint]
     lib.moe_timing_read.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int)]
     lib.moe_probe_cus.restype = ctypes.c_int
@@ -185,7 +237,8 @@ def load_library():
                "moe_layer_forward_packed", "moe_layer_forward_noalloc", "moe_layer_forward_fused_packed",
                "moe_timing_enable", "moe_timing_disable", "moe_timing_read", "moe_probe_hbm_read", "moe_probe_mfma",
                "moe_route_select", "moe_route_scored", "moe_balance_loss", "moe_route_select_backward",
-               "moe_gate_backward", "moe_experts_backward", "moe_combine_dropout", "moe_dropout_backward"):
+               "moe_gate_backward", "moe_experts_backward", "moe_combine_dropout", "moe_dropout_backward",
+               "moe_norm_forward", "moe_norm_backward", "moe_grad_norm", "moe_adam_step", "moe_adam_state_values"):
         getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -891,6 +944,313 @@ def dropout_backward(dims: Dims, p: float, rng, dout, dy=None, stream=None):
     if st:
         _check("moe_dropout_backward", st)
     return o
+
+
+# ---- around the layer: the norm in front of it, the gradients' norm, the update ----
+def norm_forward(dims: Dims, opts: NormOptions, x, weight=None, bias=None, residual=None, sum=None, y=None, mean=None,
+                 rstd=None, keep=False, stream=None):
+    """y = norm(x + residual) over the rows of x [T][d], times weight [d] plus bias [d]
+    (None: 1 and 0). Returns (y, s, mean, rstd): s [T][d] is the row that was normalised (x
+    itself without a residual; sum may be x or residual to write it there), mean and rstd
+    [T] fp32 are what norm_backward takes (given, or made with keep=True; mean is None for
+    an RMS norm)."""
+    lib = _lib or load_library()
+    dev = x.device
+    scope = _enter("x", dev, stream)
+    try:
+        T, d, dt, wt = dims.T, dims.d, dims.dtype, opts.param_dtype
+        px = _in(x, "x", dt, (T, d), dev)
+        pr = _opt(residual, "residual", dt, (T, d), dev)
+        pw = _opt(weight, "weight", wt, (d,), dev)
+        pb = _opt(bias, "bias", wt, (d,), dev)
+        s = x
+        if residual is not None:
+            s = _new(sum, "sum", dt, (T, d), dev)
+        elif sum is not None:
+            raise ValueError("sum needs a residual")
+        o = _new(y, "y", dt, (T, d), dev)
+        if mean is not None or (keep and opts.kind == "layer"):
+            mean = _new(mean, "mean", torch.float32, (T,), dev)
+        if rstd is not None or keep:
+            rstd = _new(rstd, "rstd", torch.float32, (T,), dev)
+        st = lib.moe_norm_forward(dims.ref(), opts.ref(), px, pr, pw, pb, None if residual is None else s.data_ptr(),
+                                  o.data_ptr(), _ptr(mean), _ptr(rstd), _here(dev))
+    finally:
+        _leave(scope)
+    if st:
+        _check("moe_norm_forward", st)
+    return o, s, mean, rstd
+
+
+def norm_backward_workspace_bytes(dims: Dims, opts: NormOptions) -> int:
+    return _sized(dims, ("norm", opts), lambda: load_library().moe_norm_backward_workspace_bytes(dims.ref(), opts.ref()))
+
+
+def norm_backward(dims: Dims, opts: NormOptions, dy, s, weight, rstd, mean=None, dx_in=None, dx=None, dweight=None,
+                  dbias=None, want_dweight=True, want_dbias=False, ws=None, stream=None):
+    """Gradients of norm_forward for dy [T][d]: s, rstd (and mean for a layer norm) as the
+    forward returned them, dx_in [T][d] the gradient that reaches s by other ways (added to
+    dx). dx may be dy, s or dx_in. Returns (dx [T][d], dweight [d] fp32, dbias [d] fp32;
+    what is not wanted is None, unless its tensor is given)."""
+    lib = _lib or load_library()
+    dev = dy.device
+    scope = _enter("dy", dev, stream)
+    try:
+        T, d, dt, f32 = dims.T, dims.d, dims.dtype, torch.float32
+        pd = _in(dy, "dy", dt, (T, d), dev)
+        ps = _in(s, "s", dt, (T, d), dev)
+        pw = _opt(weight, "weight", opts.param_dtype, (d,), dev)
+        pr = _in(rstd, "rstd", f32, (T,), dev)
+        pm = _opt(mean, "mean", f32, (T,), dev)
+        pi = _opt(dx_in, "dx_in", dt, (T, d), dev)
+        o = _new(dx, "dx", dt, (T, d), dev)
+        w = pws = None
+        nws = 0
+        if want_dweight or dweight is not None:
+            dweight = _new(dweight, "dweight", f32, (d,), dev)
+        if want_dbias or dbias is not None:
+            dbias = _new(dbias, "dbias", f32, (d,), dev)
+        if dweight is not None or dbias is not None:
+            w = _scratch(ws, norm_backward_workspace_bytes(dims, opts) if ws is None else 0, dev)
+            pws, nws = w.data_ptr(), w.numel() * w.element_size()
+        st = lib.moe_norm_backward(dims.ref(), opts.ref(), pd, ps, pw, pm, pr, pi, o.data_ptr(), _ptr(dweight),
+                                   _ptr(dbias), pws, nws, _here(dev))
+    finally:
+        _leave(scope)
+    if st:
+        _check("moe_norm_backward", st)
+    return o, dweight, dbias
+
+
+def _flat(t: torch.Tensor, name: str, dtypes, n, dev) -> int:
+    """The pointer of one tensor of a list, checked."""
+    if t.device != dev or t.dtype not in dtypes or not t.is_contiguous() or (n is not None and t.numel() != n):
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    return t.data_ptr()
+
+
+def _list_device(tensors, name: str) -> torch.device:
+    if not tensors:
+        raise ValueError(f"{name} is empty")
+    return tensors[0].device
+
+
+class GradList:
+    """Gradients that a program keeps in place from step to step, checked once: grad_norm
+    and adam_step take it where they take a list of tensors. It holds the tensors; their
+    memory must not be replaced under it (Tensor.data = .., set_, resize_)."""
+
+    def __init__(self, grads):
+        self.tensors = [t.detach() for t in grads]
+        self.device = _list_device(self.tensors, "grads")
+        kinds = tuple(MOE_DTYPE)
+        rows = array.array("q")
+        for i, t in enumerate(self.tensors):
+            p = _flat(t, f"grads[{i}]", kinds, None, self.device)
+            rows.extend((p, t.numel(), MOE_DTYPE[t.dtype]))
+        self._rows = rows
+        self._ptr = rows.buffer_info()[0]
+        self._ws = None
+
+    def __len__(self):
+        return len(self.tensors)
+
+    def __reduce__(self):
+        """Copies and pickles are made anew from the tensors: addresses are not carried over."""
+        return GradList, (self.tensors,)
+
+
+class AdamState:
+    """Parameters and their AdamW states, checked once and updated in place by adam_step:
+    lists of contiguous tensors, one entry to a parameter (fp32 or bf16). m and v are
+    fp32 of the parameter's size, or uint8 codes with uint8 scales m_scale, v_scale
+    [ceil(n / 128)] (v then codes the second moment's root); all zeros is the state before
+    the first step. master (None, or None for single tensors): fp32 weights that a bf16
+    parameter is the rounding of. It holds the tensors; their memory must not be replaced
+    under it (Tensor.data = .., set_, resize_)."""
+
+    def __init__(self, params, m, v, m_scale=None, v_scale=None, master=None):
+        k = len(params)
+        self.device = dev = _list_device(params, "params")
+        self.bits = 8 if m and m[0].dtype is torch.uint8 else 32
+        if self.bits == 8 and (m_scale is None or v_scale is None):
+            raise ValueError("8-bit states need m_scale and v_scale")
+        if self.bits == 32 and (m_scale is not None or v_scale is not None):
+            raise ValueError("m_scale and v_scale belong to 8-bit states")
+        lists = {"params": params, "m": m, "v": v}
+        if self.bits == 8:
+            lists.update(m_scale=m_scale, v_scale=v_scale)
+        if master is not None:
+            lists["master"] = master
+        for name, ts in lists.items():
+            if len(ts) != k:
+                raise ValueError(f"{name} has {len(ts)} tensors, expected {k}")
+            setattr(self, name, [None if t is None else t.detach() for t in ts])
+        if self.bits == 32:
+            self.m_scale = self.v_scale = None
+        if master is None:
+            self.master = None
+        kind = (torch.uint8,) if self.bits == 8 else (torch.float32,)
+        rows, spans = array.array("q"), []
+
+        def take(t, name, dtypes, n):
+            p = _flat(t, name, dtypes, n, dev)
+            if t.numel():
+                spans.append((p, p + t.numel() * t.element_size(), name))
+            return p
+        for i in range(k):
+            p = self.params[i]
+            n = p.numel()
+            pp = take(p, f"params[{i}]", tuple(MOE_DTYPE), n)
+            pw = 0
+            if self.master is not None and self.master[i] is not None:
+                if p.dtype is not torch.bfloat16:
+                    raise ValueError(f"master[{i}]: only bf16 parameters have master weights")
+                pw = take(self.master[i], f"master[{i}]", (torch.float32,), n)
+            pm, pv = take(self.m[i], f"m[{i}]", kind, n), take(self.v[i], f"v[{i}]", kind, n)
+            qm = qv = 0
+            if self.bits == 8:
+                nb = -(-n // 128)
+                qm = take(self.m_scale[i], f"m_scale[{i}]", (torch.uint8,), nb)
+                qv = take(self.v_scale[i], f"v_scale[{i}]", (torch.uint8,), nb)
+            rows.extend((pp, pw, pm, pv, qm, qv, n, MOE_DTYPE[p.dtype]))
+        spans.sort()
+        for a, b in zip(spans, spans[1:]):
+            if b[0] < a[1]:
+                raise ValueError(f"{a[2]} and {b[2]} overlap")
+        self._rows = rows
+        self._ptr = rows.buffer_info()[0]
+
+    def __len__(self):
+        return len(self.params)
+
+    def __reduce__(self):
+        """Copies and pickles are made anew from the tensors: addresses are not carried over."""
+        return AdamState, (self.params, self.m, self.v, self.m_scale, self.v_scale, self.master)
+
+
+def adam_state(params, bits: int = 32, master: bool = False) -> AdamState:
+    """New AdamW states (all zeros) for a list of parameters, in 32 or 8 bits; master=True
+    adds fp32 master weights to the bf16 ones."""
+    if bits not in (32, 8):
+        raise ValueError("bits must be 32 or 8")
+    kind = torch.float32 if bits == 32 else torch.uint8
+
+    def zeros(n, dtype, p):
+        return torch.zeros(n, dtype=dtype, device=p.device)
+    m, v = ([zeros(p.numel(), kind, p) for p in params] for _ in range(2))
+    ms = vs = None
+    if bits == 8:
+        ms, vs = ([zeros(-(-p.numel() // 128), torch.uint8, p) for p in params] for _ in range(2))
+    w = None
+    if master:
+        w = [p.detach().float() if p.dtype is torch.bfloat16 else None for p in params]
+    return AdamState(params, m, v, ms, vs, w)
+
+
+def _grad_list(grads) -> GradList:
+    return grads if isinstance(grads, GradList) else GradList(grads)
+
+
+def grad_norm_workspace_bytes(grads) -> int:
+    g = _grad_list(grads)
+    return int(load_library().moe_grad_norm_workspace_bytes(g._ptr, len(g)))
+
+
+def grad_norm(grads, grad_scale: float = 1.0, max_norm: float = float("inf"), out=None, ws=None, stream=None):
+    """2-norm over all of a list of gradients (fp32 or bf16; a list of tensors or a
+    GradList) times grad_scale, and the factor that unscales and clips them to max_norm.
+    Returns out [2] fp32: the norm, and grad_scale * min(1, max_norm / (norm + 1e-6)) for
+    adam_step's gscale (out[1:]), NaN where the norm is not finite."""
+    lib = _lib or load_library()
+    g = _grad_list(grads)
+    dev = g.device
+    scope = _enter("grads[0]", dev, stream)
+    try:
+        o = _new(out, "out", torch.float32, (2,), dev)
+        if ws is None and g._ws is None:
+            g._ws = grad_norm_workspace_bytes(g)
+        w = _scratch(ws, g._ws or 0, dev)
+        st = lib.moe_grad_norm(g._ptr, len(g), grad_scale, max_norm, o.data_ptr(), w.data_ptr(),
+                               w.numel() * w.element_size(), _here(dev))
+    finally:
+        _leave(scope)
+    if st:
+        _check("moe_grad_norm", st)
+    return o
+
+
+def adam_step(opts: AdamOptions, state: AdamState, grads, lr=None, step=None, lr_step=None, gscale=None, rng=None,
+              stream=None):
+    """One AdamW step of state's parameters with grads (a list of tensors in the parameters'
+    order, fp32 or bf16, or a GradList), in place. lr and step (from 1) are numbers, or
+    lr_step is a float64 tensor [2] on the GPU that holds both and is read when the step
+    runs (a captured graph's owner updates it between replays). gscale: fp32 tensor [1] that
+    the gradients are multiplied by (grad_norm's out[1:]); one that is not finite leaves
+    everything as it was. rng: int64 tensor [2] on the GPU, seed and offset (another offset
+    for every step), needed for 8-bit states and stochastic rounding. Returns state."""
+    lib = _lib or load_library()
+    g = _grad_list(grads)
+    dev = state.device
+    if len(g) != len(state):
+        raise ValueError(f"grads has {len(g)} tensors, expected {len(state)}")
+    if g.device != dev:
+        raise ValueError(f"grads[0] is on {g.device}, expected {dev}")
+    if lr_step is None and (lr is None or step is None):
+        raise ValueError("lr and step, or lr_step, are needed")
+    if rng is None and (state.bits == 8 or opts.stochastic):
+        raise ValueError("8-bit states and stochastic rounding need rng")
+    scope = _enter("params[0]", dev, stream)
+    try:
+        pl = _opt(lr_step, "lr_step", torch.float64, (2,), dev)
+        pg = _opt(gscale, "gscale", torch.float32, (1,), dev)
+        pr = _opt(rng, "rng", torch.int64, (2,), dev)
+        o = _AdamOpts(0.0 if lr is None else lr, opts.beta1, opts.beta2, opts.eps, opts.weight_decay,
+                      1 if step is None else step, state.bits, int(bool(opts.stochastic)))
+        st = lib.moe_adam_step(ctypes.byref(o), state._ptr, g._ptr, len(g), pl, pg, pr, _here(dev))
+    finally:
+        _leave(scope)
+    if st:
+        _check("moe_adam_step", st)
+    return state
+
+
+def adam_state_values(state: AdamState, m=None, r=None, dtype=torch.bfloat16, stream=None):
+    """What 8-bit states stand for, as lists of tensors of the states' sizes (given, or new
+    of dtype, fp32 or bf16): (first moments, roots of the second moments)."""
+    lib = _lib or load_library()
+    dev = state.device
+    if state.bits != 8:
+        raise ValueError("the states are not held in 8 bits")
+    if m is not None and len(m):
+        dtype = m[0].dtype
+    if dtype not in MOE_DTYPE:
+        raise ValueError("dtype must be torch.float32 or torch.bfloat16")
+    scope = _enter("params[0]", dev, stream)
+    try:
+        ptrs = []
+        out = []
+        for name, ts in (("m", m), ("r", r)):
+            if ts is None:
+                ts = [torch.empty(c.numel(), dtype=dtype, device=dev) for c in state.m]
+            if len(ts) != len(state):
+                raise ValueError(f"{name} has {len(ts)} tensors, expected {len(state)}")
+            ptrs.append(array.array("q", [_flat(t, f"{name}[{i}]", (dtype,), c.numel(), dev)
+                                          for i, (t, c) in enumerate(zip(ts, state.m))]))
+            out.append(ts)
+        st = lib.moe_adam_state_values(state._ptr, len(state), ptrs[0].buffer_info()[0], ptrs[1].buffer_info()[0],
+                                       MOE_DTYPE[dtype], _here(dev))
+    finally:
+        _leave(scope)
+    if st:
+        _check("moe_adam_state_values", st)
+    return out[0], out[1]
 
 
 def timing_enable(capacity: int, stages=None):

@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_amd.so")
 ARCH = "gfx950"
 SOURCES = ["route.hip", "dispatch.hip", "ffn.hip", "combine.hip", "backward.hip", "moe_abi.hip", "probes.hip",
-           "select.hip", "gate_backward.hip", "dropout.hip", "router_abi.hip"]
+           "select.hip", "gate_backward.hip", "dropout.hip", "router_abi.hip", "norm.hip", "optim.hip", "train_abi.hip"]
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-fPIC", "-std=c++17",
     # no packed-fp32 instructions in any generated code

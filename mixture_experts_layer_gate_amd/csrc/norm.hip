@@ -1,0 +1,432 @@
+// The norm in front of the layer (RMS or layer norm, the residual added) and its
+// gradients. The contract is in include/moe.h.
+#include "common.h"
+#include "train.h"
+
+namespace moe {
+
+namespace {
+
+// One 16-byte vector of a row: eight bf16 or four fp32 values.
+template <int kDtype> constexpr int kVec = kDtype == 1 ? 8 : 4;
+
+template <int kDtype>
+__device__ __forceinline__ void unpack(const uint4& u, float (&v)[kVec<kDtype>]) {
+  if constexpr (kDtype == 1) {
+    v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
+    v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
+  } else {
+    v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
+    v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+  }
+}
+
+// Rounds to nearest even and keeps NaN (an fp32 to bf16 conversion instruction).
+template <int kDtype>
+__device__ __forceinline__ uint4 pack(const float (&v)[kVec<kDtype>]) {
+  if constexpr (kDtype == 1) {
+    bf16x8_t o;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = static_cast<__bf16>(v[j]);
+    return *reinterpret_cast<uint4*>(&o);
+  } else {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+}
+
+// Elements N i .. N i + N - 1 of a weight vector of either type.
+template <int N>
+__device__ __forceinline__ void load_w(const void* p, int w_bf16, int i, float (&v)[N]) {
+  if (w_bf16) {
+    if constexpr (N == 8) {
+      unpack<1>(reinterpret_cast<const uint4*>(p)[i], v);
+    } else {
+      const uint2 u = reinterpret_cast<const uint2*>(p)[i];
+      v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) {
+      const float4 a = reinterpret_cast<const float4*>(p)[i * (N / 4) + q];
+      v[4 * q] = a.x; v[4 * q + 1] = a.y; v[4 * q + 2] = a.z; v[4 * q + 3] = a.w;
+    }
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// Sum over the workgroup (kWaveRow: over the wave), the same value in every
+// thread. red: one float per wave; alternating halves need no second barrier.
+template <bool kWaveRow>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = wave_sum(v);
+  if constexpr (kWaveRow) return v;
+  const int nw = blockDim.x >> 6;
+  if (nw == 1) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = 0.0f;
+  for (int i = 0; i < nw; ++i) v += red[i];
+  return v;
+}
+
+constexpr float kShrink = 0x1p-80f;
+
+// One row to a workgroup (kWaveRow: to a wave), kept in registers as fp32: NV
+// vectors to a thread. The variance is that of the differences to the mean, taken
+// from the registers. A row whose sums pass fp32's range is scaled by 2^-80 and
+// summed again, so the statistics are right for every finite row.
+template <int kDtype, bool kLayer, int NV, bool kWaveRow>
+__global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a) {
+  constexpr int V = kVec<kDtype>;
+  __shared__ float red[2][16];
+  const int nvec = a.d / V;
+  const int lanes = kWaveRow ? 64 : blockDim.x;
+  const int tid = kWaveRow ? (threadIdx.x & 63) : threadIdx.x;
+  const int per = kWaveRow ? (blockDim.x >> 6) : 1;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * per + (kWaveRow ? (threadIdx.x >> 6) : 0); t < a.T;
+       t += static_cast<int64_t>(gridDim.x) * per) {
+    float v[NV][V];
+    const uint4* px = reinterpret_cast<const uint4*>(a.x) + t * nvec;
+    const uint4* pr = reinterpret_cast<const uint4*>(a.residual) + t * nvec;
+    uint4 ux[NV], ur[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = tid + j * lanes;
+      ux[j] = c < nvec ? px[c] : make_uint4(0, 0, 0, 0);
+      if (a.residual) ur[j] = c < nvec ? pr[c] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = tid + j * lanes;
+      unpack<kDtype>(ux[j], v[j]);
+      if (a.residual) {
+        float r[V];
+        unpack<kDtype>(ur[j], r);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[j][i] += r[i];
+        const uint4 o = pack<kDtype>(v[j]);
+        unpack<kDtype>(o, v[j]);
+        if (a.sum && c < nvec) reinterpret_cast<uint4*>(a.sum)[t * nvec + c] = o;
+      }
+    }
+    float mean = 0.0f, var = 0.0f;
+    bool small = false;  // scaled by kShrink
+    for (;;) {
+      if constexpr (kLayer) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) s += v[j][i];
+        mean = row_sum<kWaveRow>(s, red[0]) * inv_d;
+      }
+      float q = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (tid + j * lanes < nvec) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float e = kLayer ? v[j][i] - mean : v[j][i];
+            q = fmaf(e, e, q);
+          }
+        }
+      var = row_sum<kWaveRow>(q, red[1]) * inv_d;
+      if (small || var < INFINITY) break;
+      small = true;
+      if (!kWaveRow) __syncthreads();  // red is written again
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[j][i] *= kShrink;
+    }
+    float rstd, mul, mean_out = mean;
+    if (!small) {
+      rstd = mul = 1.0f / sqrtf(var + a.eps);
+    } else {
+      const double up = 1.0 / static_cast<double>(kShrink);
+      const double r = 1.0 / sqrt(static_cast<double>(var) * up * up + static_cast<double>(a.eps));
+      rstd = static_cast<float>(r);
+      mul = static_cast<float>(fmin(r * up, 0x1.fffffep127));
+      mean_out = static_cast<float>(static_cast<double>(mean) * up);
+    }
+    if (tid == 0) {
+      if (kLayer && a.mean) a.mean[t] = mean_out;
+      if (a.rstd) a.rstd[t] = rstd;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = tid + j * lanes;
+      if (c >= nvec) continue;
+      float w[V], b[V];
+      if (a.w) load_w<V>(a.w, a.w_bf16, c, w);
+      if (a.b) load_w<V>(a.b, a.w_bf16, c, b);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float y = (kLayer ? v[j][i] - mean : v[j][i]) * mul;
+        if (a.w) y *= w[i];
+        if (a.b) y += b[i];
+        v[j][i] = y;
+      }
+      reinterpret_cast<uint4*>(a.y)[t * nvec + c] = pack<kDtype>(v[j]);
+    }
+    if (!kWaveRow) __syncthreads();  // red is written again
+  }
+}
+
+// Gradients: with h = (x - mean) rstd and g = dy w,
+//   dx = rstd (g - mean(g) - h mean(g h)) + dx_in      (mean(g): layer norm)
+//   dw = sum_t dy h,  db = sum_t dy.
+// A workgroup takes every parts-th row and keeps its columns' sums of dw and db
+// in registers; the parts are summed by norm_parts_kernel in their order. Both
+// row means come from one exchange between the waves.
+// Differences to the mean are formed at half size and rstd at double, so that
+// neither passes fp32's range where h does not.
+template <int kDtype, bool kLayer, int NV, bool kWaveRow>
+__global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGradArgs a) {
+  constexpr int V = kVec<kDtype>;
+  __shared__ float2 red[2][16];
+  const int nvec = a.d / V;
+  const int lanes = kWaveRow ? 64 : blockDim.x;
+  const int tid = kWaveRow ? (threadIdx.x & 63) : threadIdx.x;
+  const int nw = blockDim.x >> 6;
+  const int per = kWaveRow ? nw : 1;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per;
+  float aw[NV][V], ab[NV][V], w[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) aw[j][i] = ab[j][i] = 0.0f, w[j][i] = 1.0f;
+    if (a.w && tid + j * lanes < nvec) load_w<V>(a.w, a.w_bf16, tid + j * lanes, w[j]);
+  }
+  int half = 0;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * per + (kWaveRow ? (threadIdx.x >> 6) : 0); t < a.T; t += step) {
+    uint4 ud[NV], ux[NV], ui[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = tid + j * lanes;
+      const bool in = c < nvec;
+      const int64_t at = t * nvec + c;
+      ud[j] = in ? reinterpret_cast<const uint4*>(a.dy)[at] : make_uint4(0, 0, 0, 0);
+      ux[j] = in ? reinterpret_cast<const uint4*>(a.x)[at] : make_uint4(0, 0, 0, 0);
+      if (a.dx_in) ui[j] = in ? reinterpret_cast<const uint4*>(a.dx_in)[at] : make_uint4(0, 0, 0, 0);
+    }
+    const float rstd = a.rstd[t], r2 = 2.0f * rstd, m2 = kLayer ? -0.5f * a.mean[t] : 0.0f;
+    float h[NV][V], g[NV][V];
+    float sg = 0.0f, sh = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      unpack<kDtype>(ux[j], h[j]);
+      unpack<kDtype>(ud[j], g[j]);
+      const bool in = tid + j * lanes < nvec;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        h[j][i] = in ? fmaf(h[j][i], 0.5f, m2) * r2 : 0.0f;
+        aw[j][i] = fmaf(g[j][i], h[j][i], aw[j][i]);
+        if constexpr (kLayer) ab[j][i] += g[j][i];
+        g[j][i] *= w[j][i];
+        if constexpr (kLayer) sg += g[j][i];
+        sh = fmaf(g[j][i], h[j][i], sh);
+      }
+    }
+    if constexpr (kLayer) sg = wave_sum(sg);
+    sh = wave_sum(sh);
+    if constexpr (!kWaveRow) {
+      if (nw > 1) {
+        if ((threadIdx.x & 63) == 0) red[half][threadIdx.x >> 6] = make_float2(sg, sh);
+        __syncthreads();
+        sg = sh = 0.0f;
+        for (int i = 0; i < nw; ++i) {
+          const float2 p = red[half][i];
+          sg += p.x;
+          sh += p.y;
+        }
+        half ^= 1;
+      }
+    }
+    sg *= inv_d;
+    sh *= inv_d;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = tid + j * lanes;
+      if (c >= nvec) continue;
+      float o[V];
+      if (a.dx_in) unpack<kDtype>(ui[j], o);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float e = fmaf(-h[j][i], sh, g[j][i]);
+        if constexpr (kLayer) e -= sg;
+        o[i] = a.dx_in ? fmaf(e, rstd, o[i]) : e * rstd;
+      }
+      reinterpret_cast<uint4*>(a.dx)[t * nvec + c] = pack<kDtype>(o);
+    }
+  }
+  // this workgroup's part
+  if constexpr (kWaveRow) {
+    __shared__ float joined[64 * NV * V];
+    for (int which = 0; which < (kLayer ? 2 : 1); ++which) {
+      float* part = which == 0 ? a.part_w : a.part_b;
+      if (!part) continue;
+      for (int k = 0; k < nw; ++k) {
+        __syncthreads();
+        if ((threadIdx.x >> 6) == k) {
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              float* p = joined + (j * V + i) * 64 + tid;
+              const float v = which == 0 ? aw[j][i] : ab[j][i];
+              *p = k == 0 ? v : *p + v;
+            }
+        }
+      }
+      if ((threadIdx.x >> 6) == nw - 1) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int c = tid + j * 64;
+          if (c >= nvec) continue;
+          float4* p = reinterpret_cast<float4*>(part + static_cast<int64_t>(blockIdx.x) * a.d + c * V);
+#pragma unroll
+          for (int q = 0; q < V / 4; ++q) {
+            const float* f = joined + (j * V + 4 * q) * 64 + tid;
+            p[q] = make_float4(f[0], f[64], f[128], f[192]);
+          }
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = tid + j * lanes;
+      if (c >= nvec) continue;
+      const int64_t at = static_cast<int64_t>(blockIdx.x) * a.d + c * V;
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q) {
+        if (a.part_w)
+          reinterpret_cast<float4*>(a.part_w + at)[q] =
+              make_float4(aw[j][4 * q], aw[j][4 * q + 1], aw[j][4 * q + 2], aw[j][4 * q + 3]);
+        if (kLayer && a.part_b)
+          reinterpret_cast<float4*>(a.part_b + at)[q] =
+              make_float4(ab[j][4 * q], ab[j][4 * q + 1], ab[j][4 * q + 2], ab[j][4 * q + 3]);
+      }
+    }
+  }
+}
+
+// Column sums of the parts: 16 columns to a workgroup (64 bytes of a part's row),
+// 64 threads to each four of them, joined through LDS in a fixed order.
+__global__ __launch_bounds__(256) void norm_parts_kernel(const float* __restrict__ part_w,
+                                                         const float* __restrict__ part_b, int parts, int d,
+                                                         float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float4 join[64][4];
+  const float* part = blockIdx.y == 0 ? part_w : part_b;
+  float* out = blockIdx.y == 0 ? dw : db;
+  if (!out) return;
+  const int q = threadIdx.x & 3, g = threadIdx.x >> 2;
+  const int c = blockIdx.x * 16 + q * 4;
+  float4 s = make_float4(0, 0, 0, 0);
+  if (c < d) {
+    for (int p = g; p < parts; p += 64) {
+      const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(p) * d + c);
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+  }
+  join[g][q] = s;
+  for (int n = 32; n > 0; n >>= 1) {
+    __syncthreads();
+    if (g < n) {
+      const float4 v = join[g + n][q];
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      join[g][q] = s;
+    }
+  }
+  if (g == 0 && c < d) *reinterpret_cast<float4*>(out + c) = s;
+}
+
+struct Shape {
+  bool wave;    // one row to a wave
+  int nv;       // vectors to a thread
+  int threads;
+};
+
+Shape row_shape(int dtype, int64_t d, int most) {
+  const int64_t nvec = d / (dtype == 1 ? 8 : 4);
+  // rows of at most 128 vectors: a wave to each, four to a workgroup
+  if (nvec <= 64) return {true, 1, 256};
+  if (nvec <= 128) return {true, 2, 256};
+  int nv = 1;
+  while (nvec > static_cast<int64_t>(most) * nv && nv < 4) nv *= 2;
+  return {false, nv, static_cast<int>((nvec + 64 * nv - 1) / (64 * nv)) * 64};
+}
+
+template <int kDtype, bool kLayer>
+void dispatch_norm(const Shape& sh, const NormArgs& a, dim3 grid, hipStream_t s) {
+  const dim3 block(sh.threads);
+  if (sh.wave) {
+    if (sh.nv == 1) hipLaunchKernelGGL((norm_kernel<kDtype, kLayer, 1, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((norm_kernel<kDtype, kLayer, 2, true>), grid, block, 0, s, a);
+    return;
+  }
+  switch (sh.nv) {
+    case 1: hipLaunchKernelGGL((norm_kernel<kDtype, kLayer, 1, false>), grid, block, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((norm_kernel<kDtype, kLayer, 2, false>), grid, block, 0, s, a); break;
+    default:
+      if constexpr (kDtype == 0)
+        hipLaunchKernelGGL((norm_kernel<kDtype, kLayer, 4, false>), grid, block, 0, s, a);
+  }
+}
+
+template <int kDtype, bool kLayer>
+void dispatch_grad(const Shape& sh, const NormGradArgs& a, dim3 grid, hipStream_t s) {
+  const dim3 block(sh.threads);
+  if (sh.wave) {
+    if (sh.nv == 1) hipLaunchKernelGGL((norm_grad_kernel<kDtype, kLayer, 1, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((norm_grad_kernel<kDtype, kLayer, 2, true>), grid, block, 0, s, a);
+    return;
+  }
+  switch (sh.nv) {
+    case 1: hipLaunchKernelGGL((norm_grad_kernel<kDtype, kLayer, 1, false>), grid, block, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((norm_grad_kernel<kDtype, kLayer, 2, false>), grid, block, 0, s, a); break;
+    default:
+      if constexpr (kDtype == 0)
+        hipLaunchKernelGGL((norm_grad_kernel<kDtype, kLayer, 4, false>), grid, block, 0, s, a);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_norm(int dtype, bool layer, const NormArgs& a, hipStream_t s) {
+  const Shape sh = row_shape(dtype, a.d, 1024);
+  const int64_t groups = sh.wave ? (a.T + 3) / 4 : a.T, most = int64_t(1) << 21;
+  const dim3 grid(static_cast<unsigned>(groups < most ? groups : most));
+  if (dtype == 1) layer ? dispatch_norm<1, true>(sh, a, grid, s) : dispatch_norm<1, false>(sh, a, grid, s);
+  else layer ? dispatch_norm<0, true>(sh, a, grid, s) : dispatch_norm<0, false>(sh, a, grid, s);
+  return hipGetLastError();
+}
+
+int norm_grad_parts(int dtype, int64_t T, int64_t d) {
+  const Shape sh = row_shape(dtype, d, 1024);
+  const int64_t groups = sh.wave ? (T + 3) / 4 : T, most = 512;
+  return static_cast<int>(groups < most ? groups : most);
+}
+
+hipError_t launch_norm_grad(int dtype, bool layer, const NormGradArgs& a, int parts, float* dw, float* db,
+                            hipStream_t s) {
+  const Shape sh = row_shape(dtype, a.d, 1024);
+  const dim3 grid(parts);
+  if (dtype == 1) layer ? dispatch_grad<1, true>(sh, a, grid, s) : dispatch_grad<1, false>(sh, a, grid, s);
+  else layer ? dispatch_grad<0, true>(sh, a, grid, s) : dispatch_grad<0, false>(sh, a, grid, s);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  if (!dw && !db) return hipSuccess;
+  hipLaunchKernelGGL(norm_parts_kernel, dim3((a.d + 15) / 16, db ? 2 : 1), dim3(256), 0, s, a.part_w, a.part_b, parts,
+                     a.d, dw, db);
+  return hipGetLastError();
+}
+
+}  // namespace moe
