@@ -152,7 +152,7 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a)
       const double up = 1.0 / static_cast<double>(kShrink);
       const double r = 1.0 / sqrt(static_cast<double>(var) * up * up + static_cast<double>(a.eps));
       rstd = static_cast<float>(r);
-      mul = static_cast<float>(fmin(r * up, 0x1.fffffep127));
+      mul = r * up > 0x1.fffffep127 ? 0x1.fffffep127f : static_cast<float>(r * up);  // (NaN stays)
       mean_out = static_cast<float>(static_cast<double>(mean) * up);
     }
     if (tid == 0) {
