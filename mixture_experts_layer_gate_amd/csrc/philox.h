@@ -11,6 +11,11 @@ struct Philox {
   uint32_t x[4];
 };
 
+// One instruction (the compiler makes two).
+__device__ __forceinline__ uint32_t xor_of(uint32_t a, uint32_t b, uint32_t c) {
+  return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
+}
+
 __device__ __forceinline__ Philox philox(uint64_t counter, uint64_t offset, uint64_t seed) {
   uint32_t c0 = static_cast<uint32_t>(counter), c1 = static_cast<uint32_t>(counter >> 32);
   uint32_t c2 = static_cast<uint32_t>(offset), c3 = static_cast<uint32_t>(offset >> 32);
@@ -18,8 +23,8 @@ __device__ __forceinline__ Philox philox(uint64_t counter, uint64_t offset, uint
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
-    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c0 = xor_of(static_cast<uint32_t>(b >> 32), c1, k0);
+    c2 = xor_of(static_cast<uint32_t>(a >> 32), c3, k1);
     c1 = static_cast<uint32_t>(b);
     c3 = static_cast<uint32_t>(a);
     k0 += 0x9E3779B9u;

@@ -50,8 +50,13 @@ hipError_t launch_norm_grad(int dtype, bool layer, const NormGradArgs& a, int pa
 // A launch takes its tensors by value (kernel arguments hold 4 KB), so no list
 // is copied to the device and a captured graph holds its own.
 constexpr int kAdamTensors = 40;
-constexpr int kGradTensors = 120;
-constexpr int kListChunk = 8192;   // elements of one workgroup's turn
+constexpr int kGradTensors = 168;
+constexpr int kStateTensors = 56;
+// Elements of a workgroup's turn: four rounds of its 256 threads, or one where
+// that leaves compute units without a workgroup.
+constexpr int kListChunk = 8192, kListChunkSmall = 2048;
+constexpr int64_t kListSmall = int64_t(1) << 23;     // elements of a list up to which the small chunk is taken
+constexpr int64_t kListStream = int64_t(256) << 20;  // bytes of a list from which it streams past the cache
 constexpr int64_t kListElements = int64_t(1) << 36;  // of one tensor at most
 constexpr int64_t kListChunks = int64_t(1) << 23;    // of one launch at most (fewer than 2^32 threads)
 constexpr int kScaleBlock = 128;   // elements per scale of the 8-bit states
@@ -60,19 +65,18 @@ struct GradEntry {
   const void* g;
   int64_t n;
   uint32_t first;  // chunks of the launch's tensors before this one
-  uint32_t bf16;
+  uint32_t flags;  // 1 bf16, 2 aligned for wide loads
 };
 struct GradTable {
   GradEntry t[kGradTensors];
   int count;
   uint32_t chunks;
+  int chunk;       // elements of one
 };
 // Sums of squares of a table's tensors into parts [grid] (double).
 constexpr int kNormGrid = 2048;    // workgroups (parts) of one launch at most
-hipError_t launch_square_sums(const GradTable& t, int grid, double* parts, hipStream_t s);
+hipError_t launch_square_sums(const GradTable& t, bool stream, int grid, double* parts, hipStream_t s);
 hipError_t launch_grad_norm(const double* parts, int n, double scale, double max_norm, float* out, hipStream_t s);
-// Both in one workgroup, for few elements.
-hipError_t launch_grad_norm_small(const GradTable& t, double scale, double max_norm, float* out, hipStream_t s);
 
 struct AdamEntry {
   void* p;
@@ -101,6 +105,7 @@ struct AdamTable {
   AdamEntry t[kAdamTensors];
   int count;
   uint32_t chunks;
+  int chunk;
   int stochastic;           // bf16 parameters without master weights rounded stochastically
   const double* lr_step;    // device {lr, step} or null
   const float* gscale;      // device [1] or null
@@ -128,7 +133,7 @@ __host__ __device__ inline void adam_scalars(AdamScalars& k, double lr, double s
   k.inv_root = static_cast<float>(1.0 / __builtin_sqrt(1.0 - pow_step(k.beta2, step)));
   k.decay = static_cast<float>(lr * k.weight_decay);
 }
-hipError_t launch_adam(int bits, const AdamTable& t, hipStream_t s);
+hipError_t launch_adam(int bits, const AdamTable& t, bool stream, hipStream_t s);
 
 // What 8-bit states stand for.
 struct StateEntry {
@@ -143,12 +148,12 @@ struct StateEntry {
   uint32_t aligned;
 };
 struct StateTable {
-  StateEntry t[56];
+  StateEntry t[kStateTensors];
   int count;
   uint32_t chunks;
+  int chunk;
 };
 static_assert(sizeof(StateTable) <= 4096, "kernel arguments");
-constexpr int kStateTensors = 56;
-hipError_t launch_state_values(int out_dtype, const StateTable& t, hipStream_t s);
+hipError_t launch_state_values(int out_dtype, const StateTable& t, bool stream, hipStream_t s);
 
 }  // namespace moe

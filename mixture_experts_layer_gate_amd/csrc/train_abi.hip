@@ -20,7 +20,18 @@ constexpr int32_t kMostTensors = 1 << 20;
 bool ok_dtype(int64_t t) { return t == MOE_DTYPE_F32 || t == MOE_DTYPE_BF16; }
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool ok_elements(const void* p, int64_t dtype) { return p && aligned(p, dtype == MOE_DTYPE_F32 ? 4 : 2); }
-int64_t chunks_of(int64_t n) { return (n + kListChunk - 1) / kListChunk; }
+// How a list is cut, from its elements and the bytes that a call moves.
+struct Cut {
+  int chunk;
+  bool stream;
+};
+template <typename Item>
+Cut cut_of(const Item* t, int32_t count, int64_t bytes_each) {
+  int64_t n = 0;
+  for (int32_t i = 0; i < count; ++i) n += t[i].n;  // (2^56 at most)
+  return {n <= kListSmall ? kListChunkSmall : kListChunk, n >= kListStream / bytes_each};
+}
+int64_t chunks_of(int64_t n, int chunk) { return (n + chunk - 1) / chunk; }
 
 int check_norm(const moe_dims_t* dm, const moe_norm_opts_t* op) {
   if (int st = check_dims(dm)) return st;
@@ -65,10 +76,11 @@ int check_grads(const moe_grad_t* g, int32_t count) {
 int square_grid(int64_t chunks) { return static_cast<int>(chunks < kNormGrid ? chunks : kNormGrid); }
 
 template <typename Fn>
-int each_grad_table(const moe_grad_t* g, int32_t count, Fn&& fn) {
+int each_grad_table(const moe_grad_t* g, int32_t count, const Cut& cut, Fn&& fn) {
   GradTable t;
   t.count = 0;
   t.chunks = 0;
+  t.chunk = cut.chunk;
   for (int32_t i = 0; i <= count; ++i) {
     if (i == count || t.count == kGradTensors) {
       if (t.count > 0)
@@ -79,15 +91,17 @@ int each_grad_table(const moe_grad_t* g, int32_t count, Fn&& fn) {
     }
     if (g[i].n == 0) continue;
     const bool bf16 = g[i].dtype == MOE_DTYPE_BF16;
-    t.t[t.count++] = {g[i].grad, g[i].n, t.chunks, (bf16 ? 1u : 0u) | (aligned(g[i].grad, 16) ? 0u : 2u)};
-    t.chunks += static_cast<uint32_t>(chunks_of(g[i].n));
+    t.t[t.count++] = {g[i].grad, g[i].n, t.chunks, (bf16 ? 1u : 0u) | (aligned(g[i].grad, 16) ? 2u : 0u)};
+    t.chunks += static_cast<uint32_t>(chunks_of(g[i].n, cut.chunk));
   }
   return MOE_OK;
 }
 
+Cut grad_cut(const moe_grad_t* g, int32_t count) { return cut_of(g, count, 4); }
+
 int64_t grad_parts(const moe_grad_t* g, int32_t count) {
   int64_t parts = 0;
-  each_grad_table(g, count, [&](const GradTable& t) {
+  each_grad_table(g, count, grad_cut(g, count), [&](const GradTable& t) {
     parts += square_grid(t.chunks);
     return 0;
   });
@@ -213,9 +227,10 @@ int moe_grad_norm(const moe_grad_t* grads, int32_t count, double grad_scale, dou
   StageScope sc(MOE_STAGE_GRAD_NORM, s);
   double* parts = static_cast<double*>(ws);
   int64_t done = 0;
-  if (int st = each_grad_table(grads, count, [&](const GradTable& t) {
+  const Cut cut = grad_cut(grads, count);
+  if (int st = each_grad_table(grads, count, cut, [&](const GradTable& t) {
         const int grid = square_grid(t.chunks);
-        const int e = hip_status(launch_square_sums(t, grid, parts + done, s));
+        const int e = hip_status(launch_square_sums(t, cut.stream, grid, parts + done, s));
         done += grid;
         return e;
       }))
@@ -264,13 +279,15 @@ int moe_adam_step(const moe_adam_opts_t* op, const moe_adam_tensor_t* tensors, c
   k.eps = static_cast<float>(op->eps);
   if (!lr_step) adam_scalars(k, op->lr, static_cast<double>(op->step));
   const uintptr_t code_align = op->state_bits == 8 ? 8 : 16;
+  const Cut cut = cut_of(tensors, count, op->state_bits == 8 ? 10 : 22);
+  t.chunk = cut.chunk;
   int64_t base = 0;
   for (int32_t i = 0; i < count; ++i) {
     const moe_adam_tensor_t& a = tensors[i];
     if (a.n > 0) {
-      const int64_t c = chunks_of(a.n);
+      const int64_t c = chunks_of(a.n, cut.chunk);
       if (t.count == kAdamTensors || (t.count > 0 && t.chunks + c > kListChunks)) {
-        if (int st = hip_status(launch_adam(op->state_bits, t, s))) return st;
+        if (int st = hip_status(launch_adam(op->state_bits, t, cut.stream, s))) return st;
         t.count = 0;
         t.chunks = 0;
       }
@@ -285,7 +302,7 @@ int moe_adam_step(const moe_adam_opts_t* op, const moe_adam_tensor_t* tensors, c
     }
     base += (a.n + kScaleBlock - 1) / kScaleBlock * kScaleBlock;
   }
-  return t.count ? hip_status(launch_adam(op->state_bits, t, s)) : MOE_OK;
+  return t.count ? hip_status(launch_adam(op->state_bits, t, cut.stream, s)) : MOE_OK;
 }
 
 int moe_adam_state_values(const moe_adam_tensor_t* tensors, int32_t count, void* const* m_out, void* const* r_out,
@@ -297,15 +314,17 @@ int moe_adam_state_values(const moe_adam_tensor_t* tensors, int32_t count, void*
     if (tensors[i].n && (!ok_elements(m_out[i], out_dtype) || !ok_elements(r_out[i], out_dtype))) return MOE_ERR_INVALID;
   hipStream_t s = static_cast<hipStream_t>(stream);
   StageScope sc(MOE_STAGE_ADAM, s);
+  const Cut cut = cut_of(tensors, count, 6);
   StateTable t;
   t.count = 0;
   t.chunks = 0;
+  t.chunk = cut.chunk;
   for (int32_t i = 0; i < count; ++i) {
     const moe_adam_tensor_t& a = tensors[i];
     if (a.n == 0) continue;
-    const int64_t c = chunks_of(a.n);
+    const int64_t c = chunks_of(a.n, cut.chunk);
     if (t.count == kStateTensors || (t.count > 0 && t.chunks + c > kListChunks)) {
-      if (int st = hip_status(launch_state_values(out_dtype, t, s))) return st;
+      if (int st = hip_status(launch_state_values(out_dtype, t, cut.stream, s))) return st;
       t.count = 0;
       t.chunks = 0;
     }
@@ -314,7 +333,7 @@ int moe_adam_state_values(const moe_adam_tensor_t* tensors, int32_t count, void*
                       m_out[i], r_out[i], a.n, t.chunks, al ? 1u : 0u};
     t.chunks += static_cast<uint32_t>(c);
   }
-  return t.count ? hip_status(launch_state_values(out_dtype, t, s)) : MOE_OK;
+  return t.count ? hip_status(launch_state_values(out_dtype, t, cut.stream, s)) : MOE_OK;
 }
 
 }  // extern "C"
