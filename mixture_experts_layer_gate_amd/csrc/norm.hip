@@ -53,25 +53,32 @@ __device__ __forceinline__ void load_w(const void* p, int w_bf16, int i, float (
   }
 }
 
+// Sum over a wave in every lane: rows of 16 by rotations inside them, then the
+// four rows' sums.
+template <int kRor>
+__device__ __forceinline__ float ror_add(float v) {
+  return v + __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), 0x120 + kRor, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float lane_of(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  v = ror_add<1>(ror_add<2>(ror_add<4>(ror_add<8>(v))));
+  return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
 }
 
+__device__ __forceinline__ float sum4(const float4& v) { return (v.x + v.y) + (v.z + v.w); }
+
 // Sum over the workgroup (kWaveRow: over the wave), the same value in every
-// thread. red: one float per wave; alternating halves need no second barrier.
+// thread. red: one float to a wave, 16 of them, those without a wave 0.
 template <bool kWaveRow>
 __device__ __forceinline__ float row_sum(float v, float* red) {
   v = wave_sum(v);
   if constexpr (kWaveRow) return v;
-  const int nw = blockDim.x >> 6;
-  if (nw == 1) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  v = 0.0f;
-  for (int i = 0; i < nw; ++i) v += red[i];
-  return v;
+  const float4* q = reinterpret_cast<const float4*>(red);
+  return (sum4(q[0]) + sum4(q[1])) + (sum4(q[2]) + sum4(q[3]));
 }
 
 constexpr float kShrink = 0x1p-80f;
@@ -83,7 +90,9 @@ constexpr float kShrink = 0x1p-80f;
 template <int kDtype, bool kLayer, int NV, bool kWaveRow>
 __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a) {
   constexpr int V = kVec<kDtype>;
-  __shared__ float red[2][16];
+  __shared__ __attribute__((aligned(16))) float red[2][16];
+  if (!kWaveRow && threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = 0.0f;
+  if (!kWaveRow) __syncthreads();
   const int nvec = a.d / V;
   const int lanes = kWaveRow ? 64 : blockDim.x;
   const int tid = kWaveRow ? (threadIdx.x & 63) : threadIdx.x;
@@ -114,6 +123,14 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a)
         unpack<kDtype>(o, v[j]);
         if (a.sum && c < nvec) reinterpret_cast<uint4*>(a.sum)[t * nvec + c] = o;
       }
+    }
+    // (ahead of the sums, which they then do not wait behind)
+    float w[NV][V], b[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = tid + j * lanes;
+      if (a.w && c < nvec) load_w<V>(a.w, a.w_bf16, c, w[j]);
+      if (kLayer && a.b && c < nvec) load_w<V>(a.b, a.w_bf16, c, b[j]);
     }
     float mean = 0.0f, var = 0.0f;
     bool small = false;  // scaled by kShrink
@@ -163,14 +180,11 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a)
     for (int j = 0; j < NV; ++j) {
       const int c = tid + j * lanes;
       if (c >= nvec) continue;
-      float w[V], b[V];
-      if (a.w) load_w<V>(a.w, a.w_bf16, c, w);
-      if (a.b) load_w<V>(a.b, a.w_bf16, c, b);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         float y = (kLayer ? v[j][i] - mean : v[j][i]) * mul;
-        if (a.w) y *= w[i];
-        if (a.b) y += b[i];
+        if (a.w) y *= w[j][i];
+        if (kLayer && a.b) y += b[j][i];
         v[j][i] = y;
       }
       reinterpret_cast<uint4*>(a.y)[t * nvec + c] = pack<kDtype>(v[j]);
@@ -190,7 +204,11 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a)
 template <int kDtype, bool kLayer, int NV, bool kWaveRow>
 __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGradArgs a) {
   constexpr int V = kVec<kDtype>;
-  __shared__ float2 red[2][16];
+  __shared__ __attribute__((aligned(16))) float red[2][2][16];
+  if (!kWaveRow) {
+    if (threadIdx.x < 64) red[threadIdx.x >> 5][(threadIdx.x >> 4) & 1][threadIdx.x & 15] = 0.0f;
+    __syncthreads();
+  }
   const int nvec = a.d / V;
   const int lanes = kWaveRow ? 64 : blockDim.x;
   const int tid = kWaveRow ? (threadIdx.x & 63) : threadIdx.x;
@@ -198,16 +216,22 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
   const int per = kWaveRow ? nw : 1;
   const float inv_d = 1.0f / static_cast<float>(a.d);
   const int64_t step = static_cast<int64_t>(gridDim.x) * per;
-  float aw[NV][V], ab[NV][V], w[NV][V];
+  // 16 columns to a thread of a full workgroup leave no registers for the next row
+  // and the weights, which are read again for every row then
+  constexpr bool kWide = !kWaveRow && NV * V > 8;
+  float aw[NV][V], ab[NV][V], w[kWide ? 1 : NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) aw[j][i] = ab[j][i] = 0.0f, w[j][i] = 1.0f;
-    if (a.w && tid + j * lanes < nvec) load_w<V>(a.w, a.w_bf16, tid + j * lanes, w[j]);
+    for (int i = 0; i < V; ++i) {
+      aw[j][i] = ab[j][i] = 0.0f;
+      if (!kWide) w[j][i] = 1.0f;
+    }
+    if (!kWide && a.w && tid + j * lanes < nvec) load_w<V>(a.w, a.w_bf16, tid + j * lanes, w[j]);
   }
-  int half = 0;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * per + (kWaveRow ? (threadIdx.x >> 6) : 0); t < a.T; t += step) {
-    uint4 ud[NV], ux[NV], ui[NV];
+  uint4 ud[NV], ux[NV], ui[NV];
+  float rstd = 0.0f, mean = 0.0f;
+  const auto fetch = [&](int64_t t) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = tid + j * lanes;
@@ -217,20 +241,39 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
       ux[j] = in ? reinterpret_cast<const uint4*>(a.x)[at] : make_uint4(0, 0, 0, 0);
       if (a.dx_in) ui[j] = in ? reinterpret_cast<const uint4*>(a.dx_in)[at] : make_uint4(0, 0, 0, 0);
     }
-    const float rstd = a.rstd[t], r2 = 2.0f * rstd, m2 = kLayer ? -0.5f * a.mean[t] : 0.0f;
+    rstd = a.rstd[t];
+    if constexpr (kLayer) mean = a.mean[t];
+  };
+  int64_t t = static_cast<int64_t>(blockIdx.x) * per + (kWaveRow ? (threadIdx.x >> 6) : 0);
+  if (!kWide && t < a.T) fetch(t);
+  for (int half = 0; t < a.T; t += step, half ^= 1) {
+    if (kWide) fetch(t);
+    const float rs = rstd, r2 = 2.0f * rstd, m2 = kLayer ? -0.5f * mean : 0.0f;
     float h[NV][V], g[NV][V];
-    float sg = 0.0f, sh = 0.0f;
+    uint4 add[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       unpack<kDtype>(ux[j], h[j]);
       unpack<kDtype>(ud[j], g[j]);
+      add[j] = ui[j];
+    }
+    // the next row is on its way while this one's sums are exchanged
+    if (!kWide && t + step < a.T) fetch(t + step);
+    float sg = 0.0f, sh = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
       const bool in = tid + j * lanes < nvec;
+      if constexpr (kWide) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[0][i] = 1.0f;
+        if (a.w && in) load_w<V>(a.w, a.w_bf16, tid + j * lanes, w[0]);
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         h[j][i] = in ? fmaf(h[j][i], 0.5f, m2) * r2 : 0.0f;
         aw[j][i] = fmaf(g[j][i], h[j][i], aw[j][i]);
         if constexpr (kLayer) ab[j][i] += g[j][i];
-        g[j][i] *= w[j][i];
+        g[j][i] *= w[kWide ? 0 : j][i];
         if constexpr (kLayer) sg += g[j][i];
         sh = fmaf(g[j][i], h[j][i], sh);
       }
@@ -238,17 +281,15 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
     if constexpr (kLayer) sg = wave_sum(sg);
     sh = wave_sum(sh);
     if constexpr (!kWaveRow) {
-      if (nw > 1) {
-        if ((threadIdx.x & 63) == 0) red[half][threadIdx.x >> 6] = make_float2(sg, sh);
-        __syncthreads();
-        sg = sh = 0.0f;
-        for (int i = 0; i < nw; ++i) {
-          const float2 p = red[half][i];
-          sg += p.x;
-          sh += p.y;
-        }
-        half ^= 1;
+      // (the other half is read until every wave is past this barrier)
+      if ((threadIdx.x & 63) == 0) {
+        red[half][0][threadIdx.x >> 6] = sh;
+        if (kLayer) red[half][1][threadIdx.x >> 6] = sg;
       }
+      __syncthreads();
+      const float4* q = reinterpret_cast<const float4*>(red[half][0]);
+      sh = (sum4(q[0]) + sum4(q[1])) + (sum4(q[2]) + sum4(q[3]));
+      if constexpr (kLayer) sg = (sum4(q[4]) + sum4(q[5])) + (sum4(q[6]) + sum4(q[7]));
     }
     sg *= inv_d;
     sh *= inv_d;
@@ -257,12 +298,12 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
       const int c = tid + j * lanes;
       if (c >= nvec) continue;
       float o[V];
-      if (a.dx_in) unpack<kDtype>(ui[j], o);
+      if (a.dx_in) unpack<kDtype>(add[j], o);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         float e = fmaf(-h[j][i], sh, g[j][i]);
         if constexpr (kLayer) e -= sg;
-        o[i] = a.dx_in ? fmaf(e, rstd, o[i]) : e * rstd;
+        o[i] = a.dx_in ? fmaf(e, rs, o[i]) : e * rs;
       }
       reinterpret_cast<uint4*>(a.dx)[t * nvec + c] = pack<kDtype>(o);
     }
@@ -412,7 +453,8 @@ hipError_t launch_norm(int dtype, bool layer, const NormArgs& a, hipStream_t s) 
 
 int norm_grad_parts(int dtype, int64_t T, int64_t d) {
   const Shape sh = row_shape(dtype, d, 1024);
-  const int64_t groups = sh.wave ? (T + 3) / 4 : T, most = 512;
+  // workgroups that are resident at once: a part is written and read once more
+  const int64_t groups = sh.wave ? (T + 3) / 4 : T, most = 256 * (1024 / sh.threads > 0 ? 1024 / sh.threads : 1);
   return static_cast<int>(groups < most ? groups : most);
 }
 
