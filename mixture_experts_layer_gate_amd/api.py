@@ -1047,15 +1047,19 @@ class GradList:
     memory must not be replaced under it (Tensor.data = .., set_, resize_)."""
 
     def __init__(self, grads):
-        self.tensors = [t.detach() for t in grads]
-        self.device = _list_device(self.tensors, "grads")
-        kinds = tuple(MOE_DTYPE)
-        rows = array.array("q")
-        for i, t in enumerate(self.tensors):
-            p = _flat(t, f"grads[{i}]", kinds, None, self.device)
-            rows.extend((p, t.numel(), MOE_DTYPE[t.dtype]))
-        self._rows = rows
-        self._ptr = rows.buffer_info()[0]
+        self._take([t.detach() for t in grads])
+
+    def _take(self, tensors):
+        self.tensors = tensors
+        self.device = dev = _list_device(tensors, "grads")
+        rows = []
+        for i, t in enumerate(tensors):
+            kind = MOE_DTYPE.get(t.dtype)
+            if kind is None or t.device != dev or not t.is_contiguous():
+                _flat(t, f"grads[{i}]", tuple(MOE_DTYPE), None, dev)
+            rows += (t.data_ptr(), t.numel(), kind)
+        self._rows = array.array("q", rows)
+        self._ptr = self._rows.buffer_info()[0]
         self._ws = None
 
     def __len__(self):
@@ -1155,7 +1159,12 @@ def adam_state(params, bits: int = 32, master: bool = False) -> AdamState:
 
 
 def _grad_list(grads) -> GradList:
-    return grads if isinstance(grads, GradList) else GradList(grads)
+    """grads, or a list of tensors checked for the length of a call."""
+    if isinstance(grads, GradList):
+        return grads
+    g = GradList.__new__(GradList)
+    g._take(grads)
+    return g
 
 
 def grad_norm_workspace_bytes(grads) -> int:
