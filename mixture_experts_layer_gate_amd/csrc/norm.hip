@@ -116,18 +116,29 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a)
   const int tid = kWaveRow ? (threadIdx.x & 63) : threadIdx.x;
   const int per = kWaveRow ? (blockDim.x >> 6) : 1;
   const float inv_d = 1.0f / static_cast<float>(a.d);
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * per + (kWaveRow ? (threadIdx.x >> 6) : 0); t < a.T;
-       t += static_cast<int64_t>(gridDim.x) * per) {
-    float v[NV][V];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per;
+  uint4 ux[NV], ur[NV];
+  const auto fetch = [&](int64_t t) {
     const uint4* px = reinterpret_cast<const uint4*>(a.x) + t * nvec;
     const uint4* pr = reinterpret_cast<const uint4*>(a.residual) + t * nvec;
-    uint4 ux[NV], ur[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = tid + j * lanes;
       ux[j] = c < nvec ? get<kStream>(px + c) : make_uint4(0, 0, 0, 0);
       if (a.residual) ur[j] = c < nvec ? get<kStream>(pr + c) : make_uint4(0, 0, 0, 0);
     }
+  };
+  int64_t t = static_cast<int64_t>(blockIdx.x) * per + (kWaveRow ? (threadIdx.x >> 6) : 0);
+  if (t < a.T) fetch(t);
+  float w[NV][V], b[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = tid + j * lanes;
+    if (a.w && c < nvec) load_w<V>(a.w, a.w_bf16, c, w[j]);
+    if (kLayer && a.b && c < nvec) load_w<V>(a.b, a.w_bf16, c, b[j]);
+  }
+  for (; t < a.T; t += step) {
+    float v[NV][V];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = tid + j * lanes;
@@ -142,14 +153,8 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a)
         if (a.sum && c < nvec) put<kStream>(reinterpret_cast<uint4*>(a.sum) + t * nvec + c, o);
       }
     }
-    // (ahead of the sums, which they then do not wait behind)
-    float w[NV][V], b[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = tid + j * lanes;
-      if (a.w && c < nvec) load_w<V>(a.w, a.w_bf16, c, w[j]);
-      if (kLayer && a.b && c < nvec) load_w<V>(a.b, a.w_bf16, c, b[j]);
-    }
+    // the next row is on its way while this one's sums are exchanged
+    if (t + step < a.T) fetch(t + step);
     float mean = 0.0f, var = 0.0f;
     bool small = false;  // scaled by kShrink
     for (;;) {
@@ -468,13 +473,14 @@ struct NormGradLaunch {
   }
 };
 
+constexpr int64_t kResident = 2048;
 constexpr int64_t kStreamBytes = int64_t(256) << 20;
 
 }  // namespace
 
 hipError_t launch_norm(int dtype, bool layer, const NormArgs& a, hipStream_t s) {
   const Shape sh = row_shape(dtype, a.d, 1024);
-  const int64_t groups = sh.wave ? (a.T + 3) / 4 : a.T, most = int64_t(1) << 21;
+  const int64_t groups = sh.wave ? (a.T + 3) / 4 : a.T, most = 256 * (kResident / sh.threads);
   const dim3 grid(static_cast<unsigned>(groups < most ? groups : most));
   const int64_t bytes = a.T * a.d * (dtype == 1 ? 2 : 4) * (a.residual ? a.sum ? 4 : 3 : 2);
   by_type(dtype, layer, bytes >= kStreamBytes, sh, NormLaunch{a, grid, dim3(sh.threads), s});
