@@ -384,33 +384,42 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
 }
 
 // Column sums of the parts: 16 columns to a workgroup (64 bytes of a part's row),
-// 64 threads to each four of them, joined through LDS in a fixed order.
-__global__ __launch_bounds__(256) void norm_parts_kernel(const float* __restrict__ part_w,
-                                                         const float* __restrict__ part_b, int parts, int d,
-                                                         float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float4 join[64][4];
+// four to a thread; its threads' sums are joined inside the waves, then between
+// them, in a fixed order. 256 threads up to 256 parts, 1024 above (measured at
+// 512 parts of 512 columns: 12.4 and 11.3 us with the rows' pass of 8192; at 256
+// parts of 7168 columns 42.4 and 42.9 with that of 4096).
+__global__ __launch_bounds__(1024) void norm_parts_kernel(const float* __restrict__ part_w,
+                                                          const float* __restrict__ part_b, int parts, int d,
+                                                          float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float4 join[16][4];
   const float* part = blockIdx.y == 0 ? part_w : part_b;
   float* out = blockIdx.y == 0 ? dw : db;
   if (!out) return;
-  const int q = threadIdx.x & 3, g = threadIdx.x >> 2;
+  const int q = threadIdx.x & 3, groups = blockDim.x >> 2;
   const int c = blockIdx.x * 16 + q * 4;
   float4 s = make_float4(0, 0, 0, 0);
   if (c < d) {
-    for (int p = g; p < parts; p += 64) {
+    for (int p = threadIdx.x >> 2; p < parts; p += groups) {
       const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(p) * d + c);
       s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
     }
   }
-  join[g][q] = s;
-  for (int n = 32; n > 0; n >>= 1) {
-    __syncthreads();
-    if (g < n) {
-      const float4 v = join[g + n][q];
-      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-      join[g][q] = s;
-    }
+#pragma unroll
+  for (int o = 4; o < 64; o <<= 1) {
+    s.x += __shfl_xor(s.x, o);
+    s.y += __shfl_xor(s.y, o);
+    s.z += __shfl_xor(s.z, o);
+    s.w += __shfl_xor(s.w, o);
   }
-  if (g == 0 && c < d) *reinterpret_cast<float4*>(out + c) = s;
+  if ((threadIdx.x & 63) < 4) join[threadIdx.x >> 6][q] = s;
+  __syncthreads();
+  if (threadIdx.x < 4 && c < d) {
+    for (unsigned i = 1; i < blockDim.x >> 6; ++i) {
+      const float4 v = join[i][q];
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    *reinterpret_cast<float4*>(out + c) = s;
+  }
 }
 
 struct Shape {
@@ -473,7 +482,7 @@ struct NormGradLaunch {
   }
 };
 
-constexpr int64_t kResident = 2048;
+constexpr int64_t kResident = 2048;  // threads that a compute unit holds
 constexpr int64_t kStreamBytes = int64_t(256) << 20;
 
 }  // namespace
@@ -489,8 +498,10 @@ hipError_t launch_norm(int dtype, bool layer, const NormArgs& a, hipStream_t s) 
 
 int norm_grad_parts(int dtype, int64_t T, int64_t d) {
   const Shape sh = row_shape(dtype, d, 1024);
-  // workgroups that are resident at once: a part is written and read once more
-  const int64_t groups = sh.wave ? (T + 3) / 4 : T, most = 256 * (1024 / sh.threads > 0 ? 1024 / sh.threads : 1);
+  // One workgroup to a compute unit, two of few threads: every part is written and
+  // read once more. Measured with one, two, three: 4096 x 7168 42, 48, 52 us; 8192
+  // x 4096 48, 51, 57; 16384 x 2048 66, 50, 53; 8192 x 512 12.6, 12.4, 14.0.
+  const int64_t groups = sh.wave ? (T + 3) / 4 : T, most = sh.threads < 512 ? 512 : 256;
   return static_cast<int>(groups < most ? groups : most);
 }
 
@@ -502,7 +513,7 @@ hipError_t launch_norm_grad(int dtype, bool layer, const NormGradArgs& a, int pa
   by_type(dtype, layer, bytes >= kStreamBytes, sh, NormGradLaunch{a, grid, dim3(sh.threads), s});
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (!dw && !db) return hipSuccess;
-  hipLaunchKernelGGL(norm_parts_kernel, dim3((a.d + 15) / 16, db ? 2 : 1), dim3(256), 0, s, a.part_w, a.part_b, parts,
+  hipLaunchKernelGGL(norm_parts_kernel, dim3((a.d + 15) / 16, db ? 2 : 1), dim3(parts > 256 ? 1024 : 256), 0, s, a.part_w, a.part_b, parts,
                      a.d, dw, db);
   return hipGetLastError();
 }
