@@ -53,11 +53,14 @@ __device__ __forceinline__ void load_w(const void* p, int w_bf16, int i, float (
   }
 }
 
-// kStream: a batch larger than the 256 MB cache passes through once, and no cache
+// kStream: a batch of over half the 256 MB cache passes through once, and no cache
 // line is kept for what it reads, nor for the sum, which the backward reads much
-// later; y and dx stay in it for the layer behind. Measured, ordinary and streaming: norm
-// of 16384 x 6144 with residual 143 and 126 us (131 with y streaming too); but
-// gradients of 2047 x 6144 with bias, which the cache holds, 22 and 24 us.
+// later; y and dx stay in it for what runs next. Measured, ordinary loads and
+// stores, these, and y and dx streaming too: norm of 16384 x 6144 with residual
+// alone 153, 152 and 145 us, but with a gate of 8 experts behind it 218, 204 and
+// 214; gradients of 8192 x 6144 with the next layer's dropout 109, 100 and 109;
+// norm of 4096 x 7168 alone 45, 40 and 41, with the gate 84, 75 and 85. Gradients
+// of 2047 x 6144 with bias, which the cache holds: 22 us, and 24 with streaming.
 template <bool kStream>
 __device__ __forceinline__ uint4 get(const uint4* p) {
   const u32x4_t* q = reinterpret_cast<const u32x4_t*>(p);
@@ -483,7 +486,7 @@ struct NormGradLaunch {
 };
 
 constexpr int64_t kResident = 2048;  // threads that a compute unit holds
-constexpr int64_t kStreamBytes = int64_t(256) << 20;
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
 
 }  // namespace
 

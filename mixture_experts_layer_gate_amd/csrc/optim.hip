@@ -22,11 +22,12 @@ __device__ __forceinline__ int find_tensor(const Table& t, uint32_t c) {
   return __builtin_amdgcn_readfirstlane(at - 1);
 }
 
-// kStream: lists larger than the 256 MB cache pass through once, and no cache
-// line is kept for them. Measured, ordinary and streaming loads and stores: 2-norm of 302 M fp32
-// gradients 198 and 179 us, update of 302 M bf16 weights with fp32 masters and
-// states 1746 and 1672 us; but of 1.1 M fp32 weights, which the cache holds, 11.1
-// and 13.4 us.
+// kStream: lists of over half the 256 MB cache pass through once, and no cache line
+// is kept for them. Measured, ordinary and streaming loads and stores (three lists
+// in turn): update of fp32 weights with fp32 states, 4 M (117 MB) 20.5 and 22.0 us,
+// 8 M (235 MB) 48 and 42, 64 M 360 and 336; of bf16 weights with 8-bit states, 12 M
+// (126 MB) 29 and 31, 16 M 42 and 42, 64 M 145 and 139; 2-norm of fp32 gradients,
+// 16 M (67 MB) 16.1 and 16.1, 32 M (134 MB) 28.8 and 26.0, 302 M 198 and 179.
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 template <bool kStream>
 __device__ __forceinline__ uint4 load16(const void* p) {

@@ -56,7 +56,7 @@ constexpr int kStateTensors = 56;
 // that leaves compute units without a workgroup.
 constexpr int kListChunk = 8192, kListChunkSmall = 2048;
 constexpr int64_t kListSmall = int64_t(1) << 23;     // elements of a list up to which the small chunk is taken
-constexpr int64_t kListStream = int64_t(256) << 20;  // bytes of a list from which it streams past the cache
+constexpr int64_t kListStream = int64_t(128) << 20;  // bytes of a list from which it streams past the cache
 constexpr int64_t kListElements = int64_t(1) << 36;  // of one tensor at most
 constexpr int64_t kListChunks = int64_t(1) << 23;    // of one launch at most (fewer than 2^32 threads)
 constexpr int kScaleBlock = 128;   // elements per scale of the 8-bit states

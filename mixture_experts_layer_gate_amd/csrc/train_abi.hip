@@ -20,16 +20,22 @@ constexpr int32_t kMostTensors = 1 << 20;
 bool ok_dtype(int64_t t) { return t == MOE_DTYPE_F32 || t == MOE_DTYPE_BF16; }
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool ok_elements(const void* p, int64_t dtype) { return p && aligned(p, dtype == MOE_DTYPE_F32 ? 4 : 2); }
-// How a list is cut, from its elements and the bytes that a call moves.
+int64_t size_of(int64_t dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+
+// How a list is cut, from its elements and the bytes that a call moves
+// (each(t): those of an element).
 struct Cut {
   int chunk;
   bool stream;
 };
-template <typename Item>
-Cut cut_of(const Item* t, int32_t count, int64_t bytes_each) {
-  int64_t n = 0;
-  for (int32_t i = 0; i < count; ++i) n += t[i].n;  // (2^56 at most)
-  return {n <= kListSmall ? kListChunkSmall : kListChunk, n >= kListStream / bytes_each};
+template <typename Item, typename Fn>
+Cut cut_of(const Item* t, int32_t count, Fn&& each) {
+  double n = 0, bytes = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    n += static_cast<double>(t[i].n);
+    bytes += static_cast<double>(t[i].n) * static_cast<double>(each(i));
+  }
+  return {n <= kListSmall ? kListChunkSmall : kListChunk, bytes >= kListStream};
 }
 int64_t chunks_of(int64_t n, int chunk) { return (n + chunk - 1) / chunk; }
 
@@ -97,7 +103,9 @@ int each_grad_table(const moe_grad_t* g, int32_t count, const Cut& cut, Fn&& fn)
   return MOE_OK;
 }
 
-Cut grad_cut(const moe_grad_t* g, int32_t count) { return cut_of(g, count, 4); }
+Cut grad_cut(const moe_grad_t* g, int32_t count) {
+  return cut_of(g, count, [&](int32_t i) { return size_of(g[i].dtype); });
+}
 
 int64_t grad_parts(const moe_grad_t* g, int32_t count) {
   int64_t parts = 0;
@@ -279,7 +287,10 @@ int moe_adam_step(const moe_adam_opts_t* op, const moe_adam_tensor_t* tensors, c
   k.eps = static_cast<float>(op->eps);
   if (!lr_step) adam_scalars(k, op->lr, static_cast<double>(op->step));
   const uintptr_t code_align = op->state_bits == 8 ? 8 : 16;
-  const Cut cut = cut_of(tensors, count, op->state_bits == 8 ? 10 : 22);
+  const Cut cut = cut_of(tensors, count, [&](int32_t i) {
+    return 2 * size_of(tensors[i].dtype) + size_of(grads[i].dtype) + (op->state_bits == 8 ? 4 : 16) +
+           (tensors[i].master ? 8 : 0);
+  });
   t.chunk = cut.chunk;
   int64_t base = 0;
   for (int32_t i = 0; i < count; ++i) {
@@ -314,7 +325,7 @@ int moe_adam_state_values(const moe_adam_tensor_t* tensors, int32_t count, void*
     if (tensors[i].n && (!ok_elements(m_out[i], out_dtype) || !ok_elements(r_out[i], out_dtype))) return MOE_ERR_INVALID;
   hipStream_t s = static_cast<hipStream_t>(stream);
   StageScope sc(MOE_STAGE_ADAM, s);
-  const Cut cut = cut_of(tensors, count, 6);
+  const Cut cut = cut_of(tensors, count, [&](int32_t) { return 2 + 2 * size_of(out_dtype); });
   StateTable t;
   t.count = 0;
   t.chunks = 0;
