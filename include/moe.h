@@ -611,7 +611,8 @@ typedef struct {
 
 /* out[0] = N = |grad_scale| (sum over all elements g^2)^(1/2), and the factor
  * that unscales and clips: out[1] = grad_scale min(1, max_norm / (N + 1e-6)), or
- * NaN where N is not finite. Squares are summed in double in a fixed order.
+ * NaN where N (formed in double) is not finite. Squares are summed in double in a
+ * fixed order.
  * out [2] fp32 (DEVICE). grad_scale finite, max_norm >= 0 (infinity: no clipping),
  * else MOE_ERR_INVALID. ws: at least moe_grad_norm_workspace_bytes (0 for an
  * invalid list), 256-byte aligned. An empty list gives N = 0. */
@@ -634,10 +635,11 @@ int moe_grad_norm(const moe_grad_t* grads, int32_t count, double grad_scale, dou
  * second moment, a 2^(E - 15) with bits c << 19: four exponent bits, three (m, with
  * a sign) or four fraction bits, gradual underflow. E = 255: NaN. All zero bytes
  * are the state before the first step. m' and sqrt(v') are formed in fp32 and then
- * rounded at random: E is the least exponent whose top code holds the 128 largest
- * (255 where one is not finite), and a value is rounded away from zero where the
- * part of a code step that it drops and u / 2^16 reach 1, u the element's 16-bit
- * number; a root above 0 stays above 0.
+ * rounded at random: E is the least exponent whose top code holds the largest of the
+ * 128 (255 where one is not finite; their codes are 0 then), and a value is rounded
+ * away from zero where the part of a code step that it drops (to 2^-20 of a step)
+ * and u / 2^16 reach 1, u the element's 16-bit number; a root above 0 takes code 1
+ * at least.
  *
  * Numbers: elements are counted through the list, each tensor beginning at a
  * multiple of 128; element i takes number i % 8 (low half of word 0, its high half,

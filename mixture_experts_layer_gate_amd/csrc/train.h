@@ -118,7 +118,7 @@ static_assert(sizeof(AdamTable) <= 4096 && sizeof(GradTable) <= 4096, "kernel ar
 __host__ __device__ inline double pow_step(double b, double step) {
 #pragma clang fp contract(off)
   // squarings: an error of about step * 2^-53, and b^step is 0 long before that counts
-  uint64_t e = step < 9.0e15 ? static_cast<uint64_t>(step) : uint64_t(9000000000000000);
+  uint64_t e = step < 1.0 ? 0 : step < 9.0e15 ? static_cast<uint64_t>(step) : uint64_t(9000000000000000);
   double r = 1.0;
   while (e) {
     if (e & 1) r = r * b;
