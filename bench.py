@@ -12,6 +12,7 @@ moe_layer_forward on the weights as stored.
   python bench.py --backward [--workload NAME] ...   (the layer's backward instead)
   python bench.py --backward --saved ...             (with FC1's g|u kept by the forward)
   python bench.py --backward --wgrad-bf16 ...        (weight gradients written as bf16)
+  python bench.py --backward --update 8|32 ...       (and the norm, the gradients' norm and the AdamW update)
 
 The default workload is the Mixtral-8x22B-shaped prefill layer (T=8192,
 d=6144, f=16384, E=8, top-2, bf16, routing skewed by the gate-logit bias
@@ -73,6 +74,9 @@ def parse():
     p.add_argument("--saved", action="store_true",
                    help="with --backward: the forward keeps FC1's g|u (moe_layer_forward_train) and the backward "
                         "reads it (moe_layer_backward_saved); also times forward + backward both ways")
+    p.add_argument("--update", type=int, choices=[8, 32], default=0,
+                   help="with --backward: also time what a training step runs around the layer (norm and its gradients, "
+                        "the gradients' norm, AdamW on the layer's weights with states of so many bits)")
     p.add_argument("--copy-probe", action="store_true",
                    help="only run 5 device copies of 1 GiB (reference kernel for HBM byte counters)")
     return p.parse_args()
@@ -364,6 +368,58 @@ def cpu_baseline_backward(cfg, inp, dout, ntok: int, seed: int = 0):
                       f"tokens of workload {cfg.name}, seed {seed} inputs; {dt:.1f} s"}
 
 
+def time_update(args, cfg, dims, inp, grads, stream) -> dict:
+    """What a training step runs around the layer, one after another on its tensors: the
+    norm in front of it with the residual added, the norm's gradients, the 2-norm of the
+    layer's gradients and the AdamW step (bf16 weights rounded stochastically). Mean ms of
+    each and the rate of the bytes it cannot do without."""
+    import torch
+    import mixture_experts_layer_gate_amd as moe
+
+    x, res = inp["x"], inp["x"].flip(0).contiguous()
+    weight = torch.ones(cfg.d, device=x.device)
+    opts = moe.NormOptions("rms")
+    y, s, _, rstd = moe.norm_forward(dims, opts, x, weight, residual=res, keep=True)
+    out = {n: torch.empty_like(x) for n in ("s", "y", "dx")}
+    dw = torch.empty(cfg.d, device=x.device)
+    ws = torch.empty(moe.norm_backward_workspace_bytes(dims, opts), dtype=torch.uint8, device=x.device)
+    names = ("wg", "w1", "w3", "w2")
+    state = moe.adam_state([inp[n] for n in names], args.update)
+    gl = moe.GradList([grads["d" + n] for n in names])
+    gws = torch.empty(moe.grad_norm_workspace_bytes(gl), dtype=torch.uint8, device=x.device)
+    norm = torch.zeros(2, device=x.device)
+    rng = torch.tensor([args.seed, 0], device=x.device)
+    adam = moe.AdamOptions(weight_decay=0.1, stochastic=True)
+    n = sum(inp[k].numel() for k in names)
+    gb = sum(g.numel() * g.element_size() for g in gl.tensors)
+    rows = cfg.T * cfg.d * 2
+    calls = {
+        "norm": (lambda: moe.norm_forward(dims, opts, x, weight, residual=res, sum=out["s"], y=out["y"], rstd=rstd,
+                                          stream=stream), 4 * rows),
+        "norm_grad": (lambda: moe.norm_backward(dims, opts, y, s, weight, rstd, dx_in=res, dx=out["dx"], dweight=dw, ws=ws,
+                                                stream=stream), 4 * rows),
+        "grad_norm": (lambda: moe.grad_norm(gl, 1.0, 1.0, out=norm, ws=gws, stream=stream), gb),
+        # lr 0: the weights stay what the other measurements run on
+        "adam": (lambda: moe.adam_step(adam, state, gl, lr=0.0, step=1, gscale=norm[1:], rng=rng, stream=stream),
+                 n * (4 + (16 if args.update == 32 else 4)) + gb),
+    }
+    ms = {}
+    for name, (fn, nbytes) in calls.items():
+        for _ in range(max(args.warmup, 1)):
+            fn()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record(stream)
+        for _ in range(args.steps):
+            fn()
+        e1.record(stream)
+        torch.cuda.synchronize()
+        t = e0.elapsed_time(e1) / args.steps
+        ms[name] = {"ms": round(t, 4), "GBps": round(nbytes / (t * 1e-3) / 1e9, 1)}
+    return {"state_bits": args.update, "parameters": n, "state_bytes": sum(
+        t.numel() * t.element_size() for ts in (state.m, state.v, state.m_scale, state.v_scale) if ts for t in ts),
+        "stages": ms}
+
+
 def run_backward(args, seed: int) -> dict:
     """One measurement of moe_layer_backward on the workload's inputs for `seed`:
     the forward runs once for the routing, then every step computes all
@@ -501,6 +557,8 @@ def run_backward(args, seed: int) -> dict:
     }
     if pair is not None:
         res["train_pair"] = pair
+    if args.update:
+        res["update"] = time_update(args, cfg, dims, inp, grads, stream)
     if not args.no_cpu_baseline:
         ntok = min(cfg.T, args.cpu_sample_tokens if args.cpu_sample_tokens > 0 else 32)
         res["cpu_baseline"] = cpu_baseline_backward(cfg, inp, dout, ntok, seed)

@@ -197,3 +197,20 @@ def test_a_stream_of_steps_over_kept_gradients():
         assert torch.equal(out, first)
         for n in ("params", "m", "v", "m_scale", "v_scale"):
             assert all(torch.equal(x, y) for x, y in zip(getattr(a, n), getattr(b, n))), (k, n)
+
+
+def test_bench_update_line():
+    """bench.py --backward --update: one JSON line that carries the norm's, the gradient norm's and the update's times."""
+    import json
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    cmd = [sys.executable, os.path.join(root, "bench.py"), "--backward", "--update", "8", "--wgrad-bf16", "--workload",
+           "mixtral_decode_t16", "--steps", "2", "--warmup", "1", "--no-cpu-baseline"]
+    _say("bench --backward --update 8")
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0, r.stderr[-2000:]
+    j = json.loads([l for l in r.stdout.splitlines() if l.startswith("{")][0])
+    assert set(j["update"]["stages"]) == {"norm", "norm_grad", "grad_norm", "adam"}
+    assert j["update"]["state_bits"] == 8 and all(v["ms"] > 0 for v in j["update"]["stages"].values())
