@@ -599,8 +599,9 @@ int moe_norm_backward(const moe_dims_t* dims, const moe_norm_opts_t* opts, const
 
 /* ---- behind the backward: the gradients' norm and the update ----
  * Both take a list of tensors, a HOST array that is read during the call only (a
- * captured graph holds its contents). At most 2^36 elements to a tensor and 2^20
- * tensors (MOE_ERR_UNSUPPORTED beyond); tensors of 0 elements are passed over.
+ * captured graph holds its contents). At most 2^36 elements to a gradient, 2^34 to
+ * a parameter, and 2^20 tensors (MOE_ERR_UNSUPPORTED beyond); tensors of 0 elements
+ * are passed over.
  * Buffers need their element's alignment; where all of a tensor's are 16-byte
  * aligned (8-bit codes: 8-byte) the loads are wide. */
 typedef struct {

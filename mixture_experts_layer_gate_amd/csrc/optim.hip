@@ -177,7 +177,7 @@ __device__ __forceinline__ double chunk_squares(const GradTable& t, uint32_t c) 
   const void* p = from(g.g, bf16, i0);
   const int left = left_of(g.n, i0, t.chunk);
   double s = 0.0;
-  for (int q = 0; q < left; q += 2048) {
+  for (int q = 0; q < left; q += kRound) {
     float v[8];
     if (bf16) load8<kStream>(p, true, Place<4>(q, left, aligned), v);
     else load8<kStream>(p, false, Place<1024>(q, left, aligned), v);
@@ -329,11 +329,18 @@ __device__ __forceinline__ bool roots(const float (&v)[8], float (&r)[8], uint32
   return true;
 }
 
-// One turn of a workgroup to at most t.chunk elements of a tensor. With 8-bit
-// states bound by the vector instructions and memory alike (measured on 88 M bf16
-// weights with bf16 gradients: see the launcher), with 32-bit ones by memory.
+// One turn of a workgroup to at most t.chunk elements of a tensor.
+// With 32-bit states bound by memory, where fewer, shorter turns at a time keep the
+// accesses closer together: 302 M bf16 weights with fp32 masters, states and
+// gradients in turns of 2048, at most 3, 4, 5, 6, 8 waves to a SIMD 1541, 1525,
+// 1584, 1601, 1616 us; in turns of 4096 1572 and 1601 with 3 and 4, of 8192 1589,
+// 1657, 1665, 1678, 1686 with 3, 4, 5, 6, 8 (9.66 GB: 6.3 TB/s at best).
+// With 8-bit states by the vector instructions, some 450 to a wave's 512 elements,
+// and memory alike: 88 M bf16 weights and gradients 171 us (883 MB, 5.2 TB/s); with
+// 4, 5, 6 and 8 waves (and the states read out) 273, 250, 237, 234 us.
 template <int kBits, bool kStream>
-__global__ __launch_bounds__(256) void adam_kernel(AdamTable t) {
+__global__ __attribute__((amdgpu_waves_per_eu(1, kBits == 32 ? 4 : 8))) __launch_bounds__(256) void adam_kernel(
+    AdamTable t) {
 #pragma clang fp contract(off)
   const uint32_t c = blockIdx.x;
   const AdamEntry& en = t.t[find_tensor<kAdamTensors>(t, c)];
@@ -359,7 +366,7 @@ __global__ __launch_bounds__(256) void adam_kernel(AdamTable t) {
   uint8_t* const qm = kBits == 8 ? en.ms + i0 / kScaleBlock : nullptr;
   uint8_t* const qv = kBits == 8 ? en.vs + i0 / kScaleBlock : nullptr;
   const float nan = __uint_as_float(0x7fc00000u);
-  for (int q = 0; q < left; q += 2048) {
+  for (int q = 0; q < left; q += kRound) {
     const Place<kGap> at(q, left, al);
     float w[8], g[8], m[8], v[8];
     if (master) load8<kStream>(master, false, at, w);
@@ -471,7 +478,7 @@ __global__ __launch_bounds__(256) void state_values_kernel(StateTable t) {
   void* const pm = const_cast<void*>(from(en.m_out, kOut == 1, i0));
   void* const pr = const_cast<void*>(from(en.r_out, kOut == 1, i0));
   const float nan = __uint_as_float(0x7fc00000u);
-  for (int q = 0; q < left; q += 2048) {
+  for (int q = 0; q < left; q += kRound) {
     const Place<4> at(q, left, en.aligned);
     if (at.i >= left) break;
     const uint2 cm = load_codes<kStream>(en.m + i0, at), cv = load_codes<kStream>(en.v + i0, at);

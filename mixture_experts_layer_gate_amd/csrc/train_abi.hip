@@ -29,13 +29,13 @@ struct Cut {
   bool stream;
 };
 template <typename Item, typename Fn>
-Cut cut_of(const Item* t, int32_t count, Fn&& each) {
+Cut cut_of(const Item* t, int32_t count, int chunk, Fn&& each) {
   double n = 0, bytes = 0;
   for (int32_t i = 0; i < count; ++i) {
     n += static_cast<double>(t[i].n);
     bytes += static_cast<double>(t[i].n) * static_cast<double>(each(i));
   }
-  return {n <= kListSmall ? kListChunkSmall : kListChunk, bytes >= kListStream};
+  return {n <= kListSmall ? kRound : chunk, bytes >= kListStream};
 }
 int64_t chunks_of(int64_t n, int chunk) { return (n + chunk - 1) / chunk; }
 
@@ -104,7 +104,7 @@ int each_grad_table(const moe_grad_t* g, int32_t count, const Cut& cut, Fn&& fn)
 }
 
 Cut grad_cut(const moe_grad_t* g, int32_t count) {
-  return cut_of(g, count, [&](int32_t i) { return size_of(g[i].dtype); });
+  return cut_of(g, count, kListChunk, [&](int32_t i) { return size_of(g[i].dtype); });
 }
 
 int64_t grad_parts(const moe_grad_t* g, int32_t count) {
@@ -150,7 +150,7 @@ int check_tensors(const moe_adam_tensor_t* t, int32_t count, int bits, bool with
   for (int32_t i = 0; i < count; ++i) {
     const moe_adam_tensor_t& a = t[i];
     if (a.n < 0) return MOE_ERR_INVALID;
-    if (a.n > kListElements) return MOE_ERR_UNSUPPORTED;
+    if (a.n > kAdamElements) return MOE_ERR_UNSUPPORTED;
     if (with_params && !ok_dtype(a.dtype)) return MOE_ERR_INVALID;
     if (a.n == 0) continue;
     if (with_params) {
@@ -287,7 +287,7 @@ int moe_adam_step(const moe_adam_opts_t* op, const moe_adam_tensor_t* tensors, c
   k.eps = static_cast<float>(op->eps);
   if (!lr_step) adam_scalars(k, op->lr, static_cast<double>(op->step));
   const uintptr_t code_align = op->state_bits == 8 ? 8 : 16;
-  const Cut cut = cut_of(tensors, count, [&](int32_t i) {
+  const Cut cut = cut_of(tensors, count, op->state_bits == 8 ? kCodeChunk : kRound, [&](int32_t i) {
     return 2 * size_of(tensors[i].dtype) + size_of(grads[i].dtype) + (op->state_bits == 8 ? 4 : 16) +
            (tensors[i].master ? 8 : 0);
   });
@@ -325,7 +325,7 @@ int moe_adam_state_values(const moe_adam_tensor_t* tensors, int32_t count, void*
     if (tensors[i].n && (!ok_elements(m_out[i], out_dtype) || !ok_elements(r_out[i], out_dtype))) return MOE_ERR_INVALID;
   hipStream_t s = static_cast<hipStream_t>(stream);
   StageScope sc(MOE_STAGE_ADAM, s);
-  const Cut cut = cut_of(tensors, count, [&](int32_t) { return 2 + 2 * size_of(out_dtype); });
+  const Cut cut = cut_of(tensors, count, kCodeChunk, [&](int32_t) { return 2 + 2 * size_of(out_dtype); });
   StateTable t;
   t.count = 0;
   t.chunks = 0;
