@@ -219,6 +219,11 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a)
   }
 }
 
+template <int kDtype, int NV, bool kWaveRow>
+constexpr bool wide() {
+  return !kWaveRow && NV * kVec<kDtype> > 8;
+}
+
 // Gradients: with h = (x - mean) rstd and g = dy w,
 //   dx = rstd (g - mean(g) - h mean(g h)) + dx_in      (mean(g): layer norm)
 //   dw = sum_t dy h,  db = sum_t dy.
@@ -227,8 +232,8 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a)
 // row means come from one exchange between the waves.
 // Differences to the mean are formed at half size and rstd at double, so that
 // neither passes fp32's range where h does not.
-template <int kDtype, bool kLayer, int NV, bool kWaveRow, bool kStream>
-__global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGradArgs a) {
+template <int kDtype, bool kLayer, int NV, bool kWaveRow, bool kStream, bool kSums>
+__device__ __forceinline__ void grad_rows(const NormGradArgs& a, int block, int blocks) {
   constexpr int V = kVec<kDtype>;
   __shared__ __attribute__((aligned(16))) float red[2][2][16];
   if (!kWaveRow) {
@@ -241,10 +246,11 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
   const int nw = blockDim.x >> 6;
   const int per = kWaveRow ? nw : 1;
   const float inv_d = 1.0f / static_cast<float>(a.d);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * per;
-  // 16 columns to a thread of a full workgroup leave no registers for the next row
-  // and the weights, which are read again for every row then
-  constexpr bool kWide = !kWaveRow && NV * V > 8;
+  const int64_t step = static_cast<int64_t>(blocks) * per;
+  // 16 columns to a thread of a full workgroup leave no registers for their sums, for
+  // the next row and for the weights, which are read again for every row then
+  constexpr bool kWide = wide<kDtype, NV, kWaveRow>();
+  static_assert(!(kWide && kSums), "columns summed apart");
   float aw[NV][V], ab[NV][V], w[kWide ? 1 : NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -265,12 +271,13 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
       const int64_t at = t * nvec + c;
       ud[j] = in ? get<kStream>(reinterpret_cast<const uint4*>(a.dy) + at) : make_uint4(0, 0, 0, 0);
       ux[j] = in ? get<kStream>(reinterpret_cast<const uint4*>(a.x) + at) : make_uint4(0, 0, 0, 0);
-      if (a.dx_in) ui[j] = in ? get<kStream>(reinterpret_cast<const uint4*>(a.dx_in) + at) : make_uint4(0, 0, 0, 0);
+      if (!kWide && a.dx_in)
+        ui[j] = in ? get<kStream>(reinterpret_cast<const uint4*>(a.dx_in) + at) : make_uint4(0, 0, 0, 0);
     }
     rstd = a.rstd[t];
     if constexpr (kLayer) mean = a.mean[t];
   };
-  int64_t t = static_cast<int64_t>(blockIdx.x) * per + (kWaveRow ? (threadIdx.x >> 6) : 0);
+  int64_t t = static_cast<int64_t>(block) * per + (kWaveRow ? (threadIdx.x >> 6) : 0);
   if (!kWide && t < a.T) fetch(t);
   for (int half = 0; t < a.T; t += step, half ^= 1) {
     if (kWide) fetch(t);
@@ -281,7 +288,7 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
     for (int j = 0; j < NV; ++j) {
       unpack<kDtype>(ux[j], h[j]);
       unpack<kDtype>(ud[j], g[j]);
-      add[j] = ui[j];
+      if (!kWide) add[j] = ui[j];
     }
     // the next row is on its way while this one's sums are exchanged
     if (!kWide && t + step < a.T) fetch(t + step);
@@ -297,8 +304,8 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         h[j][i] = in ? fmaf(h[j][i], 0.5f, m2) * r2 : 0.0f;
-        aw[j][i] = fmaf(g[j][i], h[j][i], aw[j][i]);
-        if constexpr (kLayer) ab[j][i] += g[j][i];
+        if constexpr (kSums) aw[j][i] = fmaf(g[j][i], h[j][i], aw[j][i]);
+        if constexpr (kSums && kLayer) ab[j][i] += g[j][i];
         g[j][i] *= w[kWide ? 0 : j][i];
         if constexpr (kLayer) sg += g[j][i];
         sh = fmaf(g[j][i], h[j][i], sh);
@@ -324,6 +331,7 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
       const int c = tid + j * lanes;
       if (c >= nvec) continue;
       float o[V];
+      if (kWide && a.dx_in) add[j] = reinterpret_cast<const uint4*>(a.dx_in)[t * nvec + c];
       if (a.dx_in) unpack<kDtype>(add[j], o);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -334,6 +342,7 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
       reinterpret_cast<uint4*>(a.dx)[t * nvec + c] = pack<kDtype>(o);
     }
   }
+  if constexpr (!kSums) return;
   // this workgroup's part
   if constexpr (kWaveRow) {
     __shared__ float joined[64 * NV * V];
@@ -358,7 +367,7 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
         for (int j = 0; j < NV; ++j) {
           const int c = tid + j * 64;
           if (c >= nvec) continue;
-          float4* p = reinterpret_cast<float4*>(part + static_cast<int64_t>(blockIdx.x) * a.d + c * V);
+          float4* p = reinterpret_cast<float4*>(part + static_cast<int64_t>(block) * a.d + c * V);
 #pragma unroll
           for (int q = 0; q < V / 4; ++q) {
             const float* f = joined + (j * V + 4 * q) * 64 + tid;
@@ -372,7 +381,7 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
     for (int j = 0; j < NV; ++j) {
       const int c = tid + j * lanes;
       if (c >= nvec) continue;
-      const int64_t at = static_cast<int64_t>(blockIdx.x) * a.d + c * V;
+      const int64_t at = static_cast<int64_t>(block) * a.d + c * V;
 #pragma unroll
       for (int q = 0; q < V / 4; ++q) {
         if (a.part_w)
@@ -384,6 +393,91 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
       }
     }
   }
+}
+
+template <int kDtype, bool kLayer, int NV, bool kWaveRow, bool kStream>
+__global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGradArgs a) {
+  grad_rows<kDtype, kLayer, NV, kWaveRow, kStream, true>(a, blockIdx.x, gridDim.x);
+}
+
+// dw and db of 64 bytes of columns over all rows, which need nothing but the rows'
+// statistics: four vectors to a row, a row to every four threads. A thread's sums
+// go into its total every 32 rows; the threads' totals are joined inside the rows
+// of 16 lanes, then between those, in a fixed order.
+template <int kDtype, bool kLayer>
+__device__ __forceinline__ void grad_columns(const NormGradArgs& a, int block, float* dw, float* db) {
+  constexpr int V = kVec<kDtype>;
+  __shared__ float join[kLayer ? 2 : 1][64][4 * V];
+  const int nvec = a.d / V, groups = blockDim.x >> 2;
+  const int q = threadIdx.x & 3, c = block * 4 + q;
+  float tw[V], tb[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) tw[i] = tb[i] = 0.0f;
+  if (c < nvec) {
+    for (int64_t t0 = threadIdx.x >> 2; t0 < a.T; t0 += 32 * groups) {
+      const int64_t end = t0 + 32 * groups < a.T ? t0 + 32 * groups : a.T;
+      float aw[V], ab[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) aw[i] = ab[i] = 0.0f;
+#pragma unroll 4
+      for (int64_t t = t0; t < end; t += groups) {
+        const int64_t at = t * nvec + c;
+        float g[V], h[V];
+        unpack<kDtype>(reinterpret_cast<const uint4*>(a.dy)[at], g);
+        unpack<kDtype>(reinterpret_cast<const uint4*>(a.x)[at], h);
+        const float r2 = 2.0f * a.rstd[t], m2 = kLayer ? -0.5f * a.mean[t] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          aw[i] = fmaf(g[i], fmaf(h[i], 0.5f, m2) * r2, aw[i]);
+          if constexpr (kLayer) ab[i] += g[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        tw[i] += aw[i];
+        tb[i] += ab[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    tw[i] = ror_add<4>(ror_add<8>(tw[i]));
+    if constexpr (kLayer) tb[i] = ror_add<4>(ror_add<8>(tb[i]));
+  }
+  if ((threadIdx.x & 15) < 4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      join[0][threadIdx.x >> 4][q * V + i] = tw[i];
+      if constexpr (kLayer) join[kLayer ? 1 : 0][threadIdx.x >> 4][q * V + i] = tb[i];
+    }
+  }
+  __syncthreads();
+  const int which = threadIdx.x / (4 * V), i = threadIdx.x % (4 * V), col = block * 4 * V + i;
+  if (which < (kLayer ? 2 : 1) && col < a.d) {
+    float* out = which == 0 ? dw : db;
+    if (out) {
+      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // (a multiple of four rows of 16 lanes: whole waves)
+      for (unsigned r = 0; r < blockDim.x >> 4; r += 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] += join[which][r + k][i];
+      }
+      out[col] = (s[0] + s[1]) + (s[2] + s[3]);
+    }
+  }
+}
+
+// Both in one launch: the first `columns` workgroups sum dw and db, the others form
+// dx. For short batches, where reading dy and x twice costs less than writing parts
+// and a launch to sum them, and for rows of over 8192 columns, whose sums leave a
+// thread no registers (2047 x 16384 with bias: 94 us, and 644 with parts). Measured against
+// parts: 32 x 7168 4.3 and 7.0 us, 512 x 7168 12.3 and 15.4, 768 x 7168 17.0 and
+// 15.6; 1024 x 4096 with bias 12.5 and 15.2, 2047 x 4096 21.7 and 20.3; 1024 x 512
+// 4.9 and 7.3, 2047 x 512 12.4 and 8.0.
+template <int kDtype, bool kLayer, int NV, bool kWaveRow>
+__global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_short_kernel(NormGradArgs a, int columns, float* dw,
+                                                                                float* db) {
+  if (static_cast<int>(blockIdx.x) < columns) grad_columns<kDtype, kLayer>(a, blockIdx.x, dw, db);
+  else grad_rows<kDtype, kLayer, NV, kWaveRow, false, false>(a, blockIdx.x - columns, gridDim.x - columns);
 }
 
 // Column sums of the parts: 16 columns to a workgroup (64 bytes of a part's row),
@@ -481,10 +575,28 @@ struct NormGradLaunch {
   hipStream_t s;
   template <int kDtype, bool kLayer, int NV, bool kWaveRow, bool kStream>
   void launch() const {
-    hipLaunchKernelGGL((norm_grad_kernel<kDtype, kLayer, NV, kWaveRow, kStream>), grid, block, 0, s, a);
+    if constexpr (!wide<kDtype, NV, kWaveRow>())
+      hipLaunchKernelGGL((norm_grad_kernel<kDtype, kLayer, NV, kWaveRow, kStream>), grid, block, 0, s, a);
   }
 };
 
+struct NormShortLaunch {
+  const NormGradArgs& a;
+  int columns;
+  float *dw, *db;
+  dim3 grid, block;
+  hipStream_t s;
+  template <int kDtype, bool kLayer, int NV, bool kWaveRow, bool kStream>
+  void launch() const {
+    hipLaunchKernelGGL((norm_grad_short_kernel<kDtype, kLayer, NV, kWaveRow>), grid, block, 0, s, a, columns, dw, db);
+  }
+};
+
+// Whether dw and db are summed by columns rather than from parts (as measured above).
+bool by_columns(int dtype, const Shape& sh, int64_t T, int64_t d) {
+  if (!sh.wave && sh.nv * (dtype == 1 ? 8 : 4) > 8) return true;
+  return T <= 1024 && T * d * (dtype == 1 ? 2 : 4) <= int64_t(10) << 20;
+}
 constexpr int64_t kResident = 2048;  // threads that a compute unit holds
 constexpr int64_t kStreamBytes = int64_t(128) << 20;
 
@@ -511,13 +623,25 @@ int norm_grad_parts(int dtype, int64_t T, int64_t d) {
 hipError_t launch_norm_grad(int dtype, bool layer, const NormGradArgs& a, int parts, float* dw, float* db,
                             hipStream_t s) {
   const Shape sh = row_shape(dtype, a.d, 1024);
+  const bool sums = dw || db;
+  if (by_columns(dtype, sh, a.T, a.d)) {
+    const int columns = sums ? (a.d / (dtype == 1 ? 8 : 4) + 3) / 4 : 0;
+    const int64_t groups = sh.wave ? (a.T + 3) / 4 : a.T;
+    const int rows = static_cast<int>(groups < 1024 ? groups : 1024);
+    // (where dx takes the place of what the columns read, they are summed first)
+    const bool apart = sums && (a.dx == a.dy || a.dx == a.x);
+    by_type(dtype, layer, false, sh,
+            NormShortLaunch{a, columns, dw, db, dim3(columns + (apart ? 0 : rows)), dim3(sh.threads), s});
+    if (apart) by_type(dtype, layer, false, sh, NormShortLaunch{a, 0, dw, db, dim3(rows), dim3(sh.threads), s});
+    return hipGetLastError();
+  }
   const dim3 grid(parts);
   const int64_t bytes = a.T * a.d * (dtype == 1 ? 2 : 4) * (a.dx_in ? 4 : 3);
   by_type(dtype, layer, bytes >= kStreamBytes, sh, NormGradLaunch{a, grid, dim3(sh.threads), s});
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (!dw && !db) return hipSuccess;
-  hipLaunchKernelGGL(norm_parts_kernel, dim3((a.d + 15) / 16, db ? 2 : 1), dim3(parts > 256 ? 1024 : 256), 0, s, a.part_w, a.part_b, parts,
-                     a.d, dw, db);
+  hipLaunchKernelGGL(norm_parts_kernel, dim3((a.d + 15) / 16, db ? 2 : 1), dim3(parts > 256 ? 1024 : 256), 0, s,
+                     a.part_w, a.part_b, parts, a.d, dw, db);
   return hipGetLastError();
 }
 
