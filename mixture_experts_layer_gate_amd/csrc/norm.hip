@@ -146,15 +146,16 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a)
     for (int j = 0; j < NV; ++j) {
       const int c = tid + j * lanes;
       unpack<kDtype>(ux[j], v[j]);
+      uint4 o = ux[j];
       if (a.residual) {
         float r[V];
         unpack<kDtype>(ur[j], r);
 #pragma unroll
         for (int i = 0; i < V; ++i) v[j][i] += r[i];
-        const uint4 o = pack<kDtype>(v[j]);
+        o = pack<kDtype>(v[j]);
         unpack<kDtype>(o, v[j]);
-        if (a.sum && c < nvec) put<kStream>(reinterpret_cast<uint4*>(a.sum) + t * nvec + c, o);
       }
+      if (a.sum && c < nvec) put<kStream>(reinterpret_cast<uint4*>(a.sum) + t * nvec + c, o);
     }
     // the next row is on its way while this one's sums are exchanged
     if (t + step < a.T) fetch(t + step);

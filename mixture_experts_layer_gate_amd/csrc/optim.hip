@@ -335,8 +335,8 @@ __device__ __forceinline__ bool roots(const float (&v)[8], float (&r)[8], uint32
 // gradients in turns of 2048, at most 3, 4, 5, 6, 8 waves to a SIMD 1541, 1525,
 // 1584, 1601, 1616 us; in turns of 4096 1572 and 1601 with 3 and 4, of 8192 1589,
 // 1657, 1665, 1678, 1686 with 3, 4, 5, 6, 8 (9.66 GB: 6.3 TB/s at best).
-// With 8-bit states by the vector instructions, some 450 to a wave's 512 elements,
-// and memory alike: 88 M bf16 weights and gradients 171 us (883 MB, 5.2 TB/s); with
+// With 8-bit states by the vector instructions, some 490 to a wave's 512 elements,
+// and memory alike: 88 M bf16 weights and gradients 170 us (883 MB, 5.2 TB/s); with
 // 4, 5, 6 and 8 waves (and the states read out) 273, 250, 237, 234 us.
 template <int kBits, bool kStream>
 __global__ __attribute__((amdgpu_waves_per_eu(1, kBits == 32 ? 4 : 8))) __launch_bounds__(256) void adam_kernel(

@@ -321,8 +321,12 @@ int moe_adam_state_values(const moe_adam_tensor_t* tensors, int32_t count, void*
   if (!ok_dtype(out_dtype)) return MOE_ERR_INVALID;
   if (int st = check_tensors(tensors, count, 8, false)) return st;
   if (count > 0 && (!m_out || !r_out)) return MOE_ERR_INVALID;
+  Seen seen;
+  if (!seen.make(2 * static_cast<size_t>(count) + 1)) return MOE_ERR_HIP;
   for (int32_t i = 0; i < count; ++i)
-    if (tensors[i].n && (!ok_elements(m_out[i], out_dtype) || !ok_elements(r_out[i], out_dtype))) return MOE_ERR_INVALID;
+    if (tensors[i].n && (!ok_elements(m_out[i], out_dtype) || !ok_elements(r_out[i], out_dtype) ||
+                         seen.again(m_out[i]) || seen.again(r_out[i])))
+      return MOE_ERR_INVALID;
   hipStream_t s = static_cast<hipStream_t>(stream);
   StageScope sc(MOE_STAGE_ADAM, s);
   const Cut cut = cut_of(tensors, count, kCodeChunk, [&](int32_t) { return 2 + 2 * size_of(out_dtype); });

@@ -214,3 +214,64 @@ def test_bench_update_line():
     j = json.loads([l for l in r.stdout.splitlines() if l.startswith("{")][0])
     assert set(j["update"]["stages"]) == {"norm", "norm_grad", "grad_norm", "adam"}
     assert j["update"]["state_bits"] == 8 and all(v["ms"] > 0 for v in j["update"]["stages"].values())
+
+
+@pytest.mark.parametrize("T,d", [(1030, 520), (1100, 1032), (1030, 4104), (1500, 7168), (2500, 2048), (700, 8192), (300, 12296)])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+def test_norm_backward_of_longer_batches(dt, kind, T, d):
+    """Batches whose weight gradients are summed from parts of the rows, and wide ones summed by columns: every output, in
+    place too, and with the bias' or the weight's gradient alone. Bounds as for the short ones, a part having at most
+    T / 256 rows of its own."""
+    layer = kind == "layer"
+    half = BF if dt is BF16 else U
+    _say(f"{kind} {dt} {T} x {d}")
+    gen = torch.Generator(device="cuda").manual_seed(T + d)
+    rn = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    x, dy, di = (rn(T, d) + 0.5 * rn(T, 1)).to(dt), (rn(T, d) * 0.01).to(dt), (rn(T, d) * 0.01).to(dt)
+    w = 1 + 0.2 * rn(d)
+    dims, opts = moe.Dims(T, d, 64, 8, 2, dt), moe.NormOptions(kind, 1e-5)
+    _, s, mean, rstd = moe.norm_forward(dims, opts, x, w, keep=True)
+    dx, dw, db = moe.norm_backward(dims, opts, dy, s, w, rstd, mean=mean, dx_in=di, want_dbias=layer)
+    nm = mean.double()[:, None] if layer else torch.zeros((T, 1), dtype=torch.float64, device="cuda")
+    nr = rstd.double()[:, None]
+    h, up = (s.double() - nm) * nr, dy.double()
+    g = up * w.double()
+    mgh, mg = (g * h).mean(1, keepdim=True), g.mean(1, keepdim=True)
+    rx = nr * (g - h * mgh - (mg if layer else 0)) + di.double()
+    bound = nr * U * (4 * g.abs() + 50 * h.abs() * (g * h).abs().mean(1, keepdim=True) + 46 * g.abs().mean(1, keepdim=True))
+    assert bool(((dx.double() - rx).abs() <= bound + (half + 2 * U) * rx.abs() + 2 * U * di.double().abs()).all())
+    rows = -(-T // 256) + 64
+    assert bool(((dw.double() - (up * h).sum(0)).abs() <= (rows + 4) * U * (up * h).abs().sum(0)).all())
+    if layer:
+        assert bool(((db.double() - up.sum(0)).abs() <= rows * U * up.abs().sum(0)).all())
+        only = moe.norm_backward(dims, opts, dy, s, w, rstd, mean=mean, dx_in=di, want_dweight=False, want_dbias=True)
+        assert torch.equal(only[0], dx) and only[1] is None and torch.equal(only[2], db)
+    only = moe.norm_backward(dims, opts, dy, s, w, rstd, mean=mean, dx_in=di)
+    assert torch.equal(only[0], dx) and torch.equal(only[1], dw) and only[2] is None
+    none = moe.norm_backward(dims, opts, dy, s, w, rstd, mean=mean, dx_in=di, want_dweight=False)
+    assert torch.equal(none[0], dx)
+    for k in range(3):
+        t = [dy.clone(), s.clone(), di.clone()]
+        got = moe.norm_backward(dims, opts, t[0], t[1], w, rstd, mean=mean, dx_in=t[2], dx=t[k], want_dbias=layer)
+        assert torch.equal(got[0], dx) and torch.equal(got[1], dw) and (not layer or torch.equal(got[2], db))
+
+
+def test_sum_without_a_residual_is_x():
+    """Through the C ABI: the sum's tensor takes x, and y is the norm of it."""
+    lib = moe.load_library()
+    for T, d, dt in ((5, 64, BF16), (3, 7168, BF16), (4, 1048, F32)):
+        dims, opts = moe.Dims(T, d, 64, 8, 2, dt), moe.NormOptions("layer", 1e-5)
+        x = torch.randn((T, d), device="cuda").to(dt)
+        s, y = torch.zeros_like(x), torch.zeros_like(x)
+        st = lib.moe_norm_forward(dims.ref(), opts.ref(), x.data_ptr(), None, None, None, s.data_ptr(), y.data_ptr(), None,
+                                  None, torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert st == 0 and torch.equal(s, x) and torch.equal(y, moe.norm_forward(dims, opts, x)[0])
+
+
+def test_state_values_refuse_an_output_twice():
+    st = moe.adam_state([torch.zeros(9, device="cuda"), torch.zeros(9, device="cuda")], 8)
+    a, b, c = (torch.zeros(9, device="cuda") for _ in range(3))
+    with pytest.raises(moe.MoeError):
+        moe.adam_state_values(st, m=[a, b], r=[a, c])
