@@ -319,3 +319,18 @@ def test_states_are_copied_with_their_tensors(bits):
     assert h._rows[0] == h.tensors[0].data_ptr() != g._rows[0]
     for value in (moe.NormOptions("layer"), moe.AdamOptions(beta2=0.9)):
         assert pickle.loads(pickle.dumps(value)) == value
+
+
+def test_checked_lists_are_fixed():
+    """What the lists hold was read when they were made: it is not exchanged under them."""
+    st, g = moe.adam_state([torch.zeros(7)]), moe.GradList([torch.zeros(7)])
+    with pytest.raises(AttributeError, match="fixed"):
+        st.m = [torch.zeros(7)]
+    with pytest.raises(TypeError):
+        st.m[0] = torch.zeros(7)
+    with pytest.raises(AttributeError, match="fixed"):
+        g.tensors = [torch.zeros(7)]
+    with pytest.raises(TypeError):
+        g.tensors[0] = torch.zeros(7)
+    assert moe.grad_norm_workspace_bytes(g) == moe.grad_norm_workspace_bytes(g) > 0 if os.path.exists(
+        moe.library_path()) else True
