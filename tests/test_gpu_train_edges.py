@@ -275,3 +275,23 @@ def test_state_values_refuse_an_output_twice():
     a, b, c = (torch.zeros(9, device="cuda") for _ in range(3))
     with pytest.raises(moe.MoeError):
         moe.adam_state_values(st, m=[a, b], r=[a, c])
+
+
+@pytest.mark.parametrize("d", [256, 1032, 4104, 7168, 16384])
+@pytest.mark.parametrize("offset", [1e2, 1e4, 1e6, -3e7])
+def test_layer_norm_of_rows_far_from_zero(offset, d):
+    """fp32 rows of unit spread around a large mean. What the mean's own rounding costs is taken back, so that y is off by
+    the roundings of the differences (exact where x lies within a factor of two of the mean, else u of it, a size of the
+    spread here) and of the row's sums over them: 60 u of a size of sqrt(d), and mean by its rounding as a number."""
+    T = 7
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    x = (torch.randn((T, d), generator=gen, device="cuda").double() * max(1.0, abs(offset) * 2.0 ** -20) + offset).float()
+    dims, opts = moe.Dims(T, d, 64, 8, 2, F32), moe.NormOptions("layer", 1e-5)
+    y, _, mean, rstd = moe.norm_forward(dims, opts, x, keep=True)
+    z = x.double()
+    mu = z.mean(1, keepdim=True)
+    rs = 1 / torch.sqrt(((z - mu) ** 2).mean(1, keepdim=True) + 1e-5)
+    assert bool(((mean.double()[:, None] - mu).abs() <= 1.01 * U * mu.abs() + 60 * U / rs).all())
+    assert bool(((rstd.double()[:, None] / rs - 1).abs() <= 60 * U).all())
+    h = (z - mu) * rs
+    assert bool(((y.double() - h).abs() <= 60 * U * (1 + h.abs())).all())
