@@ -959,9 +959,9 @@ def norm_forward(dims: Dims, opts: NormOptions, x, weight=None, bias=None, resid
                  rstd=None, keep=False, stream=None):
     """y = norm(x + residual) over the rows of x [T][d], times weight [d] plus bias [d]
     (None: 1 and 0). Returns (y, s, mean, rstd): s [T][d] is the row that was normalised (x
-    itself without a residual; sum may be x or residual to write it there), mean and rstd
-    [T] fp32 are what norm_backward takes (given, or made with keep=True; mean is None for
-    an RMS norm)."""
+    itself without a residual, None if y took its place; sum may be x or residual to write
+    it there), mean and rstd [T] fp32 are what norm_backward takes (given, or made with
+    keep=True; mean is None for an RMS norm)."""
     lib = _lib or load_library()
     dev = x.device
     scope = _enter("x", dev, stream)
@@ -977,6 +977,8 @@ def norm_forward(dims: Dims, opts: NormOptions, x, weight=None, bias=None, resid
         elif sum is not None:
             raise ValueError("sum needs a residual")
         o = _as(y, "y", x, dev)
+        if y is not None and residual is None and T and o.data_ptr() == px:
+            s = None
         if mean is not None or (keep and opts.kind == "layer"):
             mean = _new(mean, "mean", torch.float32, (T,), dev)
         if rstd is not None or keep:
@@ -1188,7 +1190,7 @@ def grad_norm_workspace_bytes(grads) -> int:
     n = g.__dict__.get("_ws")
     if n is None:
         n = int(load_library().moe_grad_norm_workspace_bytes(g._ptr, len(g)))
-        g._ws = n
+        g.__dict__["_ws"] = n  # (two threads may both come here, with the same size)
     return n
 
 

@@ -295,3 +295,20 @@ def test_layer_norm_of_rows_far_from_zero(offset, d):
     assert bool(((rstd.double()[:, None] / rs - 1).abs() <= 60 * U).all())
     h = (z - mu) * rs
     assert bool(((y.double() - h).abs() <= 60 * U * (1 + h.abs())).all())
+
+
+def test_norm_over_its_own_input_returns_no_row():
+    """y over x without a residual: x no longer holds the row that was normalised, so none is handed out for the backward."""
+    dims, opts = moe.Dims(5, 64, 64, 8, 2, F32), moe.NormOptions("rms", 1e-6)
+    x = torch.randn((5, 64), device="cuda")
+    want, row, _, _ = moe.norm_forward(dims, opts, x, keep=True)
+    assert row is x
+    r = torch.randn_like(x)
+    both, s, _, _ = moe.norm_forward(dims, opts, x.clone(), residual=r, keep=True)
+    c, q = x.clone(), x.clone()
+    got, kept, _, _ = moe.norm_forward(dims, opts, c, y=c, keep=True)
+    assert got is c and kept is None and torch.equal(got, want)
+    got, kept, _, _ = moe.norm_forward(dims, opts, q, residual=r, y=q, keep=True)  # the sum is apart
+    assert got is q and torch.equal(kept, s) and torch.equal(got, both)
+    e = torch.zeros((0, 64), device="cuda")
+    assert moe.norm_forward(moe.Dims(0, 64, 64, 8, 2, F32), opts, e, y=e)[1] is e

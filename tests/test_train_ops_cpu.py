@@ -334,3 +334,18 @@ def test_checked_lists_are_fixed():
         g.tensors[0] = torch.zeros(7)
     assert moe.grad_norm_workspace_bytes(g) == moe.grad_norm_workspace_bytes(g) > 0 if os.path.exists(
         moe.library_path()) else True
+
+
+def test_workspace_size_of_a_list_asked_for_by_two_threads(monkeypatch):
+    """The second asks while the first one's query runs: both get the size."""
+    g, deep, sizes = moe.GradList([torch.ones(5)]), [], []
+
+    class Lib:
+        def moe_grad_norm_workspace_bytes(self, ptr, count):
+            if not deep:
+                deep.append(1)
+                sizes.append(moe.grad_norm_workspace_bytes(g))
+            return 512
+
+    monkeypatch.setattr(api, "load_library", Lib)
+    assert moe.grad_norm_workspace_bytes(g) == 512 and sizes == [512] and moe.grad_norm_workspace_bytes(g) == 512
