@@ -558,8 +558,8 @@ int moe_dropout_backward(const moe_dims_t* dims, double p, const uint64_t* rng, 
  *   MOE_NORM_LAYER:  rstd = (mean (s - mean s)^2 + eps)^(-1/2), y = (s - mean s) rstd weight + bias
  * Statistics in fp32, from the differences to the mean (taken as a number and the
  * rest that its rounding lost); a row whose sums pass fp32's range is summed at a
- * smaller scale. y is rounded once. Infinities and
- * NaN in a row go where the formula sends them.
+ * smaller scale. y is rounded once. Infinities and NaN in a row go where the
+ * formula sends them.
  *   x, residual (NULL = 0), sum (NULL: not written; may be x or residual), y [T][d]
  *   dtype; y may be x or residual (and is not sum);
  *   weight, bias [d] of opts->param_dtype, or NULL (1 and 0); bias NULL for RMS;
