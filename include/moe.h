@@ -583,7 +583,9 @@ int moe_norm_forward(const moe_dims_t* dims, const moe_norm_opts_t* opts, const 
 /* Its gradients. With h = (s - mean) rstd (RMS: s rstd) and g = dy weight:
  *   dx = rstd (g - mean g - h mean(g h)) + dx_in   (RMS: without mean g)
  *   dweight = sum_t dy h,  dbias = sum_t dy
- * dx is the gradient of s, hence of x and of residual alike.
+ * dx is the gradient of s, hence of x and of residual alike. The mean handed in is
+ * rounded: what that puts the h of a row off by, their mean, is taken back in rows whose
+ * mean lies more than 8 / rstd from zero; in others it is at most 2^-21.
  *   dy, s [T][d] (s: the row that was normalised: x, or the forward's sum);
  *   weight as in the forward; mean (layer norm), rstd [T] as the forward gave them;
  *   dx_in [T][d] (the gradient that reaches s by other ways) or NULL;

@@ -251,20 +251,31 @@ constexpr bool wide() {
   return !kWaveRow && NV * kVec<kDtype> > 8;
 }
 
+// A layer norm's row so far from zero that the rounding of its mean is looked after in
+// the gradients: within 8 spreads it puts h off by at most 2^-21. (A NaN row is NaN
+// either way.)
+constexpr float kFar = 8.0f;
+__device__ __forceinline__ bool far_row(float mean, float rstd) { return fabsf(mean * rstd) > kFar; }
+
 // Gradients: with h = (x - mean) rstd and g = dy w,
 //   dx = rstd (g - mean(g) - h mean(g h)) + dx_in      (mean(g): layer norm)
 //   dw = sum_t dy h,  db = sum_t dy.
 // A workgroup takes every parts-th row and keeps its columns' sums of dw and db
 // in registers; the parts are summed by norm_parts_kernel in their order. Both
 // row means come from one exchange between the waves.
+// Layer norm: the mean that is handed in is rounded, which puts every h of a row off
+// by one amount, its rounding times rstd (3 % of the spread for unit spread around
+// 10^6 in fp32). The mean of h is that amount, and in rows far from zero it is taken
+// back before h is used.
 // Differences to the mean are formed at half size and rstd at double, so that
 // neither passes fp32's range where h does not.
 template <int kDtype, bool kLayer, int NV, bool kWaveRow, bool kStream, bool kSums>
 __device__ __forceinline__ void grad_rows(const NormGradArgs& a, int block, int blocks) {
   constexpr int V = kVec<kDtype>;
-  __shared__ __attribute__((aligned(16))) float red[2][2][16];
+  __shared__ __attribute__((aligned(16))) float red[2][3][16];
   if (!kWaveRow) {
-    if (threadIdx.x < 64) red[threadIdx.x >> 5][(threadIdx.x >> 4) & 1][threadIdx.x & 15] = 0.0f;
+    // (rows to workgroups have 192 threads and more)
+    if (threadIdx.x < 96) (&red[0][0][0])[threadIdx.x] = 0.0f;
     __syncthreads();
   }
   const int nvec = a.d / V;
@@ -319,6 +330,28 @@ __device__ __forceinline__ void grad_rows(const NormGradArgs& a, int block, int 
     }
     // the next row is on its way while this one's sums are exchanged
     if (!kWide && t + step < a.T) fetch(t + step);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[j][i] = tid + j * lanes < nvec ? fmaf(h[j][i], 0.5f, m2) * r2 : 0.0f;
+    if (kLayer && far_row(m2, r2)) {
+      float c = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) c += h[j][i];
+      c = wave_sum(c);
+      if constexpr (!kWaveRow) {
+        if ((threadIdx.x & 63) == 0) red[half][2][threadIdx.x >> 6] = c;
+        __syncthreads();
+        c = sum16(red[half][2]);
+      }
+      c *= inv_d;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) h[j][i] = tid + j * lanes < nvec ? h[j][i] - c : 0.0f;
+    }
     float sg = 0.0f, sh = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -330,7 +363,6 @@ __device__ __forceinline__ void grad_rows(const NormGradArgs& a, int block, int 
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        h[j][i] = in ? fmaf(h[j][i], 0.5f, m2) * r2 : 0.0f;
         if constexpr (kSums) aw[j][i] = fmaf(g[j][i], h[j][i], aw[j][i]);
         if constexpr (kSums && kLayer) ab[j][i] += g[j][i];
         g[j][i] *= w[kWide ? 0 : j][i];
@@ -426,10 +458,65 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_grad_kernel(NormGr
   grad_rows<kDtype, kLayer, NV, kWaveRow, kStream, true>(a, blockIdx.x, gridDim.x);
 }
 
+// The means of the h of N rows of a layer norm, what the rounding of the rows' means put
+// them off by: all rows by one wave, the same values in every lane.
+template <int kDtype, int N>
+__device__ __forceinline__ void shifts_of(const NormGradArgs& a, const int64_t (&t)[N], float (&c)[N]) {
+  constexpr int V = kVec<kDtype>;
+  const int nvec = a.d / V;
+  float r2[N], m2[N];
+  double s[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    r2[n] = 2.0f * a.rstd[t[n]];
+    m2[n] = -0.5f * a.mean[t[n]];
+    s[n] = 0.0;
+  }
+#pragma unroll 2
+  for (int k = threadIdx.x & 63; k < nvec; k += 64) {
+    uint4 u[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) u[n] = reinterpret_cast<const uint4*>(a.x)[t[n] * nvec + k];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      float h[V], e = 0.0f;
+      unpack<kDtype>(u[n], h);
+#pragma unroll
+      for (int i = 0; i < V; ++i) e += fmaf(h[i], 0.5f, m2[n]) * r2[n];
+      s[n] += e;
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s[n] += __shfl_xor(s[n], o);
+    c[n] = static_cast<float>(s[n] / a.d);
+  }
+}
+
+// Those means of the rows that are far from zero; the others are not read, nor theirs
+// written.
+template <int kDtype>
+__global__ __launch_bounds__(256) void norm_shift_kernel(NormGradArgs a) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 4;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); t < a.T; t += step) {
+    if (!far_row(a.mean[t], a.rstd[t])) continue;
+    const int64_t row[1] = {t};
+    float c[1];
+    shifts_of<kDtype>(a, row, c);
+    if ((threadIdx.x & 63) == 0) a.shift[t] = c[0];
+  }
+}
+
 // dw and db of 64 bytes of columns over all rows, which need nothing but the rows'
 // statistics: four vectors to a row, a row to every four threads. A thread's sums
 // go into its total every 32 rows; the threads' totals are joined inside the rows
 // of 16 lanes, then between those, in a fixed order.
+// Layer norm: a wave that has met rows far from zero takes what their h are off by out
+// of dw again. For rows over 8192 columns a launch in front has formed it (2047 x 16384
+// in bf16 74 us without that launch, 76.5 with it, 106 where every row is far); shorter
+// ones are read again by the wave, which costs other batches nothing (333 x 1048 in fp32
+// 3.6 and 3.7 us, 700 x 7168 in bf16 18 and 18, but 43 and 131 where every row is far).
 template <int kDtype, bool kLayer>
 __device__ __forceinline__ void grad_columns(const NormGradArgs& a, int block, float* dw, float* db) {
   constexpr int V = kVec<kDtype>;
@@ -439,6 +526,7 @@ __device__ __forceinline__ void grad_columns(const NormGradArgs& a, int block, f
   float tw[V], tb[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) tw[i] = tb[i] = 0.0f;
+  float most = 0.0f;  // the farthest of this thread's rows, in spreads
   if (c < nvec) {
     for (int64_t t0 = threadIdx.x >> 2; t0 < a.T; t0 += 32 * groups) {
       const int64_t end = t0 + 32 * groups < a.T ? t0 + 32 * groups : a.T;
@@ -452,6 +540,7 @@ __device__ __forceinline__ void grad_columns(const NormGradArgs& a, int block, f
         unpack<kDtype>(reinterpret_cast<const uint4*>(a.dy)[at], g);
         unpack<kDtype>(reinterpret_cast<const uint4*>(a.x)[at], h);
         const float r2 = 2.0f * a.rstd[t], m2 = kLayer ? -0.5f * a.mean[t] : 0.0f;
+        if constexpr (kLayer) most = fmaxf(most, fabsf(m2 * r2));
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           aw[i] = fmaf(g[i], fmaf(h[i], 0.5f, m2) * r2, aw[i]);
@@ -462,6 +551,41 @@ __device__ __forceinline__ void grad_columns(const NormGradArgs& a, int block, f
       for (int i = 0; i < V; ++i) {
         tw[i] += aw[i];
         tb[i] += ab[i];
+      }
+    }
+  }
+  if (kLayer && dw && __ballot(most > kFar)) {
+    // 16 rows of the wave at a time, each taken in by its four lanes
+    const int mine = (threadIdx.x & 63) >> 2;
+    for (int64_t t0 = 16 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); t0 < a.T; t0 += groups) {
+      const int64_t t = t0 + mine;
+      const bool at = t < a.T && far_row(a.mean[t], a.rstd[t]);
+      float off = 0.0f;
+      if (a.shift) {
+        if (at) off = a.shift[t];
+      } else {
+        for (uint64_t left = __ballot(at); left;) {
+          // four rows at once (fewer: the last one again), so that their loads overlap
+          int k[4];
+          int64_t rows[4];
+          float m[4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            k[n] = left ? __builtin_ctzll(left) >> 2 : k[n > 0 ? n - 1 : 0];
+            rows[n] = t0 + k[n];
+            left &= ~(15ull << (4 * k[n]));
+          }
+          shifts_of<kDtype>(a, rows, m);
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            if (mine == k[n]) off = m[n];
+        }
+      }
+      if (off != 0.0f && c < nvec) {
+        float g[V];
+        unpack<kDtype>(reinterpret_cast<const uint4*>(a.dy)[t * nvec + c], g);
+#pragma unroll
+        for (int i = 0; i < V; ++i) tw[i] = fmaf(-off, g[i], tw[i]);
       }
     }
   }
@@ -646,10 +770,22 @@ int norm_grad_parts(int dtype, int64_t T, int64_t d) {
   return static_cast<int>(groups < most ? groups : most);
 }
 
+bool norm_grad_shifts(int dtype, bool layer, int64_t T, int64_t d) {
+  const Shape sh = row_shape(dtype, d, 1024);
+  return layer && !sh.wave && sh.nv * (dtype == 1 ? 8 : 4) > 8;
+}
+
 hipError_t launch_norm_grad(int dtype, bool layer, const NormGradArgs& a, int parts, float* dw, float* db,
                             hipStream_t s) {
   const Shape sh = row_shape(dtype, a.d, 1024);
   const bool sums = dw || db;
+  if (a.shift) {
+    const int64_t groups = (a.T + 3) / 4;
+    const dim3 grid(static_cast<unsigned>(groups < 2048 ? groups : 2048));
+    if (dtype == 1) hipLaunchKernelGGL(norm_shift_kernel<1>, grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(norm_shift_kernel<0>, grid, dim3(256), 0, s, a);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
   if (by_columns(dtype, sh, a.T, a.d)) {
     const int columns = sums ? (a.d / (dtype == 1 ? 8 : 4) + 3) / 4 : 0;
     const int64_t groups = sh.wave ? (a.T + 3) / 4 : a.T;

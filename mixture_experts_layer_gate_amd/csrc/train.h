@@ -38,11 +38,14 @@ struct NormGradArgs {
   void* dx;           // [T][d]
   float* part_w;      // [parts][d] or null (no weight gradient)
   float* part_b;      // [parts][d] or null
+  float* shift;       // [T] or null (norm_grad_shifts)
   int64_t T;
   int d;
   int w_bf16;
 };
 int norm_grad_parts(int dtype, int64_t T, int64_t d);
+// Whether dweight of these rows takes [T] of what each row's h is off by.
+bool norm_grad_shifts(int dtype, bool layer, int64_t T, int64_t d);
 hipError_t launch_norm_grad(int dtype, bool layer, const NormGradArgs& a, int parts, float* dw, float* db,
                             hipStream_t s);
 

@@ -1,0 +1,101 @@
+"""Layer norm's gradients of rows far from zero, against the float64 formula on the rows
+themselves (their own mean, not the fp32 number the forward hands on).
+
+u = 2^-24. With h = (s - mean) rstd and the mean handed on off by its rounding, every h of a
+row is off by the same c, which is what the mean of those h is. Per element of h, as the
+kernels form it: the difference and its product with rstd 2 u, rstd itself 60 u (the bound
+the forward is tested with), c's own sum 40 u of the mean of |h + c| (at most 1 + |c|), its
+subtraction u. |c| stays below 1/16 here, so (62 + 1) u (|h| + 1) + 43 u: 110 u (|h| + 1).
+Rows whose mean lies within 8 spreads of zero keep c: 2^-24 of 8, with rstd's rounding 9 u. Together less than 130 u (|h| + 1).
+"""
+import pytest
+import torch
+
+import mixture_experts_layer_gate_amd as moe
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BF = 2.0 ** -8
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _say(msg):
+    print(msg, flush=True)
+
+
+def _formula(dy, s, w, eps=1e-5):
+    z, up = s.double(), dy.double()
+    mu = z.mean(1, keepdim=True)
+    rs = 1 / torch.sqrt(((z - mu) ** 2).mean(1, keepdim=True) + eps)
+    h, g = (z - mu) * rs, up * w.double()
+    mg, mgh = g.mean(1, keepdim=True), (g * h).mean(1, keepdim=True)
+    return rs * (g - mg - h * mgh), h, g, rs
+
+
+def _check(dy, s, w, dx, dw, db, half):
+    T = s.shape[0]
+    rx, h, g, rs = _formula(dy, s, w)
+    up, e = dy.double(), h.abs() + 1
+    # dh's part of dx: 130 u e mean|g h| + |h| mean(|g| 130 u e); rstd 60 u; the operations as near zero
+    mg, mge = g.abs().mean(1, keepdim=True), (g.abs() * e).mean(1, keepdim=True)
+    bound = rs * U * (70 * g.abs() + 110 * mg + 260 * e * mge) + (half + 2 * U) * rx.abs()
+    bad = ((dx.double() - rx).abs() / bound).max()
+    _say(f"  dx at {float(bad):.3f} of its bound")
+    assert float(bad) <= 1
+    rows = -(-T // 256) + 64
+    bad = ((dw.double() - (up * h).sum(0)).abs() / ((rows + 134) * U * (up.abs() * e).sum(0))).max()
+    _say(f"  dweight at {float(bad):.3f} of its bound")
+    assert float(bad) <= 1
+    assert bool(((db.double() - up.sum(0)).abs() <= rows * U * up.abs().sum(0)).all())
+
+
+# one row, rows to waves and to workgroups, short batches and long ones, rows over 8192 columns
+SHAPES = [(1, 64), (333, 1048), (333, 256), (37, 7168), (600, 4096), (1030, 520), (1100, 1032), (1030, 4104), (1500, 7168),
+          (2500, 2048), (70, 8200), (300, 12296), (1100, 16384)]
+
+
+@pytest.mark.parametrize("T,d", SHAPES)
+@pytest.mark.parametrize("offset", [3.0, 1e2, 1e4, 1e6, -3e7])
+def test_gradients_of_rows_far_from_zero(offset, T, d):
+    gen = torch.Generator(device="cuda").manual_seed(T + d)
+    rn = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    x = (rn(T, d).double() * max(1.0, abs(offset) * 2.0 ** -20) + offset).float()
+    dy, w = rn(T, d), 1 + 0.2 * rn(d)
+    dims, opts = moe.Dims(T, d, 64, 1, 1, F32), moe.NormOptions("layer", 1e-5)
+    _say(f"{T} x {d} around {offset}")
+    _, s, mean, rstd = moe.norm_forward(dims, opts, x, w, keep=True)
+    dx, dw, db = moe.norm_backward(dims, opts, dy, s, w, rstd, mean=mean, want_dbias=True)
+    _check(dy, x, w, dx, dw, db, U)
+    # the weight's gradient alone, the bias' alone, and in place: the same bits
+    only = moe.norm_backward(dims, opts, dy, s, w, rstd, mean=mean)
+    assert torch.equal(only[0], dx) and torch.equal(only[1], dw)
+    only = moe.norm_backward(dims, opts, dy, s, w, rstd, mean=mean, want_dweight=False, want_dbias=True)
+    assert torch.equal(only[0], dx) and torch.equal(only[2], db)
+    for k in range(2):
+        t = [dy.clone(), s.clone()]
+        got = moe.norm_backward(dims, opts, t[0], t[1], w, rstd, mean=mean, dx=t[k], want_dbias=True)
+        assert torch.equal(got[0], dx) and torch.equal(got[1], dw) and torch.equal(got[2], db)
+
+
+@pytest.mark.parametrize("T,d", [(64, 256), (333, 1048), (700, 7168), (1500, 1032), (70, 8200), (520, 16384)])
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+def test_gradients_of_batches_with_some_far_rows(dt, T, d):
+    """Every third row far from zero (bf16: one value but for a few elements one step apart), rows of zeros and of one
+    value among ordinary ones; without a weight."""
+    gen = torch.Generator(device="cuda").manual_seed(T + d)
+    rn = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    x = rn(T, d) + 0.5 * rn(T, 1)
+    if dt is F32:
+        x[::3] += 1e5
+    else:
+        x[::3] = 1024.0
+        x[::3, ::97] = 1032.0
+    x[1] = 0.0
+    x[2 % T] = 3.0
+    x, dy = x.to(dt), rn(T, d).to(dt)
+    dims, opts = moe.Dims(T, d, 64, 1, 1, dt), moe.NormOptions("layer", 1e-5)
+    _say(f"{T} x {d} {dt}, some rows far from zero")
+    _, s, mean, rstd = moe.norm_forward(dims, opts, x, keep=True)
+    dx, dw, db = moe.norm_backward(dims, opts, dy, s, None, rstd, mean=mean, want_dbias=True)
+    _check(dy, x, torch.ones(d, device="cuda"), dx, dw, db, BF if dt is BF16 else U)
