@@ -212,7 +212,8 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a)
 #pragma unroll
         for (int i = 0; i < V; ++i) v[j][i] *= kShrink;
     }
-    float rstd, mul, mean_out = mean + rest;
+    // (a row with an infinity: the mean is that infinity, rest NaN)
+    float rstd, mul, mean_out = fabsf(mean) == INFINITY ? mean : mean + rest;
     if (!small) {
       rstd = mul = 1.0f / sqrtf(var + a.eps);
     } else {

@@ -1,13 +1,17 @@
 """Layer norm's gradients of rows far from zero, against the float64 formula on the rows
-themselves (their own mean, not the fp32 number the forward hands on).
+themselves (their own mean, not the fp32 number the forward hands on), and the mean of rows
+that hold an infinity.
 
 u = 2^-24. With h = (s - mean) rstd and the mean handed on off by its rounding, every h of a
 row is off by the same c, which is what the mean of those h is. Per element of h, as the
 kernels form it: the difference and its product with rstd 2 u, rstd itself 60 u (the bound
 the forward is tested with), c's own sum 40 u of the mean of |h + c| (at most 1 + |c|), its
 subtraction u. |c| stays below 1/16 here, so (62 + 1) u (|h| + 1) + 43 u: 110 u (|h| + 1).
-Rows whose mean lies within 8 spreads of zero keep c: 2^-24 of 8, with rstd's rounding 9 u. Together less than 130 u (|h| + 1).
+Rows whose mean lies within 8 spreads of zero keep c: 2^-24 of 8, with rstd's rounding 9 u.
+Together less than 130 u (|h| + 1).
 """
+import math
+
 import pytest
 import torch
 
@@ -18,6 +22,7 @@ pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
 BF = 2.0 ** -8
 BF16, F32 = torch.bfloat16, torch.float32
+INF, NAN = math.inf, math.nan
 
 
 def _say(msg):
@@ -99,3 +104,28 @@ def test_gradients_of_batches_with_some_far_rows(dt, T, d):
     _, s, mean, rstd = moe.norm_forward(dims, opts, x, keep=True)
     dx, dw, db = moe.norm_backward(dims, opts, dy, s, None, rstd, mean=mean, want_dbias=True)
     _check(dy, x, torch.ones(d, device="cuda"), dx, dw, db, BF if dt is BF16 else U)
+
+@pytest.mark.parametrize("d", [256, 1032, 7168, 8200])
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+def test_mean_of_rows_that_are_not_finite(dt, d):
+    """An infinity (or several of a sign) is the row's mean; both signs, or a NaN, make it NaN; other rows keep theirs."""
+    T = 7
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    x = torch.randn((T, d), generator=gen, device="cuda").to(dt)
+    dims, opts = moe.Dims(T, d, 64, 1, 1, dt), moe.NormOptions("layer", 1e-5)
+    _, _, m0, r0 = moe.norm_forward(dims, opts, x, keep=True)
+    z = x.clone()
+    z[1, d // 2] = INF
+    z[2, 0] = -INF
+    z[3, 3] = z[3, d - 1] = INF
+    z[4, 3], z[4, d - 1] = INF, -INF
+    z[5, 1] = NAN
+    y, _, mean, rstd = moe.norm_forward(dims, opts, z, keep=True)
+    assert mean[1:4].tolist() == [INF, -INF, INF] and bool(torch.isnan(mean[4:6]).all())
+    assert bool(torch.isnan(rstd[1:6]).all()) and bool(torch.isnan(y[1:6]).all())
+    assert torch.equal(mean[[0, 6]], m0[[0, 6]]) and torch.equal(rstd[[0, 6]], r0[[0, 6]])
+    # gradients: those rows, and no other
+    dy = torch.ones((T, d), device="cuda").to(dt)
+    a = moe.norm_backward(dims, opts, dy, x, None, r0, mean=m0)
+    b = moe.norm_backward(dims, opts, dy, z, None, rstd, mean=mean)
+    assert bool(torch.isnan(b[0][1:6]).all()) and torch.equal(a[0][[0, 6]], b[0][[0, 6]])
