@@ -1251,14 +1251,16 @@ def adam_step(opts: AdamOptions, state: AdamState, grads, lr=None, step=None, lr
 
 
 def adam_state_values(state: AdamState, m=None, r=None, dtype=torch.bfloat16, stream=None):
-    """What 8-bit states stand for, as lists of tensors of the states' sizes (given, or new
-    of dtype, fp32 or bf16): (first moments, roots of the second moments)."""
+    """What 8-bit states stand for, as lists of tensors of the states' sizes (given, all of
+    one type, fp32 or bf16, or new: of the given ones' type, else of dtype): (first moments,
+    roots of the second moments)."""
     lib = _lib or load_library()
     dev = state.device
     if state.bits != 8:
         raise ValueError("the states are not held in 8 bits")
-    if m is not None and len(m):
-        dtype = m[0].dtype
+    for ts in (r, m):
+        if ts is not None and len(ts):
+            dtype = ts[0].dtype
     if dtype not in MOE_DTYPE:
         raise ValueError("dtype must be torch.float32 or torch.bfloat16")
     scope = _enter("params[0]", dev, stream)

@@ -63,6 +63,18 @@ def test_state_values_of_long_lists_and_large_tensors(dt, sizes):
         assert bool((t[:pad] == 77).all()) and bool((t[-pad:] == 77).all())
 
 
+def test_state_values_into_roots_alone():
+    """The type is that of the tensors that are given, the roots' as well as the first moments'."""
+    st = _random_states([300, 5], 6)
+    m, r = moe.adam_state_values(st, dtype=F32)
+    for given in (dict(m=[torch.empty_like(t) for t in m]), dict(r=[torch.empty_like(t) for t in r])):
+        a, b = moe.adam_state_values(st, **given)
+        assert all(t.dtype is F32 for t in a + b)
+        assert all(torch.equal(x.nan_to_num(7.0), y.nan_to_num(7.0)) for x, y in zip(a + b, m + r))
+    with pytest.raises(ValueError, match="dtype"):
+        moe.adam_state_values(st, m=[t.to(BF16) for t in m], r=r)
+
+
 # -------------------------------------------------------------------- 2-norm ----
 @pytest.mark.parametrize("sizes", [[5] * 167 + [9000], [5] * 168 + [9000], [17] * 169, [17] * 170 + [1], [3] * 337, [3] * 340 + [8193],
                                    [34000003], [68000003, 1]], ids=lambda s: f"{len(s)}x{s[0]}")
