@@ -1118,6 +1118,11 @@ class AdamState(_Fixed):
             self.m_scale = self.v_scale = None
         if master is None:
             self.master = None
+        # what autograd's version counters are kept for: views share their base's (40 tensors of their own cost a step
+        # 3 us, 40 views of one buffer 0.7)
+        given = [t for t in (*params, *(master or ())) if t is not None]
+        own = {id(t): t for t in (t if t._base is None else t._base for t in given)}
+        self._versions = tuple(t.detach() for t in own.values())
         kind = (torch.uint8,) if self.bits == 8 else (torch.float32,)
         rows, spans = array.array("q"), []
 
@@ -1223,7 +1228,9 @@ def adam_step(opts: AdamOptions, state: AdamState, grads, lr=None, step=None, lr
     runs (a captured graph's owner updates it between replays). gscale: fp32 tensor [1] that
     the gradients are multiplied by (grad_norm's out[1:]); one that is not finite leaves
     everything as it was. rng: int64 tensor [2] on the GPU, seed and offset (another offset
-    for every step), needed for 8-bit states and stochastic rounding. Returns state."""
+    for every step), needed for 8-bit states and stochastic rounding. Returns state.
+    Autograd is told that the parameters and masters changed (not by a captured graph's
+    replays): differentiating a graph that saved one before the step is an error."""
     lib = _lib or load_library()
     g = _grad_list(grads)
     dev = state.device
@@ -1247,6 +1254,7 @@ def adam_step(opts: AdamOptions, state: AdamState, grads, lr=None, step=None, lr
         _leave(scope)
     if st:
         _check("moe_adam_step", st)
+    torch.autograd.graph.increment_version(state._versions)
     return state
 
 

@@ -1,5 +1,5 @@
 """Lists of tensors at the lengths and sizes where the launches are cut: the gradients'
-2-norm, the AdamW update and the values of 8-bit states.
+2-norm, the AdamW update and the values of 8-bit states; what autograd is told of a step.
 u = 2^-24, 2^-8 bf16's half step; bounds as derived beside the same checks of short lists.
 """
 import math
@@ -165,3 +165,47 @@ def test_block_training_step_with_8_bit_states():
                     int(t["opt_rng"][0]), int(t["opt_rng"][1]))
     assert all(bool((c != 0).any()) for ts in (st.m, st.v, st.m_scale, st.v_scale) for c in ts)
     assert all(not torch.equal(a, b.reshape(a.shape)) for a, b in zip(st.params, was["params"]))
+
+
+# ------------------------------------------------------------------ autograd ----
+@pytest.mark.parametrize("bits", [32, 8])
+def test_autograd_sees_a_step(bits):
+    """A graph that saved a weight (or its master) before a step refuses to be differentiated after it."""
+    w, u = torch.nn.Parameter(torch.randn(300, device="cuda")), torch.nn.Parameter(torch.randn(5, device="cuda").to(BF16))
+    st = moe.adam_state([w, u], bits, True)
+    rng = torch.tensor([1, 2], device="cuda")
+    grads = [torch.ones(300, device="cuda"), torch.ones(5, device="cuda")]
+    for t in (w, u):
+        loss = (t * t).sum()
+        before = t._version
+        moe.adam_step(moe.AdamOptions(), st, grads, lr=1e-3, step=1, rng=rng)
+        assert t._version > before
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    master = st.master[1]._version
+    moe.adam_step(moe.AdamOptions(), st, moe.GradList(grads), lr=1e-3, step=2, rng=rng)
+    assert st.master[1]._version > master
+    (w * w).sum().backward()  # a graph made after the step is as before
+    assert torch.equal(w.grad, 2 * w)
+    # a refused step changes nothing
+    before = w._version
+    with pytest.raises(moe.MoeError):
+        moe.adam_step(moe.AdamOptions(), st, grads, lr=1e-3, step=0, rng=rng)
+    assert w._version == before
+    # tensors made for inference have no counter
+    with torch.inference_mode():
+        q = moe.adam_state([torch.ones(9, device="cuda")], bits)
+        moe.adam_step(moe.AdamOptions(), q, [torch.ones(9, device="cuda")], lr=1e-3, step=1, rng=rng)
+    moe.adam_step(moe.AdamOptions(), q, [torch.ones(9, device="cuda")], lr=1e-3, step=2, rng=rng)
+
+
+def test_autograd_sees_a_step_of_views():
+    """Parameters that are views of one buffer, and of a view's view: the buffer and each of them."""
+    flat, other = torch.randn(600, device="cuda"), torch.randn((4, 9), device="cuda")
+    ps = [flat[:300], flat[300:600].view(30, 10), other[1], other.view(-1)[18:27], torch.nn.Parameter(flat.new_zeros(7))]
+    st, x = moe.adam_state(ps), torch.ones(300, device="cuda", requires_grad=True)
+    losses = [(x[: p.numel()] * p.reshape(-1)).sum() for p in ps] + [(x[0] * flat).sum(), (x[0] * other).sum()]
+    moe.adam_step(moe.AdamOptions(), st, [torch.ones(p.numel(), device="cuda") for p in ps], lr=1e-3, step=1)
+    for loss in losses:
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
