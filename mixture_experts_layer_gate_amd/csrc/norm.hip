@@ -764,6 +764,7 @@ hipError_t launch_norm(int dtype, bool layer, const NormArgs& a, hipStream_t s) 
 
 int norm_grad_parts(int dtype, int64_t T, int64_t d) {
   const Shape sh = row_shape(dtype, d, 1024);
+  if (by_columns(dtype, sh, T, d)) return 0;
   // One workgroup to a compute unit, two of few threads: every part is written and
   // read once more. Measured with one, two, three: 4096 x 7168 42, 48, 52 us; 8192
   // x 4096 48, 51, 57; 16384 x 2048 66, 50, 53; 8192 x 512 12.6, 12.4, 14.0.
@@ -776,9 +777,9 @@ bool norm_grad_shifts(int dtype, bool layer, int64_t T, int64_t d) {
   return layer && !sh.wave && sh.nv * (dtype == 1 ? 8 : 4) > 8;
 }
 
-hipError_t launch_norm_grad(int dtype, bool layer, const NormGradArgs& a, int parts, float* dw, float* db,
-                            hipStream_t s) {
+hipError_t launch_norm_grad(int dtype, bool layer, const NormGradArgs& a, float* dw, float* db, hipStream_t s) {
   const Shape sh = row_shape(dtype, a.d, 1024);
+  const int parts = norm_grad_parts(dtype, a.T, a.d);
   const bool sums = dw || db;
   if (a.shift) {
     const int64_t groups = (a.T + 3) / 4;
@@ -787,7 +788,7 @@ hipError_t launch_norm_grad(int dtype, bool layer, const NormGradArgs& a, int pa
     else hipLaunchKernelGGL(norm_shift_kernel<0>, grid, dim3(256), 0, s, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  if (by_columns(dtype, sh, a.T, a.d)) {
+  if (parts == 0) {
     const int columns = sums ? (a.d / (dtype == 1 ? 8 : 4) + 3) / 4 : 0;
     const int64_t groups = sh.wave ? (a.T + 3) / 4 : a.T;
     const int rows = static_cast<int>(groups < 1024 ? groups : 1024);

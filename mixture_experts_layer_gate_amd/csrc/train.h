@@ -43,11 +43,11 @@ struct NormGradArgs {
   int d;
   int w_bf16;
 };
+// Parts that dweight and dbias are summed from, 0 where they are summed beside the rows.
 int norm_grad_parts(int dtype, int64_t T, int64_t d);
 // Whether dweight of these rows takes [T] of what each row's h is off by.
 bool norm_grad_shifts(int dtype, bool layer, int64_t T, int64_t d);
-hipError_t launch_norm_grad(int dtype, bool layer, const NormGradArgs& a, int parts, float* dw, float* db,
-                            hipStream_t s);
+hipError_t launch_norm_grad(int dtype, bool layer, const NormGradArgs& a, float* dw, float* db, hipStream_t s);
 
 // ---------------- lists of tensors ----------------
 // A launch takes its tensors by value (kernel arguments hold 4 KB), so no list

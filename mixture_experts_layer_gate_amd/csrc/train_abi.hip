@@ -50,16 +50,19 @@ int check_norm(const moe_dims_t* dm, const moe_norm_opts_t* op) {
 
 bool ok16_or_null(const void* p) { return !p || ok16(p); }
 
-// Parts of the weight gradients: dweight's, then dbias's; or in their place (sums by
-// columns) a number to each row.
-size_t norm_ws(const moe_dims_t* dm, bool layer, int parts, void* ws, float** w, float** b, float** shift) {
+// Parts of the weight gradients: dweight's, then dbias's (layer norm). Where columns
+// are summed beside the rows there are none, and a row's width of each is asked for all
+// the same (so that every call has its check); rows over 8192 columns keep a number to
+// each row there (norm_grad_shifts).
+size_t norm_ws(const moe_dims_t* dm, bool layer, void* ws, float** w, float** b, float** shift) {
+  const int parts = norm_grad_parts(dm->dtype, dm->T, dm->d);
   Carver c(ws);
-  float* pw = c.take<float>(sizeof(float) * parts * dm->d);
-  float* pb = c.take<float>(sizeof(float) * parts * dm->d);
+  float* first = c.take<float>(sizeof(float) * (parts ? parts : 1) * dm->d);
+  float* second = layer || !parts ? c.take<float>(sizeof(float) * (parts ? parts : 1) * dm->d) : nullptr;
   const bool shifts = norm_grad_shifts(dm->dtype, layer, dm->T, dm->d);
-  if (w) *w = pw;
-  if (b) *b = pb;
-  if (shift) *shift = shifts ? pw : nullptr;
+  if (w) *w = first;
+  if (b) *b = second;
+  if (shift) *shift = shifts ? first : nullptr;
   const size_t rows = shifts ? align_up(sizeof(float) * static_cast<size_t>(dm->T)) : 0;
   return rows > c.off ? rows : c.off;
 }
@@ -192,9 +195,7 @@ int moe_norm_forward(const moe_dims_t* dm, const moe_norm_opts_t* op, const void
 
 size_t moe_norm_backward_workspace_bytes(const moe_dims_t* dm, const moe_norm_opts_t* op) {
   if (check_norm(dm, op) != MOE_OK) return 0;
-  const size_t n = norm_ws(dm, op->kind == MOE_NORM_LAYER, norm_grad_parts(dm->dtype, dm->T, dm->d), nullptr, nullptr,
-                           nullptr, nullptr);
-  return n ? n : kAlign;
+  return norm_ws(dm, op->kind == MOE_NORM_LAYER, nullptr, nullptr, nullptr, nullptr);
 }
 
 int moe_norm_backward(const moe_dims_t* dm, const moe_norm_opts_t* op, const void* dy, const void* xs,
@@ -213,16 +214,15 @@ int moe_norm_backward(const moe_dims_t* dm, const moe_norm_opts_t* op, const voi
   }
   if (!ok16(dy) || !ok16(xs) || !ok16(dx) || !ok16_or_null(dx_in) || !ok4(rstd) || (layer && !ok4(mean)))
     return MOE_ERR_INVALID;
-  const int parts = norm_grad_parts(dm->dtype, dm->T, dm->d);
   float *pw = nullptr, *pb = nullptr, *shift = nullptr;
   if (dweight || dbias) {
-    if (int st = check_ws(ws, ws_bytes, norm_ws(dm, layer, parts, nullptr, nullptr, nullptr, nullptr))) return st;
-    norm_ws(dm, layer, parts, ws, &pw, &pb, &shift);
+    if (int st = check_ws(ws, ws_bytes, norm_ws(dm, layer, nullptr, nullptr, nullptr, nullptr))) return st;
+    norm_ws(dm, layer, ws, &pw, &pb, &shift);
   }
   StageScope sc(MOE_STAGE_NORM_BWD, s);
   const NormGradArgs a = {dy, xs, weight, mean, rstd, dx_in, dx, dweight ? pw : nullptr, dbias ? pb : nullptr,
                           dweight ? shift : nullptr, dm->T, static_cast<int>(dm->d), op->param_dtype == MOE_DTYPE_BF16};
-  return hip_status(launch_norm_grad(dm->dtype, layer, a, parts, dweight, dbias, s));
+  return hip_status(launch_norm_grad(dm->dtype, layer, a, dweight, dbias, s));
 }
 
 size_t moe_grad_norm_workspace_bytes(const moe_grad_t* grads, int32_t count) {
