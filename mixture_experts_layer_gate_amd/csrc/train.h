@@ -50,11 +50,12 @@ bool norm_grad_shifts(int dtype, bool layer, int64_t T, int64_t d);
 hipError_t launch_norm_grad(int dtype, bool layer, const NormGradArgs& a, float* dw, float* db, hipStream_t s);
 
 // ---------------- lists of tensors ----------------
-// A launch takes its tensors by value (kernel arguments hold 4 KB), so no list
+// A launch takes its tensors by value, as many as kernel arguments hold, so no list
 // is copied to the device and a captured graph holds its own.
-constexpr int kAdamTensors = 40;
-constexpr int kGradTensors = 168;
-constexpr int kStateTensors = 56;
+constexpr size_t kArgBytes = 4096;
+constexpr int kAdamTensors = 49;
+constexpr int kGradTensors = 169;
+constexpr int kStateTensors = 63;
 // Elements of a workgroup's turn, rounds of 2048 of its 256 threads: one round for
 // the update with 32-bit states, and where more leave compute units without a
 // workgroup (measured on 1.1 M fp32 weights in 40 tensors: 8.4 and 10.4 us).
@@ -118,7 +119,10 @@ struct AdamTable {
   const uint64_t* rng;      // device {seed, offset} or null
   AdamScalars k;
 };
-static_assert(sizeof(AdamTable) <= 4096 && sizeof(GradTable) <= 4096, "kernel arguments");
+// (beside the gradients' table the kernel takes a pointer)
+static_assert(sizeof(AdamTable) <= kArgBytes && sizeof(GradTable) + 8 <= kArgBytes, "kernel arguments");
+static_assert(sizeof(AdamTable) + sizeof(AdamEntry) > kArgBytes && sizeof(GradTable) + 8 + sizeof(GradEntry) > kArgBytes,
+              "as many as they hold");
 
 // The scalars that depend on lr and step; the kernels form them alike from lr_step.
 __host__ __device__ inline double pow_step(double b, double step) {
@@ -159,7 +163,7 @@ struct StateTable {
   uint32_t chunks;
   int chunk;
 };
-static_assert(sizeof(StateTable) <= 4096, "kernel arguments");
+static_assert(sizeof(StateTable) <= kArgBytes && sizeof(StateTable) + sizeof(StateEntry) > kArgBytes, "kernel arguments");
 hipError_t launch_state_values(int out_dtype, const StateTable& t, bool stream, hipStream_t s);
 
 }  // namespace moe
