@@ -565,7 +565,8 @@ int moe_dropout_backward(const moe_dims_t* dims, double p, const uint64_t* rng, 
  *   weight, bias [d] of opts->param_dtype, or NULL (1 and 0); bias NULL for RMS;
  *   mean, rstd [T] fp32 outputs, or NULL (mean NULL for RMS).
  * d % 8 == 0 and d <= 16384 (MOE_ERR_UNSUPPORTED otherwise); eps in [2^-100, 2^100],
- * else MOE_ERR_INVALID. Only T, d and dtype of dims are used. `opts` is a HOST
+ * else MOE_ERR_INVALID. dims are the layer's and must be valid as a whole, T * k and
+ * T * E below 2^31 among it; the norm itself uses T, d and dtype. `opts` is a HOST
  * pointer. Tensors of x's shape, weight and bias 16-byte aligned. */
 typedef enum {
   MOE_NORM_RMS = 0,

@@ -1,5 +1,5 @@
 """The workspace of the norm's gradients: what is asked for is what the form of the call
-writes, and a workspace of exactly that size is enough."""
+writes, and a workspace of exactly that size is enough; the dims that the norm takes."""
 import ctypes
 import os
 
@@ -41,6 +41,24 @@ def test_less_is_refused():
             need = lib.moe_norm_backward_workspace_bytes(dims, opts)
             mean, db = (A, A) if kind == "layer" else (None, None)
             assert lib.moe_norm_backward(dims, opts, A, A, A, mean, A, None, A, A, db, A, need - 1, None) == 3
+
+
+@built
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="host-only validation test")
+def test_dims_are_valid_as_a_whole():
+    """The layer's dims, experts and width of them included, also for the norm alone."""
+    A, lib, opts = 0x10000, moe.load_library(), ctypes.byref(api._NormOpts(0, 0, 1e-6))
+
+    def status(T, f, E, k):
+        dims = ctypes.byref(api._Dims(T, 64, f, E, k, 1))
+        fwd = lib.moe_norm_forward(dims, opts, A, None, A, None, None, None, None, None, None)
+        bwd = lib.moe_norm_backward(dims, opts, A, A, A, None, A, None, None, A, None, A, 1 << 50, None)
+        return fwd, bwd, lib.moe_norm_backward_workspace_bytes(dims, opts) > 0
+    for bad in ((2 ** 23 + 7, 64, 256, 8), (2 ** 28, 64, 8, 8), (64, 0, 8, 2), (64, 64, 8, 0), (64, 64, 2, 3), (64, 64, 1025, 2)):
+        assert status(*bad) == (1, 1, False), bad
+    # (these are refused for the output that is missing, behind the dims)
+    for good in ((2 ** 23 + 7, 64, 1, 1), (2 ** 23 - 1, 64, 256, 8), (64, 1, 8, 8)):
+        assert status(*good) == (1, 1, True), good
 
 
 @pytest.mark.gpu
