@@ -686,7 +686,8 @@ int moe_adam_step(const moe_adam_opts_t* opts, const moe_adam_tensor_t* tensors,
 /* What 8-bit states stand for: m_out[i] [n] = m and r_out[i] [n] = sqrt(v) of
  * tensors[i] (HOST arrays of DEVICE pointers), of out_dtype (bf16 holds every
  * code's value from 2^-126 on; smaller ones are rounded). param, master are not
- * looked at. An output that appears twice: MOE_ERR_INVALID. */
+ * looked at. An output that appears twice: MOE_ERR_INVALID; none may overlap the
+ * states. */
 int moe_adam_state_values(const moe_adam_tensor_t* tensors, int32_t count, void* const* m_out, void* const* r_out,
                           int out_dtype, void* stream);
 

@@ -4,6 +4,8 @@ Each function takes torch tensors that already live on the GPU, checks their
 dtype and shape, and passes ``data_ptr()`` values, the workspace and the
 current HIP stream to the library. No step of the layer runs here. The library
 is loaded on first use; if it is missing, calls raise -- there is no fallback.
+Autograd does not see what the calls write into tensors they are given, save the
+parameters of adam_step, whose version counters follow a step.
 """
 from __future__ import annotations
 

@@ -118,9 +118,9 @@ constexpr float kShrink = 0x1p-80f;
 // vectors to a thread. The variance is that of the differences to the mean, taken
 // from the registers, and the same exchange gives what the mean's own rounding lost,
 // so rows whose mean is many times their spread keep their precision (16384 x 7168
-// in bf16 with residual 147.5 us, without it 145.8). A row whose sums pass fp32's
-// range is scaled by 2^-80 and summed again, so the statistics are right for every
-// finite row.
+// in bf16 with a residual, written to the same outputs again: 147.5 us, and 145.8
+// without that). A row whose sums pass fp32's range is scaled by 2^-80 and summed
+// again, so the statistics are right for every finite row.
 template <int kDtype, bool kLayer, int NV, bool kWaveRow, bool kStream>
 __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a) {
   constexpr int V = kVec<kDtype>;
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(kWaveRow ? 256 : 1024) void norm_kernel(NormArgs a)
       reinterpret_cast<uint4*>(a.y)[t * nvec + c] = pack<kDtype>(v[j]);
     }
     // red is written again; alternating parts of it without this barrier let the waves
-    // drift apart (16384 x 7168, layer norm: 145 and 165 us; RMS norm equal)
+    // drift apart (16384 x 7168, layer norm with a residual: 145 and 165 us; RMS norm equal)
     if (!kWaveRow) __syncthreads();
   }
 }
@@ -748,7 +748,11 @@ bool by_columns(int dtype, const Shape& sh, int64_t T, int64_t d) {
   if (!sh.wave && sh.nv * (dtype == 1 ? 8 : 4) > 8) return true;
   return T <= 1024 && T * d * (dtype == 1 ? 2 : 4) <= int64_t(10) << 20;
 }
-constexpr int64_t kResident = 2048;  // threads that a compute unit holds
+// Threads that a compute unit holds at up to 64 registers. Layer norms of one bf16
+// vector to a thread have 66, of two 96, of four fp32 vectors 116: of these it holds
+// fewer (from 7169 columns on one workgroup, not two), and what the grid has beyond
+// them starts after the first ones have ended.
+constexpr int64_t kResident = 2048;
 constexpr int64_t kStreamBytes = int64_t(128) << 20;
 
 }  // namespace
