@@ -513,11 +513,12 @@ __global__ __launch_bounds__(256) void norm_shift_kernel(NormGradArgs a) {
 // statistics: four vectors to a row, a row to every four threads. A thread's sums
 // go into its total every 32 rows; the threads' totals are joined inside the rows
 // of 16 lanes, then between those, in a fixed order.
-// Layer norm: a wave that has met rows far from zero takes what their h are off by out
-// of dw again. For rows over 8192 columns a launch in front has formed it (2047 x 16384
-// in bf16 74 us without that launch, 76.5 with it, 106 where every row is far); shorter
-// ones are read again by the wave, which costs other batches nothing (333 x 1048 in fp32
-// 3.6 and 3.7 us, 700 x 7168 in bf16 18 and 18, but 43 and 131 where every row is far).
+// Layer norm: rows far from zero are left out of dw, and a wave that has met some adds
+// them once it knows what their h are off by. For rows over 8192 columns a launch in front has formed it (2047 x 16384
+// in bf16 74 us without that launch, 76 with it, 123 where every row is far); shorter
+// ones are read again by the wave, which costs other batches next to nothing (333 x 1048
+// in fp32 3.6 and 3.8 us, 700 x 7168 in bf16 18.1 and 18.4, but 42 and 132 where every
+// row is far).
 template <int kDtype, bool kLayer>
 __device__ __forceinline__ void grad_columns(const NormGradArgs& a, int block, float* dw, float* db) {
   constexpr int V = kVec<kDtype>;
@@ -541,10 +542,11 @@ __device__ __forceinline__ void grad_columns(const NormGradArgs& a, int block, f
         unpack<kDtype>(reinterpret_cast<const uint4*>(a.dy)[at], g);
         unpack<kDtype>(reinterpret_cast<const uint4*>(a.x)[at], h);
         const float r2 = 2.0f * a.rstd[t], m2 = kLayer ? -0.5f * a.mean[t] : 0.0f;
+        const bool later = kLayer && far_row(m2, r2);
         if constexpr (kLayer) most = fmaxf(most, fabsf(m2 * r2));
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          aw[i] = fmaf(g[i], fmaf(h[i], 0.5f, m2) * r2, aw[i]);
+          aw[i] = fmaf(later ? 0.0f : g[i], fmaf(h[i], 0.5f, m2) * r2, aw[i]);
           if constexpr (kLayer) ab[i] += g[i];
         }
       }
@@ -582,11 +584,13 @@ __device__ __forceinline__ void grad_columns(const NormGradArgs& a, int block, f
             if (mine == k[n]) off = m[n];
         }
       }
-      if (off != 0.0f && c < nvec) {
-        float g[V];
+      if (at && c < nvec) {
+        float g[V], h[V];
         unpack<kDtype>(reinterpret_cast<const uint4*>(a.dy)[t * nvec + c], g);
+        unpack<kDtype>(reinterpret_cast<const uint4*>(a.x)[t * nvec + c], h);
+        const float r2 = 2.0f * a.rstd[t], m2 = -0.5f * a.mean[t];
 #pragma unroll
-        for (int i = 0; i < V; ++i) tw[i] = fmaf(-off, g[i], tw[i]);
+        for (int i = 0; i < V; ++i) tw[i] = fmaf(g[i], fmaf(h[i], 0.5f, m2) * r2 - off, tw[i]);
       }
     }
   }

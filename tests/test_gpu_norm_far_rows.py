@@ -129,3 +129,30 @@ def test_mean_of_rows_that_are_not_finite(dt, d):
     a = moe.norm_backward(dims, opts, dy, x, None, r0, mean=m0)
     b = moe.norm_backward(dims, opts, dy, z, None, rstd, mean=mean)
     assert bool(torch.isnan(b[0][1:6]).all()) and torch.equal(a[0][[0, 6]], b[0][[0, 6]])
+
+
+@pytest.mark.parametrize("T,d", [(40, 256), (333, 1048), (700, 7168), (1100, 256), (1500, 1032), (300, 12296)])
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+def test_infinite_gradients_of_far_rows(dt, T, d):
+    """An infinite dy times h is an infinity of dweight's column, in rows far from zero as in others, and reaches no other
+    column of it and no other row of dx."""
+    gen = torch.Generator(device="cuda").manual_seed(T + d)
+    x = torch.randn((T, d), generator=gen, device="cuda")
+    x[::2] += 300.0
+    x, dy = x.to(dt), torch.randn((T, d), generator=gen, device="cuda").to(dt)
+    dims, opts = moe.Dims(T, d, 64, 1, 1, dt), moe.NormOptions("layer", 1e-5)
+    _, s, mean, rstd = moe.norm_forward(dims, opts, x, keep=True)
+    dx0, dw0, db0 = moe.norm_backward(dims, opts, dy, s, None, rstd, mean=mean, want_dbias=True)
+    # (where h is off zero by more than the row's rounding)
+    h = (x.double() - x.double().mean(1, keepdim=True)) * rstd.double()[:, None]
+    z, want = dy.clone(), dw0.clone()
+    for t, c in ((4, 7), (5, 20), (T - 2, d - 3), (T // 4 * 2, d // 2)):
+        c = c + int(h[t, c:c + 2].abs().argmax())
+        assert float(h[t, c].abs()) > 1e-3
+        z[t, c] = INF
+        want[c] = INF * float(h[t, c])
+    dx, dw, db = moe.norm_backward(dims, opts, z, s, None, rstd, mean=mean, want_dbias=True)
+    assert torch.equal(dw, want)
+    assert torch.equal(db, torch.where(torch.isinf(want), torch.full_like(db0, INF), db0))
+    rows = torch.isfinite(z).all(1)
+    assert torch.equal(dx[rows], dx0[rows]) and not bool(torch.isfinite(dx[~rows]).any())
